@@ -67,20 +67,23 @@ typedef enum {
     PKV_ERR_DEVICE_METADATA = 5  /* reported by pkv_check_device_error */
 } pkv_status;
 
-typedef enum { PKV_BF16 = 0, PKV_FP16 = 1, PKV_FP32 = 2 } pkv_dtype;
+/* PKV_E4M3: 8-bit floats with 4 exponent and 3 mantissa bits, no infinity, largest value 448. */
+typedef enum { PKV_BF16 = 0, PKV_FP16 = 1, PKV_FP32 = 2, PKV_E4M3 = 3 } pkv_dtype;
 
 /* Codes stored in the device error word (first error wins). */
 enum {
     PKV_DEVERR_NONE = 0,
-    PKV_DEVERR_SLOT = 1,        /* append / compact_tokens: slot >= num_blocks * block_size */
-    PKV_DEVERR_COPY_ID = 2,     /* copy_blocks / swap_blocks: src or dst outside its pool */
+    PKV_DEVERR_SLOT = 1,        /* append / append_rope / compact_tokens: slot >= num_blocks * block_size */
+    PKV_DEVERR_COPY_ID = 2,     /* copy_blocks / copy_blocks_fp8 / swap_blocks: src or dst outside its pool */
     PKV_DEVERR_CONTEXT_LEN = 3, /* decode: context_lens[s] < 0, above the table's capacity, or above max_context_len */
     PKV_DEVERR_BLOCK_ID = 4,    /* decode: block_tables entry outside the pool */
     PKV_DEVERR_TIMEOUT = 5,     /* a bounded in-CTA wait ran out */
     PKV_DEVERR_PREFIX_LEN = 6,  /* grouped decode: prefix_lens[s] < 0, above context_lens[s] or
                                    max_prefix_len, or not a multiple of block_size */
-    PKV_DEVERR_GROUP = 7        /* grouped decode: group_starts out of order or range, or a sequence
+    PKV_DEVERR_GROUP = 7,       /* grouped decode: group_starts out of order or range, or a sequence
                                    with a shared prefix in no group or beyond max_group_size members */
+    PKV_DEVERR_POSITION = 8,    /* append_rope: positions[t] outside [0, max_position) */
+    PKV_DEVERR_SCALE = 9        /* append_rope_fp8: rows join a block whose scale is not a positive finite number */
 };
 
 /* Shape of one layer's paged cache (host struct, read during the call). */
@@ -89,8 +92,21 @@ typedef struct {
     int32_t num_kv_heads;
     int32_t block_size;  /* tokens per block: 16 or 32 */
     int32_t head_dim;    /* 128 */
-    int32_t dtype;       /* pkv_dtype: PKV_BF16 or PKV_FP16 */
+    int32_t dtype;       /* pkv_dtype: PKV_BF16 or PKV_FP16; PKV_E4M3 for the calls that end in _fp8 */
 } pkv_cache_desc;
+
+/* The new rows of paged_kv_append_rope and how they are rotated (host struct, read during the call). */
+typedef struct {
+    int32_t num_q_heads;  /* heads of q and q_out; 0: no queries */
+    int32_t dtype;        /* of q, k, v, q_out and the norm weights: PKV_BF16 or PKV_FP16 */
+    int64_t q_stride;     /* elements from one token's row to the next, a multiple of 8 */
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t max_position; /* rows of cos_sin */
+    int32_t rot_dim;      /* dims of each head that are rotated, its first ones: 0 (none) or a multiple of 16, <= head_dim */
+    int32_t interleaved;  /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
+    float norm_eps;       /* added to the mean square; >= 0 */
+} pkv_rope_desc;
 
 /* Human-readable name of a status. Never NULL. */
 const char* pkv_status_string(pkv_status status);
@@ -113,6 +129,77 @@ int pkv_version(void);
  */
 pkv_status paged_kv_append(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens,
                            void* k_cache, void* v_cache, const pkv_cache_desc* cache, void* stream);
+
+/*
+ * Block write with the position rotation, and the norms of query and key
+ * heads, on the way: one pass over a step's new rows.  For every token t with
+ * slot_mapping[t] >= 0 and every query and key head x (head_dim values):
+ *     x' = x / sqrt(mean(x^2) + norm_eps) * w   (w = q_norm or k_norm; x' = x where that is NULL)
+ *     y  = x' with its first rot_dim dims turned by the token's position p = positions[t]:
+ *          (y_a, y_b) = (x'_a c_i - x'_b s_i, x'_b c_i + x'_a s_i) for pair i = (a, b) of pkv_rope_desc,
+ *          c_i = cos_sin[p][i], s_i = cos_sin[p][rot_dim / 2 + i], i < rot_dim / 2
+ * y goes to q_out (queries) or to the token's slot of k_cache (keys, as
+ * paged_kv_append writes them); v goes to v_cache unchanged, bit for bit.
+ * Everything between the loads and the one rounding of y is in 32 bits.
+ *
+ * q, k, v:       row t at base + t * stride elements, [num_heads][head_dim]
+ *                contiguous inside the row: slices of one fused projection
+ *                are passed as they are.  16-byte aligned; the cache's dtype.
+ *                q and q_out may be NULL when num_q_heads is 0.
+ * positions:     [num_tokens] int64 device memory; NULL when rot_dim is 0.
+ * cos_sin:       [max_position][rot_dim] fp32 device memory, 16-byte
+ *                aligned; NULL when rot_dim is 0.
+ * q_norm, k_norm: [head_dim] device memory, 16-byte aligned, or NULL.
+ * slot_mapping:  as for paged_kv_append.
+ * q_out:         [num_tokens][num_q_heads][head_dim], 16-byte aligned; may be
+ *                q itself when q_stride is num_q_heads * head_dim, and must
+ *                not overlap it otherwise, nor the k and v rows.
+ * A token with a negative slot is padding: nothing of it is read, and its row
+ * of q_out keeps its contents.  A slot past the pool is recorded as
+ * PKV_DEVERR_SLOT and a position outside [0, max_position) as
+ * PKV_DEVERR_POSITION; such a token's K and V are not written and its q_out
+ * row is zeros.  Two tokens with the same slot race (last writer undefined).
+ * num_tokens == 0 is a no-op.  Supported: head_dim 128, any block size, bf16
+ * or fp16.
+ */
+pkv_status paged_kv_append_rope(const void* q, const void* k, const void* v, const int64_t* positions,
+                                const float* cos_sin, const void* q_norm, const void* k_norm,
+                                const int64_t* slot_mapping, int64_t num_tokens, void* q_out, void* k_cache,
+                                void* v_cache, const pkv_cache_desc* cache, const pkv_rope_desc* rope, void* stream);
+
+/*
+ * paged_kv_append_rope into an 8-bit pool.  k_cache and v_cache hold e4m3
+ * values, and each (block, KV head) of either has one fp32 scale: a stored
+ * value b stands for b * scale.
+ * k_scales, v_scales: [num_blocks][num_kv_heads] fp32 device memory.
+ * For each block and KV head that rows are written to, for K and for V, with
+ * a = the largest finite magnitude of those rows (K: after the rotation):
+ *   - the block's first row is among them: the block starts afresh, and its
+ *     scale becomes P(a), the smallest power of two >= a / 448, 2^-64 at least;
+ *   - otherwise the rows join those that the block holds: the scale is kept
+ *     while a <= 448 * scale; else it becomes P(a), and the rows below the
+ *     first written one are moved to it, each value rounded once to the
+ *     nearest e4m3 value of b * (old / new).  A scale that is not a positive
+ *     finite number is recorded as PKV_DEVERR_SCALE and replaced by P(a),
+ *     with the held bytes left as they are.
+ * The new rows are stored as the nearest e4m3 values of y / scale, ties to
+ * even; infinities and NaN are stored as NaN.  A scale that is a power of two
+ * loses nothing when it is applied and keeps the relative precision of e4m3
+ * (half a step, 2^-4) down to 2^-15 of the largest magnitude it can hold; it
+ * also makes a move to a larger scale exact but for the smallest values.
+ * Rows above the first written one that the call does not write keep their
+ * bytes: a block is filled from its first row up.
+ * Tokens of one block stand together in slot_mapping, in any order, with
+ * padding between them or not; where they do not, that block's contents and
+ * scales are unspecified.
+ * cache->dtype is PKV_E4M3 and block_size 16 or 32; the rest as for
+ * paged_kv_append_rope.
+ */
+pkv_status paged_kv_append_rope_fp8(const void* q, const void* k, const void* v, const int64_t* positions,
+                                    const float* cos_sin, const void* q_norm, const void* k_norm,
+                                    const int64_t* slot_mapping, int64_t num_tokens, void* q_out, void* k_cache,
+                                    void* v_cache, float* k_scales, float* v_scales, const pkv_cache_desc* cache,
+                                    const pkv_rope_desc* rope, void* stream);
 
 /*
  * Bytes of workspace paged_attention_decode needs for these sizes (0 when
@@ -194,6 +281,27 @@ pkv_status paged_attention_decode(const void* q, const void* k_cache, const void
                                   int32_t max_context_len, float scale, void* out, int32_t out_dtype,
                                   const pkv_cache_desc* cache, int32_t partition_size, void* workspace,
                                   size_t workspace_bytes, void* stream);
+
+/*
+ * paged_attention_decode over an 8-bit pool (paged_kv_append_rope_fp8): with
+ * ks = k_scales[b][kvh], vs = v_scales[b][kvh] of the block b that holds t,
+ *     out[s][h][:] = sum_{t<L} softmax_t(scale * ks * q[s][h] . K[t]) vs V[t]
+ * q_dtype:   PKV_BF16 or PKV_FP16, the type of q.
+ * k_scales, v_scales: [num_blocks][num_kv_heads] fp32 device memory; any
+ *            finite values, powers of two or not.  Those of blocks outside
+ *            the sequences' contexts are never read.
+ * cache->dtype is PKV_E4M3.  The other arguments, the workspace
+ * (paged_attention_workspace_bytes), the split of the work
+ * (paged_attention_plan), the errors and the limits are those of
+ * paged_attention_decode.  The values enter the products exactly (as 16-bit
+ * floats), the scales as 32-bit factors of the sums.
+ */
+pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
+                                      const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t num_seqs,
+                                      int32_t num_q_heads, int32_t max_context_len, float scale, void* out,
+                                      int32_t out_dtype, const pkv_cache_desc* cache, int32_t partition_size,
+                                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * A decode step in one launch: the block write of one new token per
@@ -345,6 +453,18 @@ pkv_status paged_attention_decode_static(const void* q, const void* k_cache, con
 pkv_status copy_blocks(void* const* k_caches, void* const* v_caches, int32_t num_layers,
                        const int64_t* src_dst_pairs, int32_t num_pairs, const pkv_cache_desc* cache,
                        void* stream);
+
+/*
+ * copy_blocks for 8-bit pools: the copy takes a block's scales along, for
+ * each pair i and each layer l also
+ *     k_scales[l][dst][:] = k_scales[l][src][:]   (and the V scales)
+ * k_scales, v_scales: HOST arrays of num_layers device pointers to
+ *                  [num_blocks][num_kv_heads] fp32, 4-byte aligned.
+ * cache->dtype is PKV_E4M3; the rest as for copy_blocks.
+ */
+pkv_status copy_blocks_fp8(void* const* k_caches, void* const* v_caches, float* const* k_scales,
+                           float* const* v_scales, int32_t num_layers, const int64_t* src_dst_pairs,
+                           int32_t num_pairs, const pkv_cache_desc* cache, void* stream);
 
 /*
  * Swap-out / swap-in of whole blocks between two pools ("vllm", "como

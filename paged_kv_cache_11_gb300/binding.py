@@ -17,11 +17,12 @@ import torch
 LIB_PATH = Path(__file__).resolve().parent / "_lib" / "libpagedkv.so"
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE, PKV_ERR_CUDA, PKV_ERR_DEVICE_METADATA = range(6)
-PKV_BF16, PKV_FP16, PKV_FP32 = 0, 1, 2
+PKV_BF16, PKV_FP16, PKV_FP32, PKV_E4M3 = 0, 1, 2, 3
 DEVERR_NAMES = {0: "none", 1: "slot", 2: "copy_id", 3: "context_len", 4: "block_id", 5: "timeout",
-                6: "prefix_len", 7: "group"}
+                6: "prefix_len", 7: "group", 8: "position", 9: "scale"}
 
-_DTYPE_CODE = {torch.bfloat16: PKV_BF16, torch.float16: PKV_FP16, torch.float32: PKV_FP32}
+_DTYPE_CODE = {torch.bfloat16: PKV_BF16, torch.float16: PKV_FP16, torch.float32: PKV_FP32,
+               torch.float8_e4m3fn: PKV_E4M3}
 
 
 class CacheDesc(ctypes.Structure):
@@ -31,6 +32,20 @@ class CacheDesc(ctypes.Structure):
         ("block_size", ctypes.c_int32),
         ("head_dim", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
+    ]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_q_heads", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("max_position", ctypes.c_int64),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("norm_eps", ctypes.c_float),
     ]
 
 
@@ -62,6 +77,17 @@ def _lib() -> ctypes.CDLL:
     lib.pkv_launch_count.restype = ctypes.c_uint64
     lib.paged_kv_append.argtypes = [vp, vp, vp, i64, vp, vp, desc_p, vp]
     lib.paged_kv_append.restype = ctypes.c_int
+    rope_p = ctypes.POINTER(RopeDesc)
+    lib.paged_kv_append_rope.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, desc_p, rope_p, vp]
+    lib.paged_kv_append_rope.restype = ctypes.c_int
+    lib.paged_kv_append_rope_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, desc_p, rope_p,
+                                             vp]
+    lib.paged_kv_append_rope_fp8.restype = ctypes.c_int
+    lib.paged_attention_decode_fp8.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, ctypes.c_float,
+                                               vp, i32, desc_p, i32, vp, sz, vp]
+    lib.paged_attention_decode_fp8.restype = ctypes.c_int
+    lib.copy_blocks_fp8.argtypes = [ctypes.POINTER(vp)] * 4 + [i32, vp, i32, desc_p, vp]
+    lib.copy_blocks_fp8.restype = ctypes.c_int
     lib.paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     lib.paged_attention_workspace_bytes.restype = sz
     lib.paged_attention_plan.argtypes = [i32, i32, i32, i32, i32, i32]
@@ -155,6 +181,111 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor
                                   _ptr(v_cache), ctypes.byref(desc), _stream(stream)), "paged_kv_append")
 
 
+def _on_device(device: torch.device, stream):
+    """Context in which a call's allocations and launches belong to ``device`` and to ``stream`` (None: the device's
+    current stream): tensors made inside are the stream's, so none is handed out again while the call still runs."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    _require(stream.device == device, "stream belongs to another device")
+    return torch.cuda.stream(stream)
+
+
+def _same_device(*tensors) -> torch.device:
+    """The CUDA device that all the given tensors (None: left out) are on."""
+    dev = tensors[0].device
+    for t in tensors:
+        _require(t is None or (t.is_cuda and t.device == dev), "tensors must be on one CUDA device")
+    return dev
+
+
+def _append_rope(fp8: bool, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scales, v_scales, q_norm,
+                 k_norm, norm_eps, interleaved, q_out, stream):
+    dev = _same_device(k_cache, v_cache, k, v, slot_mapping, q, positions, cos_sin, k_scales, v_scales, q_norm, k_norm,
+                       q_out)
+    for t in (slot_mapping, positions, cos_sin, k_cache, v_cache, k_scales, v_scales, q_norm, k_norm, q_out):
+        _require(t is None or t.is_contiguous(), "all tensors but q, k and v must be contiguous")
+    desc = cache_desc(k_cache)
+    d = desc.head_dim
+    n = slot_mapping.numel()
+    _require(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype, "K and V caches differ")
+    _require(slot_mapping.dtype == torch.int64 and slot_mapping.dim() == 1, "slot_mapping must be int64 [num_tokens]")
+    for t in (k, v):
+        _require(t.dtype == k.dtype and t.shape == (n, desc.num_kv_heads, d),
+                 "k and v are [num_tokens, num_kv_heads, head_dim], of one dtype")
+    for t in (k, v) if q is None else (q, k, v):
+        _require(t.dim() == 3 and t.stride(2) == 1 and (t.stride(1) == d or t.shape[1] == 1),
+                 "a token's heads must be contiguous in q, k and v")
+    if q is None:
+        _require(q_out is None and q_norm is None, "q_out and q_norm belong to q")
+    else:
+        _require(q.dtype == k.dtype and q.shape[0] == n and q.shape[2] == d,
+                 "q is [num_tokens, num_q_heads, head_dim], of k's dtype")
+    _require((positions is None) == (cos_sin is None), "positions and cos_sin belong together")
+    rot = 0
+    if cos_sin is not None:
+        _require(positions.dtype == torch.int64 and positions.shape == (n,), "positions must be int64 [num_tokens]")
+        _require(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2, "cos_sin must be fp32 [max_position, rot_dim]")
+        rot = cos_sin.shape[1]
+        _require(rot > 0, "cos_sin without columns: pass None for no rotation")
+    for w in (q_norm, k_norm):
+        _require(w is None or (w.dtype == k.dtype and w.shape == (d,)), "norm weights are [head_dim], of k's dtype")
+    if fp8:
+        for s in (k_scales, v_scales):
+            _require(s.dtype == torch.float32 and s.shape == k_cache.shape[:2],
+                     "scales must be fp32 [num_blocks, num_kv_heads]")
+    if q_out is not None:
+        _require(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out is as q")
+    rope = RopeDesc(0 if q is None else q.shape[1], _DTYPE_CODE.get(k.dtype, -1),
+                    0 if q is None or n < 2 else q.stride(0), k.stride(0) if n > 1 else 0, v.stride(0) if n > 1 else 0,
+                    0 if cos_sin is None else cos_sin.shape[0], rot, int(interleaved), float(norm_eps))
+    if q is not None and n < 2:
+        rope.q_stride = q.shape[1] * d
+    name = "paged_kv_append_rope_fp8" if fp8 else "paged_kv_append_rope"
+    with _on_device(dev, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        pools = (_ptr(k_cache), _ptr(v_cache)) + ((_ptr(k_scales), _ptr(v_scales)) if fp8 else ())
+        _check(getattr(_lib(), name)(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(cos_sin), _ptr(q_norm), _ptr(k_norm), _ptr(slot_mapping),
+            n, _ptr(q_out), *pools, ctypes.byref(desc), ctypes.byref(rope), _stream(None)), name)
+    return q_out
+
+
+def paged_kv_append_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
+                         cos_sin: torch.Tensor | None, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                         v_cache: torch.Tensor, q_norm: torch.Tensor | None = None,
+                         k_norm: torch.Tensor | None = None, norm_eps: float = 1e-6, interleaved: bool = False,
+                         q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Block write with the rotation by position (and the RMS norm of each query and key head, where weights are
+    given) on the way; returns ``q_out``, the rotated queries.
+
+    q [num_tokens, num_q_heads, 128] (or None), k and v [num_tokens, num_kv_heads, 128] may be slices of one fused
+    projection: only a token's heads must be contiguous.  ``cos_sin`` is fp32 [max_position, rot_dim], the cosines of
+    a position's rot_dim / 2 angles before their sines (None: no rotation).  Rows of padding tokens (negative slots)
+    are left as they were; ``q_out`` may be ``q`` where that is contiguous.
+    """
+    return _append_rope(False, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, None, None, q_norm, k_norm,
+                        norm_eps, interleaved, q_out, stream)
+
+
+def paged_kv_append_rope_fp8(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
+                             cos_sin: torch.Tensor | None, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                             v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                             q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None,
+                             norm_eps: float = 1e-6, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor | None:
+    """paged_kv_append_rope into float8_e4m3fn caches with one fp32 scale per (block, KV head), ``k_scales`` and
+    ``v_scales`` [num_blocks, num_kv_heads]: a stored value stands for value * scale.
+
+    A block starts afresh when its first row is written, and its scales follow the rows it takes on (the header has
+    the rule); a block's tokens stand together in ``slot_mapping``.
+    """
+    return _append_rope(True, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scales, v_scales, q_norm,
+                        k_norm, norm_eps, interleaved, q_out, stream)
+
+
 def paged_attention_workspace_bytes(num_seqs: int, num_q_heads: int, head_dim: int, max_context_len: int,
                                     partition_size: int = 0) -> int:
     return int(_lib().paged_attention_workspace_bytes(num_seqs, num_q_heads, head_dim, max_context_len,
@@ -211,6 +342,47 @@ def paged_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks, _ptr(context_lens), num_seqs, hq,
         int(max_context_len), float(scale), _ptr(out), _DTYPE_CODE.get(out.dtype, -1), ctypes.byref(desc),
         int(partition_size), _ptr(workspace), ws_bytes, _stream(stream)), "paged_attention_decode")
+    return out
+
+
+def paged_attention_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
+                               v_scales: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                               scale: float, out: torch.Tensor | None = None, max_context_len: int | None = None,
+                               partition_size: int = 0, workspace: torch.Tensor | None = None,
+                               out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """paged_attention_decode over float8_e4m3fn caches with one fp32 scale per (block, KV head)
+    (paged_kv_append_rope_fp8); q is bf16 or fp16."""
+    dev = _same_device(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, out, workspace)
+    for t in (q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, out, workspace):
+        _require(t is None or t.is_contiguous(), "tensors must be contiguous")
+    _require(block_tables.dtype == torch.int32 and context_lens.dtype == torch.int32,
+             "block_tables and context_lens must be int32")
+    desc = cache_desc(k_cache)
+    _require(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype, "K and V caches differ")
+    _require(q.dim() == 3 and q.shape[2] == desc.head_dim, "q is [num_seqs, num_q_heads, head_dim]")
+    num_seqs, hq, d = q.shape
+    _require(block_tables.dim() == 2 and block_tables.shape[0] == num_seqs and context_lens.shape == (num_seqs,),
+             "one row of block_tables and one context length per sequence")
+    for s in (k_scales, v_scales):
+        _require(s.dtype == torch.float32 and s.shape == k_cache.shape[:2],
+                 "scales must be fp32 [num_blocks, num_kv_heads]")
+    _require(out is None or out.shape == q.shape, "out is [num_seqs, num_q_heads, head_dim]")
+    max_blocks = block_tables.shape[1]
+    if max_context_len is None:
+        max_context_len = max_blocks * desc.block_size
+    with _on_device(dev, stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+        if workspace is None:
+            need = paged_attention_workspace_bytes(num_seqs, hq, d, max_context_len, partition_size)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(_lib().paged_attention_decode_fp8(
+            _ptr(q), _DTYPE_CODE.get(q.dtype, -1), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+            _ptr(block_tables), max_blocks, _ptr(context_lens), num_seqs, hq, int(max_context_len), float(scale),
+            _ptr(out), _DTYPE_CODE.get(out.dtype, -1), ctypes.byref(desc), int(partition_size), _ptr(workspace),
+            ws_bytes, _stream(None)), "paged_attention_decode_fp8")
     return out
 
 
@@ -365,6 +537,28 @@ def copy_blocks(k_caches: torch.Tensor | Sequence[torch.Tensor], v_caches: torch
 
 def _ptr_array(ts):
     return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+
+
+def copy_blocks_fp8(k_caches: torch.Tensor | Sequence[torch.Tensor], v_caches: torch.Tensor | Sequence[torch.Tensor],
+                    k_scales: torch.Tensor | Sequence[torch.Tensor], v_scales: torch.Tensor | Sequence[torch.Tensor],
+                    src_dst_pairs: torch.Tensor, stream=None) -> None:
+    """copy_blocks for float8_e4m3fn caches: block dst := block src in every layer, K and V, with its scales."""
+    k, v, ks, vs = ([t] if isinstance(t, torch.Tensor) else list(t) for t in (k_caches, v_caches, k_scales, v_scales))
+    _require(len(k) == len(v) == len(ks) == len(vs) > 0, "need one K and one V cache per layer, and their scales")
+    dev = _same_device(src_dst_pairs, *k, *v, *ks, *vs)
+    for t in (*k, *v, *ks, *vs, src_dst_pairs):
+        _require(t.is_contiguous(), "tensors must be contiguous")
+    for t in (*k, *v):
+        _require(t.shape == k[0].shape and t.dtype == k[0].dtype, "the caches differ")
+    for t in (*ks, *vs):
+        _require(t.dtype == torch.float32 and t.shape == k[0].shape[:2],
+                 "scales must be fp32 [num_blocks, num_kv_heads]")
+    _require(src_dst_pairs.dtype == torch.int64 and src_dst_pairs.numel() % 2 == 0, "src_dst_pairs must be int64 [n, 2]")
+    desc = cache_desc(k[0])
+    with _on_device(dev, stream):
+        _check(_lib().copy_blocks_fp8(_ptr_array(k), _ptr_array(v), _ptr_array(ks), _ptr_array(vs), len(k),
+                                      _ptr(src_dst_pairs), src_dst_pairs.numel() // 2, ctypes.byref(desc),
+                                      _stream(None)), "copy_blocks_fp8")
 
 
 def swap_blocks(src_k: torch.Tensor | Sequence[torch.Tensor], src_v: torch.Tensor | Sequence[torch.Tensor],

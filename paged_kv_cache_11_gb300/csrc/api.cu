@@ -147,6 +147,21 @@ static pkv_status check_cache(const pkv_cache_desc* c) {
     return PKV_OK;
 }
 
+// The same for the calls on 8-bit pools.
+static pkv_status check_cache_fp8(const pkv_cache_desc* c) {
+    if (!c) return PKV_ERR_INVALID_ARG;
+    if (c->num_blocks < 1 || c->num_kv_heads < 1 || c->block_size < 1 || c->head_dim < 1) return PKV_ERR_INVALID_ARG;
+    if (c->dtype != PKV_E4M3) return PKV_ERR_UNSUPPORTED;
+    if (c->head_dim % 16 != 0 || (c->block_size != 16 && c->block_size != 32)) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+// Every element of a pool has a 64-bit byte offset.
+static bool pool_fits(const pkv_cache_desc* c) {
+    const unsigned __int128 block = (unsigned __int128)c->num_kv_heads * c->block_size * c->head_dim;
+    return block * (uint64_t)c->num_blocks < ((unsigned __int128)1 << 61);
+}
+
 // Streaming multiprocessors of the current device (cached per device).
 static int sm_count() {
     static int cache[kMaxDevices] = {};
@@ -243,7 +258,7 @@ const char* pkv_status_string(pkv_status s) {
     return "unknown status";
 }
 
-int pkv_version(void) { return 100; }
+int pkv_version(void) { return 110; }
 
 uint64_t pkv_launch_count(void) { return g_launches.load(); }
 
@@ -478,6 +493,229 @@ static pkv_status decode_impl(const void* q, const void* k_new, const void* v_ne
     g_launches += launches;
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
+
+// Checks and sizes shared by paged_kv_append_rope and its 8-bit form.
+static pkv_status append_rope_impl(const void* q, const void* k, const void* v, const int64_t* positions,
+                                   const float* cos_sin, const void* q_norm, const void* k_norm,
+                                   const int64_t* slot_mapping, int64_t num_tokens, void* q_out, void* k_cache,
+                                   void* v_cache, float* k_scales, float* v_scales, const pkv_cache_desc* cache,
+                                   const pkv_rope_desc* rope, bool fp8, void* stream) {
+    pkv_status st = fp8 ? check_cache_fp8(cache) : check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (!rope || num_tokens < 0 || rope->num_q_heads < 0 || rope->rot_dim < 0 || rope->q_stride < 0 ||
+        rope->k_stride < 0 || rope->v_stride < 0 || !(rope->norm_eps >= 0.f) || rope->norm_eps == INFINITY)
+        return PKV_ERR_INVALID_ARG;
+    if (cache->head_dim != kHeadDim) return PKV_ERR_UNSUPPORTED;
+    if (rope->dtype != PKV_BF16 && rope->dtype != PKV_FP16) return PKV_ERR_UNSUPPORTED;
+    if (!fp8 && rope->dtype != cache->dtype) return PKV_ERR_INVALID_ARG;
+    if (rope->rot_dim > kHeadDim || rope->rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if (rope->q_stride % 8 != 0 || rope->k_stride % 8 != 0 || rope->v_stride % 8 != 0) return PKV_ERR_INVALID_ARG;
+    if (cache->num_kv_heads > 65535 || rope->num_q_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if (!pool_fits(cache)) return PKV_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PKV_OK;
+    const int64_t rows = (int64_t)rope->num_q_heads + 2 * (int64_t)cache->num_kv_heads;
+    if (num_tokens > ((int64_t)INT_MAX * 16) / rows) return PKV_ERR_INVALID_ARG;
+    // bytes that each input spans; they must be addressable
+    const int64_t qh = (int64_t)rope->num_q_heads * kHeadDim, kh = (int64_t)cache->num_kv_heads * kHeadDim;
+    const int64_t most = INT64_MAX / 4 / num_tokens;
+    if (rope->q_stride > most || rope->k_stride > most || rope->v_stride > most) return PKV_ERR_INVALID_ARG;
+    if (!k || !v || !slot_mapping || !k_cache || !v_cache || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 8))
+        return PKV_ERR_INVALID_ARG;
+    if (qh > 0 && (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16))) return PKV_ERR_INVALID_ARG;
+    if (rope->rot_dim > 0 && (!positions || !cos_sin || !aligned(positions, 8) || !aligned(cos_sin, 16) ||
+                              rope->max_position < 1 || rope->max_position > INT64_MAX / 4 / kHeadDim))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(q_norm, 16) || !aligned(k_norm, 16)) return PKV_ERR_INVALID_ARG;
+    if (fp8 && (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4))) return PKV_ERR_INVALID_ARG;
+    if (qh > 0) {
+        // q_out may be q itself, row by row, and overlaps no other row
+        const auto overlap = [&](const void* in, int64_t stride, int64_t width) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(q_out);
+            return a < b + 2 * (uintptr_t)(num_tokens * qh) &&
+                   b < a + 2 * (uintptr_t)((num_tokens - 1) * stride + width);
+        };
+        if (overlap(q, rope->q_stride, qh) && !(q == q_out && rope->q_stride == qh)) return PKV_ERR_INVALID_ARG;
+        if (overlap(k, rope->k_stride, kh) || overlap(v, rope->v_stride, kh)) return PKV_ERR_INVALID_ARG;
+    }
+    int* err = error_word();
+    if (!err) return PKV_ERR_CUDA;
+    RopeParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.err = err;
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.q_norm = static_cast<const uint16_t*>(q_norm);
+    p.k_norm = static_cast<const uint16_t*>(k_norm);
+    p.slot_mapping = slot_mapping;
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.num_tokens = num_tokens;
+    p.num_slots = cache->num_blocks * cache->block_size;
+    p.max_position = rope->max_position;
+    p.q_stride = rope->q_stride;
+    p.k_stride = rope->k_stride;
+    p.v_stride = rope->v_stride;
+    p.num_q_heads = rope->num_q_heads;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.block_size = cache->block_size;
+    p.rot_dim = rope->rot_dim;
+    p.interleaved = rope->interleaved != 0;
+    p.norm_eps = rope->norm_eps;
+    int launches = 0;
+    const cudaError_t e = launch_rope_append(p, rope->dtype, fp8, static_cast<cudaStream_t>(stream), &launches);
+    g_launches += launches;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+extern "C" {
+
+pkv_status paged_kv_append_rope(const void* q, const void* k, const void* v, const int64_t* positions,
+                                const float* cos_sin, const void* q_norm, const void* k_norm,
+                                const int64_t* slot_mapping, int64_t num_tokens, void* q_out, void* k_cache,
+                                void* v_cache, const pkv_cache_desc* cache, const pkv_rope_desc* rope, void* stream) {
+    return append_rope_impl(q, k, v, positions, cos_sin, q_norm, k_norm, slot_mapping, num_tokens, q_out, k_cache,
+                            v_cache, nullptr, nullptr, cache, rope, false, stream);
+}
+
+pkv_status paged_kv_append_rope_fp8(const void* q, const void* k, const void* v, const int64_t* positions,
+                                    const float* cos_sin, const void* q_norm, const void* k_norm,
+                                    const int64_t* slot_mapping, int64_t num_tokens, void* q_out, void* k_cache,
+                                    void* v_cache, float* k_scales, float* v_scales, const pkv_cache_desc* cache,
+                                    const pkv_rope_desc* rope, void* stream) {
+    return append_rope_impl(q, k, v, positions, cos_sin, q_norm, k_norm, slot_mapping, num_tokens, q_out, k_cache,
+                            v_cache, k_scales, v_scales, cache, rope, true, stream);
+}
+
+pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
+                                      const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t num_seqs,
+                                      int32_t num_q_heads, int32_t max_context_len, float scale, void* out,
+                                      int32_t out_dtype, const pkv_cache_desc* cache, int32_t partition_size,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+    const pkv_status st = check_cache_fp8(cache);
+    if (st != PKV_OK) return st;
+    if (cache->head_dim != kHeadDim) return PKV_ERR_UNSUPPORTED;
+    if (q_dtype != PKV_BF16 && q_dtype != PKV_FP16) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || num_seqs > 65535 || num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0)
+        return PKV_ERR_INVALID_ARG;
+    if (out_dtype != PKV_FP32 && out_dtype != PKV_BF16 && out_dtype != PKV_FP16) return PKV_ERR_INVALID_ARG;
+    if (max_blocks_per_seq < 1 || max_context_len < 0 ||
+        (int64_t)max_blocks_per_seq * cache->block_size > INT_MAX ||
+        max_context_len > (int64_t)max_blocks_per_seq * cache->block_size)
+        return PKV_ERR_INVALID_ARG;
+    if (partition_size < 0 || partition_size % cache->block_size != 0) return PKV_ERR_INVALID_ARG;
+    if (!(scale == scale) || scale == INFINITY || scale == -INFINITY) return PKV_ERR_INVALID_ARG;
+    if (!pool_fits(cache)) return PKV_ERR_INVALID_ARG;
+    const int group = num_q_heads / cache->num_kv_heads;
+    const int head_tiles = (group + decode_head_tile(group) - 1) / decode_head_tile(group);
+    if ((int64_t)cache->num_kv_heads * head_tiles > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!q || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !context_lens || !out)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
+        return PKV_ERR_INVALID_ARG;
+    const Plan pl = make_plan(num_seqs, cache->num_kv_heads, head_tiles, max_context_len, partition_size);
+    const bool split = pl.kind != PKV_PLAN_SINGLE;
+    const size_t need =
+        paged_attention_workspace_bytes(num_seqs, num_q_heads, kHeadDim, max_context_len, partition_size);
+    if (split && !(workspace && workspace_bytes >= need && aligned(workspace, 256))) return PKV_ERR_WORKSPACE;
+    int* err = error_word();
+    if (!err) return PKV_ERR_CUDA;
+    DecodeFp8Params fp;
+    std::memset(&fp, 0, sizeof(fp));
+    fp.k8 = static_cast<const uint8_t*>(k_cache);
+    fp.v8 = static_cast<const uint8_t*>(v_cache);
+    fp.k_scales = k_scales;
+    fp.v_scales = v_scales;
+    fp.q_bf16 = q_dtype == PKV_BF16;
+    DecodeParams& p = fp.d;
+    p.q = q;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.out = out;
+    if (split) {
+        const WorkspaceLayout w =
+            workspace_layout(num_seqs, num_q_heads, kHeadDim, (int64_t)num_seqs * num_q_heads * pl.max_parts);
+        char* base = static_cast<char*>(workspace);
+        p.merge_ctr = reinterpret_cast<unsigned long long*>(base + w.ctr_off);
+        p.part_o = reinterpret_cast<float*>(base + w.o_off);
+        p.part_lse = reinterpret_cast<float*>(base + w.lse_off);
+        p.fuse_merge = pl.max_parts <= kFuseMergeMaxParts ? 1 : 0;
+        p.epoch = next_epoch();
+    }
+    p.err = err;
+    p.num_blocks = cache->num_blocks;
+    p.num_seqs = num_seqs;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.len_limit = max_context_len;  // already <= max_blocks_per_seq * block_size
+    p.partition_size = pl.partition;
+    p.max_parts = pl.max_parts;
+    p.group = group;
+    p.head_tiles = head_tiles;
+    p.out_dtype = out_dtype;
+    p.split = split ? 1 : 0;
+    p.block_size = cache->block_size;
+    p.parts_in_x = pl.max_parts > 65535 ? 1 : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    int launches = 0;
+    const cudaError_t e = launch_decode_fp8(fp, static_cast<cudaStream_t>(stream), &launches);
+    g_launches += launches;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status copy_blocks_fp8(void* const* k_caches, void* const* v_caches, float* const* k_scales,
+                           float* const* v_scales, int32_t num_layers, const int64_t* src_dst_pairs,
+                           int32_t num_pairs, const pkv_cache_desc* cache, void* stream) {
+    const pkv_status st = check_cache_fp8(cache);
+    if (st != PKV_OK) return st;
+    if (num_layers < 0 || num_pairs < 0 || !pool_fits(cache)) return PKV_ERR_INVALID_ARG;
+    if (num_layers == 0 || num_pairs == 0) return PKV_OK;
+    if (!k_caches || !v_caches || !k_scales || !v_scales || !src_dst_pairs || !aligned(src_dst_pairs, 8))
+        return PKV_ERR_INVALID_ARG;
+    for (int l = 0; l < num_layers; ++l)
+        if (!k_caches[l] || !v_caches[l] || !k_scales[l] || !v_scales[l] || !aligned(k_caches[l], 16) ||
+            !aligned(v_caches[l], 16) || !aligned(k_scales[l], 4) || !aligned(v_scales[l], 4))
+            return PKV_ERR_INVALID_ARG;
+    // head_dim is a multiple of 16: whole 16-byte vectors
+    const int64_t block_vecs = (int64_t)cache->num_kv_heads * cache->block_size * cache->head_dim / 16;
+    if ((block_vecs + 4095) / 4096 > 65535) return PKV_ERR_UNSUPPORTED;
+    int* err = error_word();
+    if (!err) return PKV_ERR_CUDA;
+    int launches = 0;
+    cudaError_t e = cudaSuccess;
+    for (int l0 = 0; l0 < num_layers && e == cudaSuccess; l0 += kCopyFp8MaxLayers) {
+        CopyFp8Params p;
+        std::memset(&p, 0, sizeof(p));
+        p.err = err;
+        p.num_layers = num_layers - l0 < kCopyFp8MaxLayers ? num_layers - l0 : kCopyFp8MaxLayers;
+        for (int l = 0; l < p.num_layers; ++l) {
+            p.k[l] = static_cast<uint4*>(k_caches[l0 + l]);
+            p.v[l] = static_cast<uint4*>(v_caches[l0 + l]);
+            p.ks[l] = k_scales[l0 + l];
+            p.vs[l] = v_scales[l0 + l];
+        }
+        p.pairs = src_dst_pairs;
+        p.num_blocks = cache->num_blocks;
+        p.block_vecs = block_vecs;
+        p.num_kv_heads = cache->num_kv_heads;
+        p.num_pairs = num_pairs;
+        e = launch_copy_blocks_fp8(p, static_cast<cudaStream_t>(stream), &launches);
+    }
+    g_launches += launches;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // extern "C"
 
 // Shared by copy_blocks and swap_blocks: whole blocks from a source pool to
 // a destination pool (which are the same pool for copy_blocks).

@@ -78,6 +78,43 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const CopyPar
     }
 }
 
+// copy_blocks of 8-bit pools: grid as copy_blocks_kernel; the first chunk of
+// each block also moves the block's row of scales.
+__global__ void __launch_bounds__(kCopyThreads) copy_blocks_fp8_kernel(const __grid_constant__ CopyFp8Params p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int pair = blockIdx.x;
+    const int layer = blockIdx.z >> 1;
+    const int64_t src = __ldg(p.pairs + 2 * (int64_t)pair), dst = __ldg(p.pairs + 2 * (int64_t)pair + 1);
+    if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) {
+        if (threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) record_error(p.err, PKV_DEVERR_COPY_ID);
+        return;
+    }
+    uint4* cache = (blockIdx.z & 1) ? p.v[layer] : p.k[layer];
+    const uint4* from = cache + src * p.block_vecs;
+    uint4* to = cache + dst * p.block_vecs;
+    if (blockIdx.y == 0) {
+        float* scales = (blockIdx.z & 1) ? p.vs[layer] : p.ks[layer];
+        for (int h = threadIdx.x; h < p.num_kv_heads; h += kCopyThreads)
+            scales[dst * p.num_kv_heads + h] = scales[src * p.num_kv_heads + h];
+    }
+    const int64_t begin = (int64_t)blockIdx.y * kCopyChunk;
+    const int64_t end = min(p.block_vecs, begin + kCopyChunk);
+    for (int64_t i0 = begin + threadIdx.x; i0 < end; i0 += (int64_t)kCopyThreads * kCopyVecsPerThread) {
+        uint4 r[kCopyVecsPerThread];
+#pragma unroll
+        for (int u = 0; u < kCopyVecsPerThread; ++u) {
+            const int64_t i = i0 + (int64_t)u * kCopyThreads;
+            if (i < end) r[u] = from[i];
+        }
+#pragma unroll
+        for (int u = 0; u < kCopyVecsPerThread; ++u) {
+            const int64_t i = i0 + (int64_t)u * kCopyThreads;
+            if (i < end) to[i] = r[u];
+        }
+    }
+}
+
 // One thread per 16-byte vector of a (token, KV head) row, for K and V.
 __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
     pdl_launch_dependents();
@@ -128,6 +165,14 @@ cudaError_t launch_copy_blocks(const CopyParams& p, cudaStream_t stream, int* la
     const int64_t chunks = (p.block_vecs + kCopyChunk - 1) / kCopyChunk;
     const dim3 grid((unsigned)p.num_pairs, (unsigned)chunks, (unsigned)(2 * p.num_layers));
     const cudaError_t e = launch_pdl(copy_blocks_kernel, grid, dim3(kCopyThreads), 0, stream, p);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+cudaError_t launch_copy_blocks_fp8(const CopyFp8Params& p, cudaStream_t stream, int* launches) {
+    const int64_t chunks = (p.block_vecs + kCopyChunk - 1) / kCopyChunk;
+    const dim3 grid((unsigned)p.num_pairs, (unsigned)chunks, (unsigned)(2 * p.num_layers));
+    const cudaError_t e = launch_pdl(copy_blocks_fp8_kernel, grid, dim3(kCopyThreads), 0, stream, p);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

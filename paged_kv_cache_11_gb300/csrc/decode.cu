@@ -533,6 +533,13 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(const DecodeP
     }
 }
 
+cudaError_t launch_reduce(const DecodeParams& p, cudaStream_t stream, int* launches) {
+    const cudaError_t e =
+        launch_pdl(reduce_kernel, dim3(p.num_q_heads, p.num_seqs), dim3(kReduceWarps * 32), 0, stream, p);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
 template <bool kBF16, int BS, int NH>
 static cudaError_t launch_decode_t(const DecodeParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv,
                                    cudaStream_t stream, int* launches) {
@@ -550,12 +557,7 @@ static cudaError_t launch_decode_t(const DecodeParams& p, const CUtensorMap& tmk
     e = launch_pdl(kern, grid, dim3((NCW + 1) * 32), S::kDynamic, stream, tmk, tmv, p);
     if (e != cudaSuccess) return e;
     ++*launches;
-    if (p.split && !p.fuse_merge) {
-        e = launch_pdl(reduce_kernel, dim3(p.num_q_heads, p.num_seqs), dim3(kReduceWarps * 32), 0, stream, p);
-        if (e != cudaSuccess) return e;
-        ++*launches;
-    }
-    return cudaSuccess;
+    return p.split && !p.fuse_merge ? launch_reduce(p, stream, launches) : cudaSuccess;
 }
 
 cudaError_t launch_decode(const DecodeParams& p, int dtype, int block_size, const CUtensorMap& tmk,

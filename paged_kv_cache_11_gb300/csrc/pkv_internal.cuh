@@ -156,6 +156,60 @@ struct CompactParams {
 };
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream, int* launches);
 
+// Block write with rotation and norms (rope_append.cu).
+struct RopeParams {
+    int* err;
+    const uint16_t* q;           // 16-bit elements; token strides below
+    const uint16_t* k;
+    const uint16_t* v;
+    const int64_t* positions;    // nullptr: rot_dim == 0
+    const float* cos_sin;        // [max_position][rot_dim]
+    const uint16_t* q_norm;      // [kHeadDim] or nullptr
+    const uint16_t* k_norm;
+    const int64_t* slot_mapping;
+    uint16_t* q_out;             // [num_tokens][num_q_heads][kHeadDim]
+    void* k_cache;               // 16-bit elements, or e4m3 bytes
+    void* v_cache;
+    float* k_scales;             // [num_blocks][num_kv_heads] (8-bit pool only)
+    float* v_scales;
+    int64_t num_tokens, num_slots, max_position;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    int num_q_heads, num_kv_heads, block_size;
+    int rot_dim, interleaved;
+    float norm_eps;
+};
+// dtype: PKV_BF16 or PKV_FP16; fp8: the pool is e4m3 with scales.
+cudaError_t launch_rope_append(const RopeParams& p, int dtype, bool fp8, cudaStream_t stream, int* launches);
+
+// Whole-block copies of 8-bit pools with their scales, up to
+// kCopyFp8MaxLayers layers per launch (append_copy.cu).
+constexpr int kCopyFp8MaxLayers = 48;
+struct CopyFp8Params {
+    int* err;
+    uint4* k[kCopyFp8MaxLayers];
+    uint4* v[kCopyFp8MaxLayers];
+    float* ks[kCopyFp8MaxLayers];
+    float* vs[kCopyFp8MaxLayers];
+    const int64_t* pairs;         // [num_pairs][2] = (src, dst)
+    int64_t num_blocks;
+    int64_t block_vecs;           // 16-byte vectors per block of one cache
+    int num_kv_heads, num_layers, num_pairs;
+};
+cudaError_t launch_copy_blocks_fp8(const CopyFp8Params& p, cudaStream_t stream, int* launches);
+
+// Decode over an 8-bit pool (decode_fp8.cu).
+struct DecodeFp8Params {
+    DecodeParams d;
+    const uint8_t* k8;           // e4m3 pools
+    const uint8_t* v8;
+    const float* k_scales;       // [num_blocks][num_kv_heads]
+    const float* v_scales;
+    int q_bf16;                  // q is bf16 (else fp16)
+};
+cudaError_t launch_decode_fp8(const DecodeFp8Params& p, cudaStream_t stream, int* launches);
+// The merge kernel of split-K calls with many partitions (decode.cu).
+cudaError_t launch_reduce(const DecodeParams& p, cudaStream_t stream, int* launches);
+
 // Launch a kernel with programmatic stream serialisation: it may start while
 // the previous kernel on the stream is still running, and must call
 // pdl_wait() before touching any memory that kernel could write.
