@@ -14,6 +14,13 @@
 // the largest weight: a context's many small weights keep their bits beside a
 // few large ones.
 //
+// vs enters through P as well: a warp keeps O in units of a reference scale
+// vref and multiplies p by vs / vref, which fp16 holds without loss while the
+// ratio is in [2^-6, 1].  Only a scale outside of that moves O to a new
+// reference (a test that the whole warp passes together), so the products
+// accumulate in O directly.  (Adding each unit's product, times vs, to O took
+// 32 more multiply-adds per unit, and a wait for the products' end.)
+//
 // A unit of work is 16 tokens of one (block, KV head) tile: 2 KiB of K and 2
 // KiB of V.  The warps of a CTA take units in turn, each through a ring of its
 // own in shared memory, filled by 16-byte asynchronous copies.  Every lane
@@ -51,6 +58,13 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// 2^x, results below 2^-126 flushed to zero: the weights have no use for them.
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // The four e4m3 values of a word as two fp16 pairs (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\t"
@@ -64,8 +78,8 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
 template <int HT>
 struct DecodeFp8Smem {
     static constexpr int kRing = kF8Warps * kF8Stages * kF8StageBytes;
-    // per-warp rows, per-warp (m, l), per-row merge weights and lse
-    static constexpr int kRed = kF8Warps * HT * kRedStride * 4 + kF8Warps * HT * 2 * 4 + HT * (kF8Warps + 1) * 4;
+    // per-warp rows, per-warp (m, l, vref), per-row merge weights and lse
+    static constexpr int kRed = kF8Warps * HT * kRedStride * 4 + kF8Warps * HT * 3 * 4 + HT * (kF8Warps + 1) * 4;
     static constexpr int kFlags = ((kRing > kRed ? kRing : kRed) + 15) / 16 * 16;
     static constexpr int kTotal = kFlags + 16;
 };
@@ -138,18 +152,20 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
         }
         ids = id;
     };
-    auto issue = [&](int n) {
+    const uint8_t* kbase = fp.k8 + kvh * tile_bytes + g * D + t * 16;
+    const uint8_t* vbase = fp.v8 + kvh * tile_bytes + 2 * t * D + g * 16;
+    const float* sbase = (lane ? fp.v_scales : fp.k_scales) + kvh;
+    const int64_t block_bytes = p.num_kv_heads * tile_bytes;
+    auto issue = [&](int n, int st) {  // unit n into stage st
         if (n < mine) {
             if ((n & 31) == 0) load_ids(n);
             const int id = __shfl_sync(0xffffffffu, ids, n & 31);
             const int sub = (warp + n * NW) & (subs - 1);
-            const int64_t tile = (int64_t)id * p.num_kv_heads + kvh;
-            const uint8_t* ks = fp.k8 + tile * tile_bytes + sub * (16 * D);
-            const uint8_t* vs = fp.v8 + tile * tile_bytes + sub * (16 * D);
-            const uint32_t st = ring_sa + (n % NST) * kF8StageBytes;
-            const uint32_t dst = st + lane * 16;
-            const uint8_t* kr = ks + g * D + t * 16;
-            const uint8_t* vr = vs + 2 * t * D + g * 16;
+            const int64_t off = id * block_bytes + sub * (16 * D);
+            const uint8_t* kr = kbase + off;
+            const uint8_t* vr = vbase + off;
+            const uint32_t sa = ring_sa + st * kF8StageBytes;
+            const uint32_t dst = sa + lane * 16;
             cp_async16(dst, kr, policy);
             cp_async16(dst + 512, kr + 64, policy);
             cp_async16(dst + 1024, kr + 8 * D, policy);
@@ -158,12 +174,12 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
             cp_async16(dst + 2560, vr + D, policy);
             cp_async16(dst + 3072, vr + 8 * D, policy);
             cp_async16(dst + 3584, vr + 9 * D, policy);
-            if (lane < 2) cp_async4(st + kF8UnitBytes + 4 * lane, (lane ? fp.v_scales : fp.k_scales) + tile);
+            if (lane < 2) cp_async4(sa + kF8UnitBytes + 4 * lane, sbase + (int64_t)id * p.num_kv_heads);
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int n = 0; n < NST - 1; ++n) issue(n);
+    for (int n = 0; n < NST - 1; ++n) issue(n, n);
 
     // ---- the query: head 8n + g, dims of chunk t (k-steps 0-3) and t + 4 (4-7)
     uint32_t qf[NH][8][2];
@@ -216,21 +232,26 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
 
     WarpAcc<NH> a;  // o[mt][n]: dims 16g + 2mt (0, 1) and 16g + 2mt + 1 (2, 3) of heads 8n + 2t, 8n + 2t + 1
     acc_reset(a);
+    float vref = 0.f, vinv = 0.f;  // O's unit and its reciprocal; 0: O is zero and has none
 
+    int st = 0, st_in = NST - 1;  // stage of unit n and of unit n + NST - 1
     for (int n = 0; n < mine; ++n) {
         cp_async_wait<NST - 2>();
         __syncwarp();  // the scales' copies of lanes 0 and 1
-        issue(n + NST - 1);
-        const uint8_t* st = ring + (n % NST) * kF8StageBytes;
-        const uint4* own = reinterpret_cast<const uint4*>(st) + lane;
-        const float* sc_ = reinterpret_cast<const float*>(st + kF8UnitBytes);
-        const float ksc = sc_[0], vsc = sc_[1];
+        issue(n + NST - 1, st_in);
+        const uint8_t* stage = ring + st * kF8StageBytes;
+        st_in = st;  // this unit's stage is free when it has been used
+        st = st + 1 == NST ? 0 : st + 1;
+        const uint4* own = reinterpret_cast<const uint4*>(stage) + lane;
+        const float2 scl = *reinterpret_cast<const float2*>(stage + kF8UnitBytes);  // ks, vs
         const int valid = min(16, len - 16 * (warp + n * NW));  // >= 1
 
-        // ---- S^T = K8 Q^T: tokens g, g + 8 x heads 2t, 2t + 1
-        float sc[NH][4];
+        // ---- S^T = K8 Q^T: tokens g, g + 8 x heads 2t, 2t + 1, in two sums
+        float sc[NH][4], sc2[NH][4];
 #pragma unroll
-        for (int m = 0; m < NH; ++m) sc[m][0] = sc[m][1] = sc[m][2] = sc[m][3] = 0.f;
+        for (int m = 0; m < NH; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[m][e] = sc2[m][e] = 0.f;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const uint4 ka = own[32 * c], kb = own[32 * (c + 2)];
@@ -241,23 +262,43 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
                 e4m3x4_to_f16(wa[j], af[0], af[2]);
                 e4m3x4_to_f16(wb[j], af[1], af[3]);
 #pragma unroll
-                for (int m = 0; m < NH; ++m) mma_16816<false>(sc[m], af, qf[m][4 * c + j][0], qf[m][4 * c + j][1]);
+                for (int m = 0; m < NH; ++m)
+                    mma_16816<false>((j & 1) ? sc2[m] : sc[m], af, qf[m][4 * c + j][0], qf[m][4 * c + j][1]);
             }
+        }
+        uint32_t vw[4][4];  // V8: tokens 2t, 2t + 1, 2t + 8, 2t + 9, dims 16g .. 16g + 15
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint4 w = own[32 * (4 + r)];
+            vw[r][0] = w.x, vw[r][1] = w.y, vw[r][2] = w.z, vw[r][3] = w.w;
+        }
+#pragma unroll
+        for (int m = 0; m < NH; ++m) {
+            const float f0 = qs[m][0] * scl.x, f1 = qs[m][1] * scl.x;
+            sc[m][0] = (sc[m][0] + sc2[m][0]) * f0;
+            sc[m][1] = (sc[m][1] + sc2[m][1]) * f1;
+            sc[m][2] = (sc[m][2] + sc2[m][2]) * f0;
+            sc[m][3] = (sc[m][3] + sc2[m][3]) * f1;
+        }
+        if (valid < 16) {
+            // rows past the context may hold anything (even NaN): their
+            // scores become -inf, their V rows zeros
+#pragma unroll
+            for (int m = 0; m < NH; ++m) {
+                if (g >= valid) sc[m][0] = sc[m][1] = -INFINITY;
+                if (g + 8 >= valid) sc[m][2] = sc[m][3] = -INFINITY;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (2 * t + (r & 1) + 8 * (r >> 1) >= valid) vw[r][0] = vw[r][1] = vw[r][2] = vw[r][3] = 0u;
         }
         // ---- online softmax; the maximum is raised, and O and l rescaled,
         // only when a score passes it by more than kLazyMargin
-        const bool va = g < valid, vb = g + 8 < valid;
         bool need = false;
 #pragma unroll
-        for (int m = 0; m < NH; ++m) {
-            const float f0 = qs[m][0] * ksc, f1 = qs[m][1] * ksc;
-            sc[m][0] = va ? sc[m][0] * f0 : -INFINITY;
-            sc[m][1] = va ? sc[m][1] * f1 : -INFINITY;
-            sc[m][2] = vb ? sc[m][2] * f0 : -INFINITY;
-            sc[m][3] = vb ? sc[m][3] * f1 : -INFINITY;
+        for (int m = 0; m < NH; ++m)
             need |= fmaxf(sc[m][0], sc[m][2]) > a.m[m][0] + kLazyMargin ||
                     fmaxf(sc[m][1], sc[m][3]) > a.m[m][1] + kLazyMargin;
-        }
         if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
             for (int m = 0; m < NH; ++m)
@@ -267,7 +308,7 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                     const float mn = fmaxf(a.m[m][c], mx);
-                    const float al = mn == -INFINITY ? 1.f : exp2f(a.m[m][c] - mn);
+                    const float al = mn == -INFINITY ? 1.f : exp2_ftz(a.m[m][c] - mn);
                     a.m[m][c] = mn;
                     a.l[m][c] *= al;
 #pragma unroll
@@ -277,14 +318,37 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
                     }
                 }
         }
+        float ratio = scl.y * vinv;  // the same in every lane
+        if (!(fabsf(ratio) <= 1.f && fabsf(ratio) >= 0x1p-6f)) {
+            if (vref == 0.f) {
+                vref = scl.y;  // a scale of zero adds nothing and sets nothing
+                vinv = vref == 0.f ? 0.f : 1.f / vref;
+                ratio = vref == 0.f ? 0.f : 1.f;
+            } else if (!(fabsf(ratio) < 0x1p-60f)) {
+                // (a scale 2^-60 times the unit or less is folded as it is:
+                // what it adds is lost beside the unit, and O times the
+                // inverse could leave fp32's range)
+                const float f = vref / scl.y;
+#pragma unroll
+                for (int m = 0; m < NH; ++m)
+#pragma unroll
+                    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a.o[mt][m][e] *= f;
+                vref = scl.y;
+                vinv = 1.f / vref;
+                ratio = 1.f;
+            }
+        }
         uint32_t ph[NH][2], pl[NH][2];
 #pragma unroll
         for (int m = 0; m < NH; ++m) {
             const float m0 = a.m[m][0] == -INFINITY ? 0.f : a.m[m][0], m1 = a.m[m][1] == -INFINITY ? 0.f : a.m[m][1];
-            const float p0 = exp2f(sc[m][0] - m0 + kF8Lift), p1 = exp2f(sc[m][1] - m1 + kF8Lift);
-            const float p2 = exp2f(sc[m][2] - m0 + kF8Lift), p3 = exp2f(sc[m][3] - m1 + kF8Lift);
+            float p0 = exp2_ftz(sc[m][0] - m0 + kF8Lift), p1 = exp2_ftz(sc[m][1] - m1 + kF8Lift);
+            float p2 = exp2_ftz(sc[m][2] - m0 + kF8Lift), p3 = exp2_ftz(sc[m][3] - m1 + kF8Lift);
             a.l[m][0] += p0 + p2;
             a.l[m][1] += p1 + p3;
+            p0 *= ratio, p1 *= ratio, p2 *= ratio, p3 *= ratio;
             float r0, r1, r2, r3;
             const uint32_t h01 = pack2<false>(p0, p1, r0, r1), h23 = pack2<false>(p2, p3, r2, r3);
             ph[m][0] = movmatrix_trans(h01);
@@ -292,18 +356,7 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
             pl[m][0] = movmatrix_trans(pack2<false>(p0 - r0, p1 - r1));
             pl[m][1] = movmatrix_trans(pack2<false>(p2 - r2, p3 - r3));
         }
-        // ---- O^T += vs V8^T P^T: tokens 2t, 2t + 1 (k 0-7), 2t + 8, 2t + 9
-        uint32_t vw[4][4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint4 w = own[32 * (4 + r)];
-            // rows past the context may hold anything (even NaN): zeros
-            const bool keep = 2 * t + (r & 1) + 8 * (r >> 1) < valid;
-            vw[r][0] = keep ? w.x : 0u;
-            vw[r][1] = keep ? w.y : 0u;
-            vw[r][2] = keep ? w.z : 0u;
-            vw[r][3] = keep ? w.w : 0u;
-        }
+        // ---- O^T += V8^T P^T: tokens 2t, 2t + 1 (k 0-7), 2t + 8, 2t + 9
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             const int j = mt >> 1;
@@ -313,11 +366,8 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
             e4m3x4_to_f16(__byte_perm(vw[2][j], vw[3][j], sel), af[2], af[3]);
 #pragma unroll
             for (int m = 0; m < NH; ++m) {
-                float o[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16816<false>(o, af, pl[m][0], pl[m][1]);
-                mma_16816<false>(o, af, ph[m][0], ph[m][1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) a.o[mt][m][e] = fmaf(o[e], vsc, a.o[mt][m][e]);
+                mma_16816<false>(a.o[mt][m], af, ph[m][0], ph[m][1]);
+                mma_16816<false>(a.o[mt][m], af, pl[m][0], pl[m][1]);
             }
         }
     }
@@ -328,8 +378,8 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     // ---- merge the warps' states, as the decode kernel does
     const int fl = flags[0];
     float* red = reinterpret_cast<float*>(smem);  // [NW][HT][kRedStride]
-    float* ml = red + NW * HT * kRedStride;       // [NW][HT][2]
-    float* wts = ml + NW * HT * 2;                // [HT][NW + 1]: weights, then the row's lse
+    float* ml = red + NW * HT * kRedStride;       // [NW][HT][3]: m, l, vref
+    float* wts = ml + NW * HT * 3;                // [HT][NW + 1]: weights, then the row's lse
 #pragma unroll
     for (int m = 0; m < NH; ++m)
 #pragma unroll
@@ -343,8 +393,9 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
                         make_float4(a.o[2 * q][m][c], a.o[2 * q][m][c + 2], a.o[2 * q + 1][m][c],
                                     a.o[2 * q + 1][m][c + 2]);
                 if (g == 0) {
-                    ml[(warp * HT + hr) * 2] = a.m[m][c];
-                    ml[(warp * HT + hr) * 2 + 1] = a.l[m][c];
+                    ml[(warp * HT + hr) * 3] = a.m[m][c];
+                    ml[(warp * HT + hr) * 3 + 1] = a.l[m][c];
+                    ml[(warp * HT + hr) * 3 + 2] = vref;
                 }
             }
         }
@@ -352,17 +403,17 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     if (tid < rows) {
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * HT + tid) * 2]);
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * HT + tid) * 3]);
         const float Mf = M == -INFINITY ? 0.f : M;
         float f[NW], sum = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            f[w] = exp2f(ml[(w * HT + tid) * 2] - Mf);  // a warp without units: 0
-            sum += f[w] * ml[(w * HT + tid) * 2 + 1];
+            f[w] = exp2f(ml[(w * HT + tid) * 3] - Mf);  // a warp without units: 0
+            sum += f[w] * ml[(w * HT + tid) * 3 + 1];
         }
         const float inv = 1.f / sum;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) wts[tid * (NW + 1) + w] = f[w] * inv;
+        for (int w = 0; w < NW; ++w) wts[tid * (NW + 1) + w] = f[w] * inv * ml[(w * HT + tid) * 3 + 2];
         // A NaN among the scores makes the outputs NaN; the merge would pass
         // over a partition whose lse is one, so it gets a finite lse.
         const float lse = M + log2f(sum) - kF8Lift;

@@ -59,6 +59,31 @@ def test_scales_far_apart(gpu, bs):
     _check(decode_inputs(17, (500, 90, 1), 8, 2, bs, BF, wild_scales=True), gpu)
 
 
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("vs", [(0.0, 2.0 ** -64, 1.0, 2.0 ** -30, -1.0, 0.0, 2.0 ** 20), (0.0,), (0.3, 0.29, 0.31, 5.0),
+                                (2.0 ** -64, 2.0 ** -63, 0.0), (-0.5, 0.5, -0.25, 1.0)])
+def test_scales_of_any_sign_and_size(gpu, vs, order):
+    inp = decode_inputs(23, (700, 90, 16), 8, 2, 16, BF)
+    n = inp["v_scales"].shape[0]
+    scales = torch.tensor((vs * n)[:n])
+    inp["v_scales"][:] = (scales if order > 0 else scales.flip(0))[:, None]
+    inp["k_scales"][::3] = 0
+    _check(inp, gpu)
+    _check(inp, gpu, partition_size=64)
+
+
+@pytest.mark.parametrize("at", [0, 3, 20])
+def test_a_block_of_huge_values_without_weight(gpu, at):
+    """Values 2^40 times the others' that no weight reaches: the output keeps the others' full precision."""
+    inp = decode_inputs(24, (500,), 4, 1, 16, BF)
+    b = int(inp["block_tables"][0, at])
+    inp["q"][:] = inp["q"][:, :1].abs()
+    inp["k_cache"].view(torch.uint8)[b] |= 0x80                       # every key of the block against the query
+    inp["k_scales"][b] = 2.0
+    inp["v_scales"][b] = 2.0 ** 40
+    _check(inp, gpu)
+
+
 @pytest.mark.parametrize("factor", [1e-30, 1e-4, 20.0])
 def test_small_and_large_queries(gpu, factor):
     inp = decode_inputs(5, (300, 40), 8, 2, 16, BF)
