@@ -23,27 +23,26 @@
 //
 // A unit of work is 16 tokens of one (block, KV head) tile: 2 KiB of K and 2
 // KiB of V.  The warps of a CTA take units in turn, each through a ring of its
-// own in shared memory, filled by 16-byte asynchronous copies.  Every lane
-// copies the very bytes that it will use, so a stage needs no barrier between
-// lanes but for its two scales:
-//   K: rows g and g + 8 (g = lane / 4), 16-byte chunks t and t + 4 of the row
-//      (t = lane % 4): full 32-byte sectors, and with the query held in the
-//      same order of dims, word j of a chunk is the A operand of k-step j;
-//   V: tokens 2t, 2t + 1, 2t + 8, 2t + 9, chunk g of the row: byte pairs of
-//      two tokens are interleaved (PRMT) to make the A operand of V^T, and a
-//      lane ends up with 16 neighbouring dims of the output.
+// own in shared memory, filled by 16-byte asynchronous copies of whole rows
+// (copies of half rows, each lane its own bytes, held the stream to 5.2 TB/s).
+// A lane (g = lane / 4, t = lane % 4) reads 16-byte chunks of them:
+//   K: rows g and g + 8, chunks 2t and 2t + 1: with the query held in the same
+//      order of dims, word j of a chunk is the A operand of one k-step;
+//   V: tokens 2t, 2t + 1, 2t + 8, 2t + 9, chunk g: byte pairs of two tokens
+//      are interleaved (PRMT) to make the A operand of V^T, and a lane ends up
+//      with 16 neighbouring dims of the output.
 // TMA copies would be 2 KiB each here, which the SM's TMA unit takes some 75
 // cycles for, 150 of the about 180 that a unit may cost at full bandwidth.
 #include "decode_common.cuh"
 
 namespace pkv {
 
-constexpr int kF8Warps = 4;             // consumer warps per CTA, each with a ring of its own
-constexpr int kF8Stages = 3;            // units in flight per warp
-constexpr int kF8CtasPerSm = 4;
+constexpr int kF8Warps = 4;             // warps per CTA, each with a ring of its own
+constexpr int kF8Stages = 2;            // pairs of units: one in use, the others in flight
+constexpr int kF8CtasPerSm = 3;
 constexpr float kF8Lift = 7.f;          // log2; kLazyMargin + kF8Lift stays below fp16's 2^16
 constexpr int kF8UnitBytes = 2 * 16 * kHeadDim;       // 16 tokens of K and V
-constexpr int kF8StageBytes = kF8UnitBytes + 16;      // and their two scales
+constexpr int kF8StageBytes = 2 * kF8UnitBytes + 16;  // two units and their scales: ks, vs, ks, vs
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint64_t policy) {
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
@@ -119,69 +118,81 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     }
     const int tok0 = part * p.partition_size;
     const int len = min(L - tok0, p.partition_size);  // tokens of this partition
-    const int nunits = (len + 15) / 16;
-    const int subs = p.block_size >> 4;  // units per block: 1 or 2
+    const int npairs = (len + 31) / 32;
+    const bool whole = p.block_size == 32;  // a pair is one block (else two)
     const bool write_partial = p.split && nparts > 1;
 
     int* flags = reinterpret_cast<int*>(smem + S::kFlags);  // [0]: bad block id, [1]: last-arrival verdict
     if (tid == 0) flags[0] = 0;
     __syncthreads();
 
-    // ---- this warp's units: warp, warp + NW, ...
-    const int mine = nunits > warp ? (nunits - 1 - warp) / NW + 1 : 0;
+    // ---- this warp's pairs: warp, warp + NW, ...
+    const int mine = npairs > warp ? (npairs - 1 - warp) / NW + 1 : 0;
     const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks_per_seq + tok0 / p.block_size;
+    const int nblk = (len - 1) / p.block_size + 1;  // blocks of this partition
     const uint64_t policy = l2_policy_evict_first();
     const int64_t tile_bytes = (int64_t)p.block_size * D;
     uint8_t* ring = smem + warp * (NST * kF8StageBytes);
     const uint32_t ring_sa = smem_addr(ring);
 
-    int ids = 0;
-    // Block id of the warp's n-th unit: 32 are read at a time, a lane each.
+    int ids0 = 0, ids1 = 0;
+    // Block ids of the warp's n-th pair: 32 pairs are read at a time, a lane
+    // each.  A pair without a second unit names its first block twice (its
+    // tokens are masked).
     auto load_ids = [&](int n0) {
         const int n = n0 + lane;
-        int id = 0;
         bool bad = false;
         if (n < mine) {
-            id = __ldg(table + (warp + n * NW) / subs);
-            bad = id < 0 || (int64_t)id >= p.num_blocks;
-            if (bad) id = 0;  // the output is zeroed below
+            const int pr = warp + n * NW;
+            const int b0 = whole ? pr : 2 * pr, b1 = whole ? pr : min(2 * pr + 1, nblk - 1);
+            ids0 = __ldg(table + b0);
+            ids1 = __ldg(table + b1);
+            bad = ids0 < 0 || (int64_t)ids0 >= p.num_blocks || ids1 < 0 || (int64_t)ids1 >= p.num_blocks;
+            if (bad) ids0 = ids1 = 0;  // the output is zeroed below
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) {
             atomicOr(flags, 1);
             record_error(p.err, PKV_DEVERR_BLOCK_ID);
         }
-        ids = id;
     };
-    const uint8_t* kbase = fp.k8 + kvh * tile_bytes + g * D + t * 16;
-    const uint8_t* vbase = fp.v8 + kvh * tile_bytes + 2 * t * D + g * 16;
-    const float* sbase = (lane ? fp.v_scales : fp.k_scales) + kvh;
+    // A copy instruction brings four whole rows; lane l has chunk l % 8 of row
+    // l / 8.  Chunk c of row r goes to chunk c ^ (r % 8) of its row in shared
+    // memory, which keeps the reads below free of bank conflicts.
+    const uint8_t* kbase = fp.k8 + kvh * tile_bytes + lane * 16;
+    const uint8_t* vbase = fp.v8 + kvh * tile_bytes + lane * 16;
+    const int r8 = lane >> 3, put = (lane >> 3) * D;
+    const uint32_t put0 = put + (((lane & 7) ^ r8) << 4), put1 = put + (((lane & 7) ^ (r8 + 4)) << 4) + 4 * D;
+    const float* sbase = ((lane & 1) ? fp.v_scales : fp.k_scales) + kvh;
     const int64_t block_bytes = p.num_kv_heads * tile_bytes;
-    auto issue = [&](int n, int st) {  // unit n into stage st
+    const int second = whole ? 16 * D : 0;  // where a pair's second unit starts in its block
+    auto issue = [&](int n, int st) {       // pair n into stage st
         if (n < mine) {
             if ((n & 31) == 0) load_ids(n);
-            const int id = __shfl_sync(0xffffffffu, ids, n & 31);
-            const int sub = (warp + n * NW) & (subs - 1);
-            const int64_t off = id * block_bytes + sub * (16 * D);
-            const uint8_t* kr = kbase + off;
-            const uint8_t* vr = vbase + off;
+            const int id0 = __shfl_sync(0xffffffffu, ids0, n & 31), id1 = __shfl_sync(0xffffffffu, ids1, n & 31);
             const uint32_t sa = ring_sa + st * kF8StageBytes;
-            const uint32_t dst = sa + lane * 16;
-            cp_async16(dst, kr, policy);
-            cp_async16(dst + 512, kr + 64, policy);
-            cp_async16(dst + 1024, kr + 8 * D, policy);
-            cp_async16(dst + 1536, kr + 8 * D + 64, policy);
-            cp_async16(dst + 2048, vr, policy);
-            cp_async16(dst + 2560, vr + D, policy);
-            cp_async16(dst + 3072, vr + 8 * D, policy);
-            cp_async16(dst + 3584, vr + 9 * D, policy);
-            if (lane < 2) cp_async4(sa + kF8UnitBytes + 4 * lane, sbase + (int64_t)id * p.num_kv_heads);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int64_t off = (u ? id1 : id0) * block_bytes + (u ? second : 0);
+                const uint8_t* kr = kbase + off;
+                const uint8_t* vr = vbase + off;
+                const uint32_t dst = sa + u * kF8UnitBytes;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // rows 8i .. 8i + 7 of K and of V
+                    cp_async16(dst + put0 + 8 * D * i, kr + 8 * D * i, policy);
+                    cp_async16(dst + put1 + 8 * D * i, kr + 8 * D * i + 4 * D, policy);
+                    cp_async16(dst + put0 + 8 * D * i + 16 * D, vr + 8 * D * i, policy);
+                    cp_async16(dst + put1 + 8 * D * i + 16 * D, vr + 8 * D * i + 4 * D, policy);
+                }
+            }
+            if (lane < 4)
+                cp_async4(sa + 2 * kF8UnitBytes + 4 * lane, sbase + (int64_t)(lane < 2 ? id0 : id1) * p.num_kv_heads);
         }
         cp_async_commit();
     };
 #pragma unroll
     for (int n = 0; n < NST - 1; ++n) issue(n, n);
 
-    // ---- the query: head 8n + g, dims of chunk t (k-steps 0-3) and t + 4 (4-7)
+    // ---- the query: head 8n + g, dims of chunk 2t (k-steps 0-3) and 2t + 1 (4-7)
     uint32_t qf[NH][8][2];
     float qs[NH][2];  // what a product of the heads 8n + 2t, 8n + 2t + 1 is multiplied by
 #pragma unroll
@@ -193,7 +204,7 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
             const uint16_t* qr = static_cast<const uint16_t*>(p.q) + ((int64_t)s * p.num_q_heads + h0 + hr) * D;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {  // 8 values each
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(qr + (c >> 1) * 64 + 16 * t + (c & 1) * 8));
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(qr + 32 * t + 8 * c));
                 const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -234,129 +245,8 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     acc_reset(a);
     float vref = 0.f, vinv = 0.f;  // O's unit and its reciprocal; 0: O is zero and has none
 
-    int st = 0, st_in = NST - 1;  // stage of unit n and of unit n + NST - 1
-    for (int n = 0; n < mine; ++n) {
-        cp_async_wait<NST - 2>();
-        __syncwarp();  // the scales' copies of lanes 0 and 1
-        issue(n + NST - 1, st_in);
-        const uint8_t* stage = ring + st * kF8StageBytes;
-        st_in = st;  // this unit's stage is free when it has been used
-        st = st + 1 == NST ? 0 : st + 1;
-        const uint4* own = reinterpret_cast<const uint4*>(stage) + lane;
-        const float2 scl = *reinterpret_cast<const float2*>(stage + kF8UnitBytes);  // ks, vs
-        const int valid = min(16, len - 16 * (warp + n * NW));  // >= 1
-
-        // ---- S^T = K8 Q^T: tokens g, g + 8 x heads 2t, 2t + 1, in two sums
-        float sc[NH][4], sc2[NH][4];
-#pragma unroll
-        for (int m = 0; m < NH; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[m][e] = sc2[m][e] = 0.f;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const uint4 ka = own[32 * c], kb = own[32 * (c + 2)];
-            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t af[4];
-                e4m3x4_to_f16(wa[j], af[0], af[2]);
-                e4m3x4_to_f16(wb[j], af[1], af[3]);
-#pragma unroll
-                for (int m = 0; m < NH; ++m)
-                    mma_16816<false>((j & 1) ? sc2[m] : sc[m], af, qf[m][4 * c + j][0], qf[m][4 * c + j][1]);
-            }
-        }
-        uint32_t vw[4][4];  // V8: tokens 2t, 2t + 1, 2t + 8, 2t + 9, dims 16g .. 16g + 15
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint4 w = own[32 * (4 + r)];
-            vw[r][0] = w.x, vw[r][1] = w.y, vw[r][2] = w.z, vw[r][3] = w.w;
-        }
-#pragma unroll
-        for (int m = 0; m < NH; ++m) {
-            const float f0 = qs[m][0] * scl.x, f1 = qs[m][1] * scl.x;
-            sc[m][0] = (sc[m][0] + sc2[m][0]) * f0;
-            sc[m][1] = (sc[m][1] + sc2[m][1]) * f1;
-            sc[m][2] = (sc[m][2] + sc2[m][2]) * f0;
-            sc[m][3] = (sc[m][3] + sc2[m][3]) * f1;
-        }
-        if (valid < 16) {
-            // rows past the context may hold anything (even NaN): their
-            // scores become -inf, their V rows zeros
-#pragma unroll
-            for (int m = 0; m < NH; ++m) {
-                if (g >= valid) sc[m][0] = sc[m][1] = -INFINITY;
-                if (g + 8 >= valid) sc[m][2] = sc[m][3] = -INFINITY;
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (2 * t + (r & 1) + 8 * (r >> 1) >= valid) vw[r][0] = vw[r][1] = vw[r][2] = vw[r][3] = 0u;
-        }
-        // ---- online softmax; the maximum is raised, and O and l rescaled,
-        // only when a score passes it by more than kLazyMargin
-        bool need = false;
-#pragma unroll
-        for (int m = 0; m < NH; ++m)
-            need |= fmaxf(sc[m][0], sc[m][2]) > a.m[m][0] + kLazyMargin ||
-                    fmaxf(sc[m][1], sc[m][3]) > a.m[m][1] + kLazyMargin;
-        if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-            for (int m = 0; m < NH; ++m)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float mx = fmaxf(sc[m][c], sc[m][c + 2]);
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    const float mn = fmaxf(a.m[m][c], mx);
-                    const float al = mn == -INFINITY ? 1.f : exp2_ftz(a.m[m][c] - mn);
-                    a.m[m][c] = mn;
-                    a.l[m][c] *= al;
-#pragma unroll
-                    for (int mt = 0; mt < 8; ++mt) {
-                        a.o[mt][m][c] *= al;
-                        a.o[mt][m][c + 2] *= al;
-                    }
-                }
-        }
-        float ratio = scl.y * vinv;  // the same in every lane
-        if (!(fabsf(ratio) <= 1.f && fabsf(ratio) >= 0x1p-6f)) {
-            if (vref == 0.f) {
-                vref = scl.y;  // a scale of zero adds nothing and sets nothing
-                vinv = vref == 0.f ? 0.f : 1.f / vref;
-                ratio = vref == 0.f ? 0.f : 1.f;
-            } else if (!(fabsf(ratio) < 0x1p-60f)) {
-                // (a scale 2^-60 times the unit or less is folded as it is:
-                // what it adds is lost beside the unit, and O times the
-                // inverse could leave fp32's range)
-                const float f = vref / scl.y;
-#pragma unroll
-                for (int m = 0; m < NH; ++m)
-#pragma unroll
-                    for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) a.o[mt][m][e] *= f;
-                vref = scl.y;
-                vinv = 1.f / vref;
-                ratio = 1.f;
-            }
-        }
-        uint32_t ph[NH][2], pl[NH][2];
-#pragma unroll
-        for (int m = 0; m < NH; ++m) {
-            const float m0 = a.m[m][0] == -INFINITY ? 0.f : a.m[m][0], m1 = a.m[m][1] == -INFINITY ? 0.f : a.m[m][1];
-            float p0 = exp2_ftz(sc[m][0] - m0 + kF8Lift), p1 = exp2_ftz(sc[m][1] - m1 + kF8Lift);
-            float p2 = exp2_ftz(sc[m][2] - m0 + kF8Lift), p3 = exp2_ftz(sc[m][3] - m1 + kF8Lift);
-            a.l[m][0] += p0 + p2;
-            a.l[m][1] += p1 + p3;
-            p0 *= ratio, p1 *= ratio, p2 *= ratio, p3 *= ratio;
-            float r0, r1, r2, r3;
-            const uint32_t h01 = pack2<false>(p0, p1, r0, r1), h23 = pack2<false>(p2, p3, r2, r3);
-            ph[m][0] = movmatrix_trans(h01);
-            ph[m][1] = movmatrix_trans(h23);
-            pl[m][0] = movmatrix_trans(pack2<false>(p0 - r0, p1 - r1));
-            pl[m][1] = movmatrix_trans(pack2<false>(p2 - r2, p3 - r3));
-        }
-        // ---- O^T += V8^T P^T: tokens 2t, 2t + 1 (k 0-7), 2t + 8, 2t + 9
+    // O^T += V8^T P^T of one unit: tokens 2t, 2t + 1 (k 0-7), 2t + 8, 2t + 9
+    auto pv = [&](const uint32_t (&vw)[4][4], const uint32_t (&ph)[NH][2], const uint32_t (&pl)[NH][2]) {
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             const int j = mt >> 1;
@@ -370,6 +260,185 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
                 mma_16816<false>(a.o[mt][m], af, pl[m][0], pl[m][1]);
             }
         }
+    };
+    // P^T of one unit as two B operands: the fp16 value and the fp16 residual
+    auto split = [&](const float (&x)[NH][4], float ratio, uint32_t (&ph)[NH][2], uint32_t (&pl)[NH][2]) {
+#pragma unroll
+        for (int m = 0; m < NH; ++m) {
+            const float p0 = x[m][0] * ratio, p1 = x[m][1] * ratio, p2 = x[m][2] * ratio, p3 = x[m][3] * ratio;
+            float r0, r1, r2, r3;
+            const uint32_t h01 = pack2<false>(p0, p1, r0, r1), h23 = pack2<false>(p2, p3, r2, r3);
+            ph[m][0] = movmatrix_trans(h01);
+            ph[m][1] = movmatrix_trans(h23);
+            pl[m][0] = movmatrix_trans(pack2<false>(p0 - r0, p1 - r1));
+            pl[m][1] = movmatrix_trans(pack2<false>(p2 - r2, p3 - r3));
+        }
+    };
+    // where the lane's chunks lie in a unit: K row g, chunks 2t and 2t + 1; V
+    // rows 2t and 2t + 1, chunk g (rows 8 further on are 8 D further on)
+    const uint32_t get_k0 = g * D + (((2 * t) ^ g) << 4), get_k1 = g * D + (((2 * t + 1) ^ g) << 4);
+    const uint32_t get_v0 = 16 * D + 2 * t * D + ((g ^ (2 * t)) << 4);
+    const uint32_t get_v1 = 16 * D + (2 * t + 1) * D + ((g ^ (2 * t + 1)) << 4);
+    // V8 of one unit: tokens 2t, 2t + 1, 2t + 8, 2t + 9, dims 16g .. 16g + 15;
+    // rows past the context may hold anything (even NaN): zeros
+    auto load_v = [&](const uint8_t* unit, int valid, uint32_t (&vw)[4][4]) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint4 w = *reinterpret_cast<const uint4*>(unit + ((r & 1) ? get_v1 : get_v0) + (r >> 1) * (8 * D));
+            vw[r][0] = w.x, vw[r][1] = w.y, vw[r][2] = w.z, vw[r][3] = w.w;
+        }
+        if (valid < 16) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (2 * t + (r & 1) + 8 * (r >> 1) >= valid) vw[r][0] = vw[r][1] = vw[r][2] = vw[r][3] = 0u;
+        }
+    };
+    // Moves O to the unit of scale vs where it has to; returns vs / vref.
+    auto take_scale = [&](float vs) {
+        float ratio = vs * vinv;
+        if (fabsf(ratio) <= 1.f && fabsf(ratio) >= 0x1p-6f) return ratio;
+        if (vref == 0.f) {
+            vref = vs;  // a scale of zero adds nothing and sets nothing
+            vinv = vref == 0.f ? 0.f : 1.f / vref;
+            ratio = vref == 0.f ? 0.f : 1.f;
+        } else if (!(fabsf(ratio) < 0x1p-60f)) {
+            // (a scale 2^-60 times the unit or less is folded as it is: what
+            // it adds is lost beside the unit, and O times the inverse could
+            // leave fp32's range)
+            const float f = vref / vs;
+#pragma unroll
+            for (int m = 0; m < NH; ++m)
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a.o[mt][m][e] *= f;
+            vref = vs;
+            vinv = 1.f / vref;
+            ratio = 1.f;
+        }
+        return ratio;
+    };
+
+    int st = 0, st_in = NST - 1;  // stage of pair n and of pair n + NST - 1
+    for (int n = 0; n < mine; ++n) {
+        cp_async_wait<NST - 2>();
+        __syncwarp();  // the scales' copies of lanes 0 to 3
+        issue(n + NST - 1, st_in);
+        const uint8_t* stage = ring + st * kF8StageBytes;
+        st_in = st;  // this pair's stage is free when it has been used
+        st = st + 1 == NST ? 0 : st + 1;
+        const float4 scl = *reinterpret_cast<const float4*>(stage + 2 * kF8UnitBytes);  // ks, vs of both units
+        const int valid = len - 32 * (warp + n * NW);  // >= 1
+
+        // ---- S^T = K8 Q^T: tokens g, g + 8 of each unit x heads 2t, 2t + 1
+        float sc[2][NH][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int m = 0; m < NH; ++m) sc[u][m][0] = sc[u][m][1] = sc[u][m][2] = sc[u][m][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint4 ka[2], kb[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint8_t* at = stage + u * kF8UnitBytes + (c ? get_k1 : get_k0);
+                ka[u] = *reinterpret_cast<const uint4*>(at);
+                kb[u] = *reinterpret_cast<const uint4*>(at + 8 * D);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t af[4];
+                    e4m3x4_to_f16(reinterpret_cast<const uint32_t*>(&ka[u])[j], af[0], af[2]);
+                    e4m3x4_to_f16(reinterpret_cast<const uint32_t*>(&kb[u])[j], af[1], af[3]);
+#pragma unroll
+                    for (int m = 0; m < NH; ++m)
+                        mma_16816<false>(sc[u][m], af, qf[m][4 * c + j][0], qf[m][4 * c + j][1]);
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int m = 0; m < NH; ++m) {
+                const float f0 = qs[m][0] * (u ? scl.z : scl.x), f1 = qs[m][1] * (u ? scl.z : scl.x);
+                sc[u][m][0] *= f0, sc[u][m][1] *= f1, sc[u][m][2] *= f0, sc[u][m][3] *= f1;
+            }
+        if (valid < 32) {  // tokens past the context do not count
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int m = 0; m < NH; ++m) {
+                    if (16 * u + g >= valid) sc[u][m][0] = sc[u][m][1] = -INFINITY;
+                    if (16 * u + g + 8 >= valid) sc[u][m][2] = sc[u][m][3] = -INFINITY;
+                }
+        }
+        // ---- online softmax; the maximum is raised, and O and l rescaled,
+        // only when a score passes it by more than kLazyMargin
+        bool need = false;
+        float mx[NH][2];
+#pragma unroll
+        for (int m = 0; m < NH; ++m)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                mx[m][c] = fmaxf(fmaxf(sc[0][m][c], sc[0][m][c + 2]), fmaxf(sc[1][m][c], sc[1][m][c + 2]));
+                need |= mx[m][c] > a.m[m][c] + kLazyMargin;
+            }
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int m = 0; m < NH; ++m)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x = mx[m][c];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                    const float mn = fmaxf(a.m[m][c], x);
+                    const float al = mn == -INFINITY ? 1.f : exp2_ftz(a.m[m][c] - mn);
+                    a.m[m][c] = mn;
+                    a.l[m][c] *= al;
+#pragma unroll
+                    for (int mt = 0; mt < 8; ++mt) {
+                        a.o[mt][m][c] *= al;
+                        a.o[mt][m][c + 2] *= al;
+                    }
+                }
+        }
+#pragma unroll
+        for (int m = 0; m < NH; ++m)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float m0 = a.m[m][c] == -INFINITY ? 0.f : a.m[m][c];
+                float sum = 0.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        sc[u][m][c + 2 * r] = exp2_ftz(sc[u][m][c + 2 * r] - m0 + kF8Lift);
+                        sum += sc[u][m][c + 2 * r];
+                    }
+                a.l[m][c] += sum;
+            }
+        // ---- O^T += vs V8^T P^T, unit by unit
+        uint32_t vw[4][4], ph[NH][2], pl[NH][2];
+        float r0 = scl.y * vinv, r1 = scl.w * vinv;
+        const bool keep = fabsf(r0) <= 1.f && fabsf(r0) >= 0x1p-6f && fabsf(r1) <= 1.f && fabsf(r1) >= 0x1p-6f;
+        if (!keep) {  // the first unit by itself, at the unit that its scale sets
+            r0 = take_scale(scl.y);
+            split(sc[0], r0, ph, pl);
+            load_v(stage, valid, vw);
+            pv(vw, ph, pl);
+#pragma unroll
+            for (int m = 0; m < NH; ++m) sc[0][m][0] = sc[0][m][1] = sc[0][m][2] = sc[0][m][3] = 0.f;
+            r1 = valid > 16 ? take_scale(scl.w) : 0.f;
+            r0 = 0.f;
+        }
+        uint32_t ph1[NH][2], pl1[NH][2];
+        split(sc[0], r0, ph, pl);
+        split(sc[1], r1, ph1, pl1);
+        load_v(stage, valid, vw);
+        pv(vw, ph, pl);
+        load_v(stage + kF8UnitBytes, valid - 16, vw);
+        pv(vw, ph1, pl1);
     }
     acc_finish(a);
     cp_async_wait<0>();

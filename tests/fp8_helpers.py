@@ -267,8 +267,10 @@ def decode_ref(inp, scale, out_dtype, heads=None):
     for exp2 and the split of P, by the roundings of 2^-24 of the sums over one
     warp's units (L / 64 at most, an addition and a rescale each), of the
     products inside a unit and of the merges (fewer than 80), relative to the
-    sum of weights times values, and by 2^-31 of the largest weight where fp16
-    has no smaller step.  The output's own rounding comes on top.
+    sum of weights times values, and by 2^-26 of the largest weight, or all of
+    the weight where it is smaller, where fp16 has no smaller step (2^-24 in a P
+    lifted by 2^7, of a scale of at least 2^-6 of O's unit).  The output's own
+    rounding comes on top.
     """
     bs, hkv = inp["k_cache"].shape[2], inp["k_cache"].shape[1]
     B, hq, _ = inp["q"].shape
@@ -292,6 +294,6 @@ def decode_ref(inp, scale, out_dtype, heads=None):
             S = abs(scale) * (np.abs(kh) @ np.abs(qh)).max()
             e_s = 11 * 2.0 ** -23 * S + 2.0 ** -25 * abs(scale) * np.abs(qh).max() * np.abs(kh).sum(axis=1).max()
             spread = (w @ np.abs(vh)) / l
-            tol[s, h] = ((2 * e_s + 2.0 ** -20 + (L / 32 + 80) * 2.0 ** -24) * spread + 2.0 ** -31 * np.abs(vh).sum(axis=0) / l)
+            tol[s, h] = ((2 * e_s + 2.0 ** -20 + (L / 32 + 80) * 2.0 ** -24) * spread + np.minimum(w, 2.0 ** -26) @ np.abs(vh) / l)
     tol += HALF[out_dtype] * np.abs(out) + TINY[out_dtype]
     return out, tol
