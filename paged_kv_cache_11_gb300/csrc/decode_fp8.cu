@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
             }
             if (lane < 4)
                 cp_async4(sa + 2 * kF8UnitBytes + 4 * lane, sbase + (int64_t)(lane < 2 ? id0 : id1) * p.num_kv_heads);
+            __syncwarp();
         }
         cp_async_commit();
     };
