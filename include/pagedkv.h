@@ -154,8 +154,8 @@ pkv_status paged_kv_append(const void* k, const void* v, const int64_t* slot_map
  * q_out:         [num_tokens][num_q_heads][head_dim], 16-byte aligned; may be
  *                q itself when q_stride is num_q_heads * head_dim, and must
  *                not overlap it otherwise, nor the k and v rows.
- * A token with a negative slot is padding: nothing of it is read, and its row
- * of q_out keeps its contents.  A slot past the pool is recorded as
+ * A token with a negative slot is padding: its position and its rows may hold
+ * anything, and its row of q_out keeps its contents.  A slot past the pool is recorded as
  * PKV_DEVERR_SLOT and a position outside [0, max_position) as
  * PKV_DEVERR_POSITION; such a token's K and V are not written and its q_out
  * row is zeros.  Two tokens with the same slot race (last writer undefined).

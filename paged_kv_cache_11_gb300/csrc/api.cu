@@ -514,7 +514,7 @@ static pkv_status append_rope_impl(const void* q, const void* k, const void* v, 
     if (!pool_fits(cache)) return PKV_ERR_INVALID_ARG;
     if (num_tokens == 0) return PKV_OK;
     const int64_t rows = (int64_t)rope->num_q_heads + 2 * (int64_t)cache->num_kv_heads;
-    if (num_tokens > ((int64_t)INT_MAX * 16) / rows) return PKV_ERR_INVALID_ARG;
+    if (num_tokens > (int64_t)INT_MAX / rows) return PKV_ERR_INVALID_ARG;  // rows are counted in 32 bits
     // bytes that each input spans; they must be addressable
     const int64_t qh = (int64_t)rope->num_q_heads * kHeadDim, kh = (int64_t)cache->num_kv_heads * kHeadDim;
     const int64_t most = INT64_MAX / 4 / num_tokens;
