@@ -33,6 +33,8 @@
 //      with 16 neighbouring dims of the output.
 // TMA copies would be 2 KiB each here, which the SM's TMA unit takes some 75
 // cycles for, 150 of the about 180 that a unit may cost at full bandwidth.
+#include <atomic>
+
 #include "decode_common.cuh"
 
 namespace pkv {
@@ -532,8 +534,17 @@ static cudaError_t launch_decode_fp8_t(const DecodeFp8Params& fp, cudaStream_t s
     const DecodeParams& p = fp.d;
     constexpr int kSmem = DecodeFp8Smem<8 * NH>::kTotal;
     auto kern = decode_fp8_kernel<NH>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    // the attribute is a device's and stays: set on the first call there
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(set.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        set |= bit;
+    }
     const unsigned heads = p.num_kv_heads * p.head_tiles;
     const dim3 grid = p.parts_in_x ? dim3(p.max_parts, heads, p.num_seqs) : dim3(heads, p.num_seqs, p.max_parts);
     e = launch_pdl(kern, grid, dim3(kF8Warps * 32), kSmem, stream, fp);
