@@ -160,7 +160,7 @@ pkv_status paged_kv_append(const void* k, const void* v, const int64_t* slot_map
  * PKV_DEVERR_POSITION; such a token's K and V are not written and its q_out
  * row is zeros.  Two tokens with the same slot race (last writer undefined).
  * num_tokens == 0 is a no-op.  Supported: head_dim 128, any block size, bf16
- * or fp16.
+ * or fp16, pools and tables of fewer than 2^31 slots and positions.
  */
 pkv_status paged_kv_append_rope(const void* q, const void* k, const void* v, const int64_t* positions,
                                 const float* cos_sin, const void* q_norm, const void* k_norm,

@@ -512,6 +512,8 @@ static pkv_status append_rope_impl(const void* q, const void* k, const void* v, 
     if (rope->q_stride % 8 != 0 || rope->k_stride % 8 != 0 || rope->v_stride % 8 != 0) return PKV_ERR_INVALID_ARG;
     if (cache->num_kv_heads > 65535 || rope->num_q_heads > 65535) return PKV_ERR_UNSUPPORTED;
     if (!pool_fits(cache)) return PKV_ERR_INVALID_ARG;
+    // slots and positions are held in 32 bits
+    if (cache->num_blocks > INT_MAX / cache->block_size || rope->max_position > INT_MAX) return PKV_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PKV_OK;
     const int64_t rows = (int64_t)rope->num_q_heads + 2 * (int64_t)cache->num_kv_heads;
     if (num_tokens > (int64_t)INT_MAX / rows) return PKV_ERR_INVALID_ARG;  // rows are counted in 32 bits
@@ -524,7 +526,7 @@ static pkv_status append_rope_impl(const void* q, const void* k, const void* v, 
         return PKV_ERR_INVALID_ARG;
     if (qh > 0 && (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16))) return PKV_ERR_INVALID_ARG;
     if (rope->rot_dim > 0 && (!positions || !cos_sin || !aligned(positions, 8) || !aligned(cos_sin, 16) ||
-                              rope->max_position < 1 || rope->max_position > INT64_MAX / 4 / kHeadDim))
+                              rope->max_position < 1))
         return PKV_ERR_INVALID_ARG;
     if (!aligned(q_norm, 16) || !aligned(k_norm, 16)) return PKV_ERR_INVALID_ARG;
     if (fp8 && (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4))) return PKV_ERR_INVALID_ARG;

@@ -10,7 +10,11 @@
 // turn needs no exchange, and its cosines and sines are one 16-byte load each.
 // The norm's sum of squares is the only exchange, over the 16 lanes.
 //
-// Bytes, not arithmetic, bound it: each row is read once and written once.
+// Bytes bound the 16-bit write: each row is read once and written once, 16384
+// normed tokens of 64/8 heads (671 MB) in 106.8 us, 6.4 TB/s.  The 8-bit write
+// waits on more: a block's scale needs all of its new rows before the first
+// byte, a chain of loads and exchanges for each run of tokens: 16384 tokens of
+// 32/8 heads (378 MB) in 70.5 us, 5.4 TB/s.
 #include <cuda_fp8.h>
 
 #include "pkv_internal.cuh"
@@ -160,49 +164,46 @@ __device__ __forceinline__ void store_row(uint16_t* row, const QuadPos& qp, cons
 }
 
 // What becomes of a token: padding, an error (recorded once by the caller), or
-// its slot and position.
+// its slot and position (32 bits hold both: the host refuses larger pools and
+// tables).
 struct Token {
-    int64_t slot, pos;
-    int err;  // PKV_DEVERR_*, 0: none
+    int slot, pos;  // slot -1: not in the pool
+    int err;        // PKV_DEVERR_*, 0: none
 };
 
 __device__ __forceinline__ Token token_at(const RopeParams& p, int64_t t) {
+    const int64_t slot = __ldg(p.slot_mapping + t);
+    const int64_t pos = p.rot_dim > 0 ? __ldg(p.positions + t) : 0;  // loaded beside the slot; padding's is not used
     Token k;
-    k.slot = __ldg(p.slot_mapping + t);
-    k.pos = p.rot_dim > 0 ? __ldg(p.positions + t) : 0;  // loaded beside the slot; padding's is not used
+    k.slot = (int)slot;
+    k.pos = (int)pos;
     k.err = 0;
-    if (k.slot >= p.num_slots)
+    if (slot >= p.num_slots) {
+        k.slot = -1;
         k.err = PKV_DEVERR_SLOT;
-    else if (k.slot >= 0 && p.rot_dim > 0 && (k.pos < 0 || k.pos >= p.max_position))
+    } else if (slot < 0) {
+        k.slot = -1;
+    } else if (p.rot_dim > 0 && (pos < 0 || pos >= p.max_position)) {
         k.err = PKV_DEVERR_POSITION;
+    }
     return k;
 }
 
-// slot -> (block, row); 32-bit arithmetic where the slot allows it
-__device__ __forceinline__ void split_slot(const RopeParams& p, int64_t slot, int64_t& blk, int& off) {
-    if (slot <= 0xffffffffll) {
-        const uint32_t b = (uint32_t)slot / (uint32_t)p.block_size;
-        blk = b;
-        off = (int)((uint32_t)slot - b * (uint32_t)p.block_size);
-    } else {
-        blk = slot / p.block_size;
-        off = (int)(slot - blk * p.block_size);
-    }
-}
-
-// kRowsPerUnit neighbouring head rows of one token and one kind (queries,
+// R neighbouring head rows of one token and one kind (queries,
 // keys or values), by one half-warp: the rows are loaded together, and share
 // the token's slot, angles and weights.  With an 8-bit pool (kQOnly) only the
-// queries are done here.
-constexpr int kRowsPerUnit = 4;
+// queries are done here.  R = 8 rows ask more of the memory at a time, 4 fill
+// the GPU with less work: 106.9 against 117.0 us for 16384 tokens of 64/8
+// heads, 16.1 against 15.8 us for 1537 of 40/40, 2.6 against 2.0 us for 64 of
+// 32/8.
+__host__ __device__ __forceinline__ uint32_t row_units(int heads, int R) { return (heads + R - 1) / R; }
+constexpr int64_t kManyUnits = 65536;  // units of 8 rows from which on R = 8
 
-__host__ __device__ __forceinline__ uint32_t row_units(int heads) { return (heads + kRowsPerUnit - 1) / kRowsPerUnit; }
-
-template <bool kBF16, bool kInter, bool kQOnly>
+template <bool kBF16, bool kInter, bool kQOnly, int R>
 __device__ __forceinline__ void do_rows(const RopeParams& p, uint32_t unit) {
     const int i = threadIdx.x & 15;
     const uint32_t half = 0xffffu << (threadIdx.x & 16);
-    const uint32_t uq = row_units(p.num_q_heads), uk = kQOnly ? 0 : row_units(p.num_kv_heads);
+    const uint32_t uq = row_units(p.num_q_heads, R), uk = kQOnly ? 0 : row_units(p.num_kv_heads, R);
     const uint32_t per_token = uq + 2 * uk;
     const uint32_t tt = unit / per_token;
     uint32_t c = unit - tt * per_token;
@@ -210,18 +211,19 @@ __device__ __forceinline__ void do_rows(const RopeParams& p, uint32_t unit) {
     if (t >= p.num_tokens) return;  // uniform over the half-warp
     const int kind = kQOnly || c < uq ? 0 : c < uq + uk ? 1 : 2;  // queries, keys, values
     c -= kind == 0 ? 0 : kind == 1 ? uq : uq + uk;
-    const int h0 = (int)c * kRowsPerUnit;
-    const int n = min(kRowsPerUnit, (kind == 0 ? p.num_q_heads : p.num_kv_heads) - h0);
+    const int h0 = (int)c * R;
+    const int n = min(R, (kind == 0 ? p.num_q_heads : p.num_kv_heads) - h0);
     const uint16_t* from = (kind == 0   ? p.q + t * p.q_stride
                             : kind == 1 ? p.k + t * p.k_stride
                                         : p.v + t * p.v_stride) +
                            h0 * kHeadDim;
-    const Token tok = token_at(p, t);
+    const int64_t slot = __ldg(p.slot_mapping + t);
+    const int64_t pos = p.rot_dim > 0 ? __ldg(p.positions + t) : 0;
     const QuadPos qp = quad_pos<kInter>(p, i);
     // the rows are loaded beside the slot and the position, not after them
-    uint2 ra[kRowsPerUnit], rb[kRowsPerUnit];
+    uint2 ra[R], rb[R];
 #pragma unroll
-    for (int r = 0; r < kRowsPerUnit; ++r)
+    for (int r = 0; r < R; ++r)
         if (r < n) {
             // read once, and q_out may be q: not through the read-only path
             ra[r] = *reinterpret_cast<const uint2*>(from + r * kHeadDim + qp.a);
@@ -230,11 +232,12 @@ __device__ __forceinline__ void do_rows(const RopeParams& p, uint32_t unit) {
     const uint16_t* wp = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
     Row weight;
     if (wp) weight = widen_row<kBF16>(ldg8(wp + qp.a), ldg8(wp + qp.b));
-    if (tok.slot < 0) return;
+    if (slot < 0) return;  // padding
     uint16_t* to = p.q_out + (t * p.num_q_heads + h0) * kHeadDim;
     int64_t to_step = kHeadDim;
-    if (tok.err) {
-        if (unit == tt * per_token && i == 0) record_error(p.err, tok.err);
+    const bool out = slot >= p.num_slots;
+    if (out || (p.rot_dim > 0 && (pos < 0 || pos >= p.max_position))) {
+        if (unit == tt * per_token && i == 0) record_error(p.err, out ? PKV_DEVERR_SLOT : PKV_DEVERR_POSITION);
         if (kind == 0)
             for (int r = 0; r < n; ++r) {
                 *reinterpret_cast<uint2*>(to + r * kHeadDim + qp.a) = make_uint2(0u, 0u);
@@ -243,17 +246,15 @@ __device__ __forceinline__ void do_rows(const RopeParams& p, uint32_t unit) {
         return;
     }
     if (!kQOnly && kind > 0) {
-        int64_t blk;
-        int off;
-        split_slot(p, tok.slot, blk, off);
+        const uint32_t blk = (uint32_t)slot / (uint32_t)p.block_size, off = (uint32_t)slot - blk * p.block_size;
         to_step = (int64_t)p.block_size * kHeadDim;
-        to = static_cast<uint16_t*>(kind == 1 ? p.k_cache : p.v_cache) + (blk * p.num_kv_heads + h0) * to_step +
+        to = static_cast<uint16_t*>(kind == 1 ? p.k_cache : p.v_cache) + ((int64_t)blk * p.num_kv_heads + h0) * to_step +
              off * kHeadDim;
     }
     if (kQOnly || kind < 2) {
-        const Turn turn = load_turn<kInter>(p, qp, tok.pos, i);
+        const Turn turn = load_turn<kInter>(p, qp, pos, i);
 #pragma unroll
-        for (int r = 0; r < kRowsPerUnit; ++r)
+        for (int r = 0; r < R; ++r)
             if (r < n) {
                 Row x = widen_row<kBF16>(ra[r], rb[r]);
                 norm_turn<kInter>(p, qp, wp != nullptr, weight, turn, half, x);
@@ -261,7 +262,7 @@ __device__ __forceinline__ void do_rows(const RopeParams& p, uint32_t unit) {
             }
     } else {  // values pass through as they are
 #pragma unroll
-        for (int r = 0; r < kRowsPerUnit; ++r)
+        for (int r = 0; r < R; ++r)
             if (r < n) {
                 *reinterpret_cast<uint2*>(to + r * to_step + qp.a) = ra[r];
                 *reinterpret_cast<uint2*>(to + r * to_step + qp.b) = rb[r];
@@ -271,16 +272,11 @@ __device__ __forceinline__ void do_rows(const RopeParams& p, uint32_t unit) {
 
 constexpr int kRopeThreads = 128;
 
-// Tokens per window of the 8-bit write: one while the warps are fewer than
-// this (a step's tokens each start a run of their own), then more, so that
-// few warps find nothing to start in a long chunk.
-constexpr int64_t kRunWarps = 4096;
-
-template <bool kBF16, bool kInter>
+template <bool kBF16, bool kInter, int R>
 __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const RopeParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    do_rows<kBF16, kInter, false>(p, (uint32_t)((blockIdx.x * (uint32_t)kRopeThreads + threadIdx.x) >> 4));
+    do_rows<kBF16, kInter, false, R>(p, blockIdx.x * (kRopeThreads / 16) + (threadIdx.x >> 4));
 }
 
 // ---------------------------------------------------------------- 8-bit pool
@@ -330,23 +326,23 @@ __device__ __forceinline__ void move_rows(uint8_t* tile, int first, float ratio,
 }
 
 // What a run's rows are written with: the block's scale for the largest
-// magnitude `a` of rows from row `first` on.  Raises the scale, and moves the
-// held rows, where the rule asks for it; returns the scale.  By a whole warp.
-__device__ __forceinline__ float settle_scale(const RopeParams& p, float* scale, uint8_t* tile, float a, int first,
-                                              int lane) {
-    float s = power_scale(a);
+// magnitude `a` of rows from row `first` on, `old` being the scale so far.  By
+// a whole warp; the one with `writes` sets the scale, and moves the held rows
+// where it is raised.
+__device__ __forceinline__ float settle_scale(const RopeParams& p, float* scale, float old, uint8_t* tile, float a,
+                                              int first, bool writes) {
+    const int lane = threadIdx.x & 31;
+    const float s = power_scale(a);
     if (first > 0) {
-        const float old = *scale;
         if (!(old > 0.f && finite(old))) {
-            if (lane == 0) record_error(p.err, PKV_DEVERR_SCALE);
+            if (writes && lane == 0) record_error(p.err, PKV_DEVERR_SCALE);
         } else if (a <= 448.f * old) {
             return old;
-        } else {
+        } else if (writes) {
             move_rows(tile, first, old / s, lane);
         }
     }
-    __syncwarp();
-    if (lane == 0) *scale = s;
+    if (writes && lane == 0) *scale = s;
     return s;
 }
 
@@ -383,18 +379,17 @@ __device__ __forceinline__ void infinite_to_nan(Row& x) {
     }
 }
 
-// A run of any shape (padding inside, refused tokens, a slot twice,
-// infinities among its values), of keys
-// (is_k) or values of KV head h, from its first token t0 on: two passes over
-// its tokens, the largest magnitudes, then the bytes.  The common runs take
-// write_run below.
+// A run of any shape (padding inside, refused tokens, a slot twice, infinities
+// among its values), of keys (is_k) or values of KV head h, from its first
+// token t0 on: two passes over its tokens, the largest magnitude, then the
+// bytes.  The common runs take write_run below.
 template <bool kBF16, bool kInter>
-__device__ __noinline__ void write_any_run(const RopeParams& p, int64_t t0, int64_t blk, int h, bool is_k) {
+__device__ __noinline__ void write_any_run(const RopeParams& p, int64_t t0, int blk, int h, bool is_k) {
     const int lane = threadIdx.x & 31, i = lane & 15, hf = lane >> 4;
     const uint32_t half = 0xffffu << (lane & 16);
     const QuadPos qp = quad_pos<kInter>(p, i);
     uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
-                    (blk * p.num_kv_heads + h) * p.block_size * kHeadDim;
+                    ((int64_t)blk * p.num_kv_heads + h) * p.block_size * kHeadDim;
     Row weight;
     if (p.k_norm) weight = widen_row<kBF16>(ldg8(p.k_norm + qp.a), ldg8(p.k_norm + qp.b));
     float a = 0.f;              // pass 0: the largest finite magnitude; pass 1: the reciprocal of the scale
@@ -402,11 +397,9 @@ __device__ __noinline__ void write_any_run(const RopeParams& p, int64_t t0, int6
     for (int pass = 0; pass < 2; ++pass) {
         for (int64_t c = t0; c < p.num_tokens; c += 32) {
             Token tok;
-            tok.slot = -1;
-            tok.pos = 0;
-            tok.err = 0;
+            tok.slot = -1, tok.pos = 0, tok.err = 0;
             if (c + lane < p.num_tokens) tok = token_at(p, c + lane);
-            const bool real = tok.slot >= 0 && tok.slot < p.num_slots;
+            const bool real = tok.slot >= 0;
             const bool mine = real && tok.slot / p.block_size == blk;
             const uint32_t other = __ballot_sync(0xffffffffu, real && !mine);
             const uint32_t before = other ? (1u << (__ffs(other) - 1)) - 1u : 0xffffffffu;
@@ -418,11 +411,11 @@ __device__ __noinline__ void write_any_run(const RopeParams& p, int64_t t0, int6
                 const int r1 = rows ? __ffs(rows) - 1 : -1;
                 rows &= rows - 1;
                 const int r = hf ? r1 : r0;
-                const int64_t slot = __shfl_sync(0xffffffffu, tok.slot, max(r, 0));
-                const int64_t pos = __shfl_sync(0xffffffffu, tok.pos, max(r, 0));
+                const int slot = __shfl_sync(0xffffffffu, tok.slot, max(r, 0));
+                const int pos = __shfl_sync(0xffffffffu, tok.pos, max(r, 0));
                 if (r >= 0) {  // uniform over the half-warp
                     const int64_t t = c + r;
-                    const int off = (int)(slot - blk * p.block_size);
+                    const int off = slot - blk * p.block_size;
                     const uint16_t* row =
                         is_k ? p.k + t * p.k_stride + h * kHeadDim : p.v + t * p.v_stride + h * kHeadDim;
                     Row x = widen_row<kBF16>(ldg8(row + qp.a), ldg8(row + qp.b));
@@ -446,196 +439,245 @@ __device__ __noinline__ void write_any_run(const RopeParams& p, int64_t t0, int6
         a = warp_max(a);
         first = __reduce_min_sync(0xffffffffu, first);
         if (first == p.block_size) return;  // every token of the run was refused
-        a = 1.f / settle_scale(p, (is_k ? p.k_scales : p.v_scales) + blk * p.num_kv_heads + h, tile, a, first, lane);
+        float* scale = (is_k ? p.k_scales : p.v_scales) + (int64_t)blk * p.num_kv_heads + h;
+        const float old = first > 0 ? *scale : 0.f;
+        __syncwarp();  // read by all before it is set
+        a = 1.f / settle_scale(p, scale, old, tile, a, first, true);
     }
 }
 
-// A run of `count` neighbouring tokens from t0 on, all of them good; `slot`
-// and `pos` are lane l's token t0 + l's.  False, and nothing written, where a
-// value is infinite.  Two passes over the rows, kPairs
-// pairs of them in flight at a time; the second finds them in the L1.  (All
-// rows of a run held in registers took 128 of them at 16 rows and 210 at 32,
-// which left too few warps to keep the memory busy.)
-template <bool kBF16, bool kInter, int BS>
-__device__ __forceinline__ bool write_run(const RopeParams& p, int64_t t0, int count, int64_t slot, int64_t pos,
-                                          int64_t blk, int h, bool is_k) {
-    constexpr int kPairs = 2;
-    const int lane = threadIdx.x & 31, i = lane & 15, hf = lane >> 4;
-    const uint32_t half = 0xffffu << (lane & 16);
+// A run of `count` <= BS neighbouring tokens from t0 on, all of them good, of
+// keys (kKeys) or values of KV head h; `off` and `pos` are lane l's token t0 +
+// l's row and position.  False, and nothing written, where a value is
+// infinite.
+//
+// A warp has 16 rows of a run at most.  They are copied to shared memory
+// (`stage`, the warp's own 8 KiB) together, turned there into 32-bit values,
+// which take the place of the rows, and become bytes once the largest
+// magnitude is known.  (Turning them twice cost 17 us more for 16384 tokens of
+// 8 KV heads; kept in registers they spilled; a CTA for each window, its runs'
+// magnitudes meeting in shared memory, took 61 us for keys and values against
+// 45.)  The two warps of a 32-row block meet at a barrier, `meet` is where they
+// leave their magnitudes.
+template <bool kBF16, bool kInter, bool kKeys, int BS>
+__device__ __forceinline__ bool write_run(const RopeParams& p, uint4* stage, float* meet, int64_t t0, int count,
+                                          int off_l, int pos_l, int first, int blk, int h) {
+    const int lane = threadIdx.x & 31, i = lane & 15, hf = lane >> 4, warp = threadIdx.x >> 5;
+    const int r0 = BS == 32 ? 16 * (warp & 1) : 0;  // the warp's first row
+    const int mine = min(count - r0, 16);           // its rows (none: <= 0)
     QuadPos qp = quad_pos<kInter>(p, i);
-    if (!is_k) qp.rotates = false;
-    const uint16_t* wp = is_k ? p.k_norm : nullptr;
+    if (!kKeys) qp.rotates = false, qp.a = 8 * i, qp.b = 8 * i + 4;
+    const int64_t stride = kKeys ? p.k_stride : p.v_stride;
+    const uint16_t* from = (kKeys ? p.k : p.v) + (t0 + r0 + hf) * stride + h * kHeadDim + 8 * i;
+    const uint32_t to = smem_addr(stage + lane);
+    __syncwarp();  // the warp is done with what the stage held
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (2 * j + hf < mine)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512 * j), "l"(from + 2 * j * stride)
+                         : "memory");
+    float* scale = (kKeys ? p.k_scales : p.v_scales) + (int64_t)blk * p.num_kv_heads + h;
+    const float old = first > 0 ? *scale : 0.f;
+    const bool norm = kKeys && p.k_norm;
     Row weight;
-    if (wp) weight = widen_row<kBF16>(ldg8(wp + qp.a), ldg8(wp + qp.b));
-    const int64_t stride = is_k ? p.k_stride : p.v_stride;
-    const uint16_t* from = (is_k ? p.k : p.v) + t0 * stride + h * kHeadDim;
-    uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
-                    (blk * p.num_kv_heads + h) * (int64_t)(BS * kHeadDim);
-    const int off_l = (int)(slot & (BS - 1));
-    const int first = __reduce_min_sync(0xffffffffu, lane < count ? off_l : BS);
-    float a = 0.f, inv = 0.f;
+    if (norm) weight = widen_row<kBF16>(ldg8(p.k_norm + qp.a), ldg8(p.k_norm + qp.b));
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();  // every lane has read `old`, too
+    // Pair j of rows lies in bytes 512j .. 512j + 511 of the stage, its 32-bit
+    // values go to 1024j .. 1024j + 1023: from the last pair down, over rows
+    // that are done.  An odd last row is done by both halves.
+    float a = 0.f;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll 1
-        for (int j0 = 0; j0 < count; j0 += 2 * kPairs) {
-            uint2 ra[kPairs], rb[kPairs];
-#pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-                const int r = j0 + 2 * j + hf;
-                if (r < count) {
-                    ra[j] = ldg8(from + r * stride + qp.a);
-                    rb[j] = ldg8(from + r * stride + qp.b);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-                if (j0 + 2 * j < count) {  // uniform over the warp
-                    const int r = j0 + 2 * j + hf, rr = min(r, count - 1);
-                    const int64_t ps = __shfl_sync(0xffffffffu, pos, rr);
-                    const int off = __shfl_sync(0xffffffffu, off_l, rr);
-                    if (r < count) {  // uniform over the half-warp
-                        Row x = widen_row<kBF16>(ra[j], rb[j]);
-                        const Turn turn = load_turn<kInter>(p, qp, ps, i);
-                        norm_turn<kInter>(p, qp, wp != nullptr, weight, turn, half, x);
-                        if (pass == 0)
-                            a = top(a, x);
-                        else
-                            store_e4m3(tile + off * kHeadDim, qp, x, inv);
-                    }
-                    __syncwarp();
-                }
-            }
+    for (int j = (mine - 1) >> 1; j >= 0; --j) {
+        const int r = min(2 * j + hf, mine - 1);
+        const uint16_t* row = reinterpret_cast<const uint16_t*>(stage) + r * kHeadDim;
+        Row y = widen_row<kBF16>(*reinterpret_cast<const uint2*>(row + qp.a),
+                                 *reinterpret_cast<const uint2*>(row + qp.b));
+        if constexpr (kKeys) {
+            const Turn turn = load_turn<kInter>(p, qp, __shfl_sync(0xffffffffu, pos_l, r0 + r), i);
+            norm_turn<kInter>(p, qp, norm, weight, turn, 0xffffffffu, y);
         }
-        if (pass == 0) {
-            a = warp_max(a);
-            if (a == INFINITY) return false;
-            inv = 1.f / settle_scale(p, (is_k ? p.k_scales : p.v_scales) + blk * p.num_kv_heads + h, tile, a, first,
-                                     lane);
-        }
+        a = top(a, y);
+        __syncwarp();
+        ulonglong2* at = reinterpret_cast<ulonglong2*>(stage + 64 * j + lane);
+        at[0] = make_ulonglong2(y.v[0], y.v[1]);
+        at[32] = make_ulonglong2(y.v[2], y.v[3]);
+        __syncwarp();
+    }
+    a = warp_max(a);
+    if constexpr (BS == 32) {
+        if (lane == 0) meet[warp & 1] = a;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+        a = fmaxf(meet[0], meet[1]);
+    }
+    if (a == INFINITY) return false;
+    uint8_t* tile = static_cast<uint8_t*>(kKeys ? p.k_cache : p.v_cache) +
+                    ((int64_t)blk * p.num_kv_heads + h) * (BS * kHeadDim);
+    const float inv = 1.f / settle_scale(p, scale, old, tile, a, first, r0 == 0);
+#pragma unroll 2
+    for (int j = 0; 2 * j < mine; ++j) {
+        const ulonglong2* at = reinterpret_cast<const ulonglong2*>(stage + 64 * j + lane);
+        const ulonglong2 lo = at[0], hi = at[32];
+        Row y;
+        y.v[0] = lo.x, y.v[1] = lo.y, y.v[2] = hi.x, y.v[3] = hi.y;
+        store_e4m3(tile + __shfl_sync(0xffffffffu, off_l, r0 + min(2 * j + hf, mine - 1)) * kHeadDim, qp, y, inv);
     }
     return true;
 }
 
-// The keys (is_k) or values of KV head h of the runs that start among the
-// tokens t0 .. t0 + window - 1, by one warp.  A run is the tokens of one
-// block, which stand together in slot_mapping but for padding.
+// The keys and values of some KV heads (items item0 .. item1 - 1, 32 at most:
+// item 2h is the keys of head h, 2h + 1 its values) of the runs that start
+// among the tokens t0 .. t0 + window - 1 (window <= 31), by one warp (BS = 16)
+// or two that go through it together.  A run is the tokens of one block, which
+// stand together in slot_mapping but for padding.  The warp looks at 64 tokens,
+// from the one before t0 on, so that a run ends among them (but for long
+// padding inside, or slots named twice).  The search takes 3 us of a call.
 template <bool kBF16, bool kInter, int BS>
-__device__ __forceinline__ void do_runs(const RopeParams& p, int64_t t0, int window, int h, bool is_k) {
+__device__ __forceinline__ void do_runs(const RopeParams& p, uint4* stage, float (*meet)[2], int64_t t0, int window,
+                                        int item0, int item1) {
     const int lane = threadIdx.x & 31;
-    const uint32_t below = (1u << lane) - 1u;
-    Token tok;
-    auto look = [&](int64_t t) {  // lane l's token t + l
-        tok.slot = -1;
-        tok.pos = 0;
-        tok.err = 0;
-        if (t + lane < p.num_tokens) tok = token_at(p, t + lane);
-    };
-    auto real = [&] { return tok.slot >= 0 && tok.slot < p.num_slots; };
-    const int64_t back = t0 - 1 - lane >= 0 ? __ldg(p.slot_mapping + (t0 - 1 - lane)) : -1;
-    look(t0);
-    if (lane < window && tok.slot >= p.num_slots && h == 0 && is_k) record_error(p.err, PKV_DEVERR_SLOT);
-    uint32_t in = __ballot_sync(0xffffffffu, real());
-    if (!(in & (window < 32 ? (1u << window) - 1u : 0xffffffffu))) return;
-    // the block of the last token in the pool before t0, over any padding
-    int64_t before = -1;
-    for (int64_t s = back, c = t0 - 1;;) {
-        const uint32_t m = __ballot_sync(0xffffffffu, s >= 0 && s < p.num_slots);
-        if (m) {
-            before = __shfl_sync(0xffffffffu, s, __ffs(m) - 1) / BS;
-            break;
-        }
-        c -= 32;
-        if (c < 0) break;
-        s = c - lane >= 0 ? __ldg(p.slot_mapping + (c - lane)) : -1;
+    const bool second = BS == 32 && ((threadIdx.x >> 5) & 1);  // the second warp of two: leaves the rest to the first
+    int turn = 0;                                              // which of the meeting places is next
+    Token tok[2];  // tokens t0 - 1 + lane and t0 + 31 + lane: bits lane and 32 + lane below
+    uint32_t in[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int64_t t = t0 - 1 + 32 * u + lane;
+        tok[u].slot = -1, tok[u].pos = 0, tok[u].err = 0;
+        if (t >= 0 && t < p.num_tokens) tok[u] = token_at(p, t);
     }
-    int64_t blk = tok.slot / BS;  // of tokens in the pool
-    const uint32_t prior = in & below;
-    const int64_t prev = __shfl_sync(0xffffffffu, blk, prior ? 31 - __clz(prior) : 0);
-    uint32_t leaders = __ballot_sync(0xffffffffu, lane < window && real() && blk != (prior ? prev : before));
-    int at = 0;  // the window in the registers starts at token t0 + at
-    while (leaders) {
-        const int l = __ffs(leaders) - 1;
-        leaders &= leaders - 1;
-        const int64_t b = __shfl_sync(0xffffffffu, blk, l - at);
-        uint32_t mine, other;
-        for (;;) {
-            mine = __ballot_sync(0xffffffffu, real() && blk == b);
-            other = __ballot_sync(0xffffffffu, real() && blk != b) & ~((1u << (l - at)) - 1u);
-            if (other || l == at) break;
-            // the run may go on past the window: start it at the run
-            at = l;
-            look(t0 + at);
-            blk = tok.slot / BS;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) in[u] = __ballot_sync(0xffffffffu, tok[u].slot >= 0);
+    if (tok[0].err == PKV_DEVERR_SLOT && lane >= 1 && lane <= window && item0 == 0 && !second)
+        record_error(p.err, PKV_DEVERR_SLOT);
+    const uint32_t inside = (2u << window) - 2u;
+    if (!(in[0] & inside)) return;
+    // the block of the last token in the pool before t0, over any padding
+    int before = __shfl_sync(0xffffffffu, tok[0].slot, 0) / BS;
+    if (!(in[0] & 1u)) {
+        before = -1;
+        for (int64_t c = t0 - 2; c >= 0; c -= 32) {
+            const int64_t s = c - lane >= 0 ? __ldg(p.slot_mapping + (c - lane)) : -1;
+            const uint32_t m = __ballot_sync(0xffffffffu, s >= 0 && s < p.num_slots);
+            if (m) {
+                before = __shfl_sync(0xffffffffu, (int)s, __ffs(m) - 1) / BS;
+                break;
+            }
         }
-        mine &= ~((1u << (l - at)) - 1u);
-        if (other) mine &= (1u << (__ffs(other) - 1)) - 1u;
-        const uint32_t run = mine >> (l - at);
-        const int count = __popc(run);
-        const bool good = __all_sync(0xffffffffu, !((mine >> lane) & 1u) || tok.err == 0);
-        // all tokens of the run are seen: another block follows, or none
-        // does, or every row of the block is there (more could only repeat)
-        const uint32_t rows =
-            __reduce_or_sync(0xffffffffu, (mine >> lane) & 1u ? 1u << (uint32_t)(tok.slot & (BS - 1)) : 0u);
-        const bool whole = other || t0 + at + 32 >= p.num_tokens || __popc(rows) == BS;
-        // tokens that follow one another, each to a row of its own
-        bool done = false;
-        if (good && whole && run == (count < 32 ? (1u << count) - 1u : 0xffffffffu) && __popc(rows) == count) {
-            const int src = min(lane + l - at, 31);
-            done = write_run<kBF16, kInter, BS>(p, t0 + l, count, __shfl_sync(0xffffffffu, tok.slot, src),
-                                        __shfl_sync(0xffffffffu, tok.pos, src), b, h, is_k);
+    }
+    uint32_t starts[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int blk = tok[u].slot / BS;
+        const uint32_t prior = in[u] & ((1u << lane) - 1u);
+        const int prev = __shfl_sync(0xffffffffu, blk, prior ? 31 - __clz(prior) : 0);
+        starts[u] = __ballot_sync(0xffffffffu, tok[u].slot >= 0 && blk != (prior ? prev : before) && (u || lane));
+        if (in[u]) before = __shfl_sync(0xffffffffu, blk, 31 - __clz(in[u]));
+    }
+    const uint64_t leaders = starts[0] | (uint64_t)starts[1] << 32, present = in[0] | (uint64_t)in[1] << 32;
+    for (uint32_t own = starts[0] & inside; own; own &= own - 1u) {
+        const int x = __ffs(own) - 1;
+        const uint64_t later = leaders & ~((2ull << x) - 1ull);
+        const uint64_t upto = later ? (later & (0ull - later)) - 1ull : ~0ull;  // bits below the next run's first
+        const uint64_t run = (present & upto) >> x;
+        const int count = __popcll(run);
+        // lane l: the run's token l
+        const int src = (x + lane) & 31;
+        const bool hi = x + lane >= 32;
+        const int sl0 = __shfl_sync(0xffffffffu, tok[0].slot, src), sl1 = __shfl_sync(0xffffffffu, tok[1].slot, src);
+        const int ps0 = __shfl_sync(0xffffffffu, tok[0].pos, src), ps1 = __shfl_sync(0xffffffffu, tok[1].pos, src);
+        const int er0 = __shfl_sync(0xffffffffu, tok[0].err, src), er1 = __shfl_sync(0xffffffffu, tok[1].err, src);
+        const bool good = __all_sync(0xffffffffu, lane >= count || (hi ? er1 : er0) == 0);
+        const int slot = hi ? sl1 : sl0, pos = hi ? ps1 : ps0, off = slot & (BS - 1);
+        const int blk = __shfl_sync(0xffffffffu, slot, 0) / BS;
+        uint32_t left = 0xffffffffu;  // items that write_any_run has to do
+        // neighbouring tokens, the run's end in sight
+        if (good && count <= BS && run == (1ull << count) - 1ull && (later || t0 + 63 >= p.num_tokens)) {
+            const int first = __reduce_min_sync(0xffffffffu, lane < count ? off : BS);
+#pragma unroll 1
+            for (int item = item0; item < item1; ++item) {
+                turn ^= 1;  // one meeting's barrier lies between two uses of a place
+                const bool done =
+                    (item & 1) ? write_run<kBF16, kInter, false, BS>(p, stage, meet[turn], t0 + x - 1, count, off, pos,
+                                                                     first, blk, item >> 1)
+                               : write_run<kBF16, kInter, true, BS>(p, stage, meet[turn], t0 + x - 1, count, off, pos,
+                                                                    first, blk, item >> 1);
+                if (done) left &= ~(1u << (item - item0));
+            }
         }
-        if (!done) write_any_run<kBF16, kInter>(p, t0 + l, b, h, is_k);
-        // a leader later in this window is found from its own slot again
-        if (leaders && at > 0) {
-            at = 0;
-            look(t0);
-            blk = tok.slot / BS;
-        }
+        for (int item = item0; item < item1; ++item)
+            if (((left >> (item - item0)) & 1u) && !second)
+                write_any_run<kBF16, kInter>(p, t0 + x - 1, blk, item >> 1, (item & 1) == 0);
     }
 }
 
-// kv_blocks of the CTAs write keys and values, a warp for each (window of
-// tokens, KV head, keys or values); the others turn the query heads.  The two
-// kinds are spread evenly over the grid: the first wait on a chain of loads
-// (slots, rows, the scale, rows again), the second stream, and side by side
-// they fill each other's pauses.  kv_rate = ceil(kv_blocks 2^32 / CTAs).
-template <bool kBF16, bool kInter, int BS>
-__global__ void __launch_bounds__(kRopeThreads) rope_fp8_kernel(const RopeParams p, uint64_t kv_rate, int window) {
+// kv_blocks of the CTAs write keys and values, a warp for each window of
+// tokens and `items` items; the others turn the query heads.  The two kinds
+// are spread evenly over the grid: the first wait on a chain of loads (slots,
+// rows and scale), the second stream, and side by side they fill each other's
+// pauses.  kv_rate = ceil(kv_blocks 2^32 / CTAs).
+template <bool kBF16, bool kInter, int BS, int R>
+__global__ void __launch_bounds__(kRopeThreads, BS == 16 ? 5 : 4)
+    rope_fp8_kernel(const RopeParams p, uint64_t kv_rate, int window, int items) {
+    __shared__ uint4 stage[kRopeThreads / 32][16 * kHeadDim / 4];  // 16 rows of 32-bit values for each warp
+    __shared__ float meet[kRopeThreads / 64][2][2];                // for each pair of warps
     pdl_launch_dependents();
     pdl_wait();
     const uint32_t kv = (uint32_t)((blockIdx.x * kv_rate) >> 32);  // CTAs of the first kind before this one
     if ((uint32_t)(((blockIdx.x + 1ull) * kv_rate) >> 32) > kv) {
-        const uint32_t w = (kv * (uint32_t)kRopeThreads + threadIdx.x) >> 5;
-        const uint32_t lanes = 2 * (uint32_t)p.num_kv_heads;
-        const uint32_t win = w / lanes, k = w - win * lanes;
+        const uint32_t w = kv * (kRopeThreads / (2 * BS)) + threadIdx.x / (2 * BS);  // one or two warps together
+        const uint32_t all = 2 * (uint32_t)p.num_kv_heads, per_window = (all + items - 1) / items;
+        const uint32_t win = w / per_window;
+        const int item0 = (int)((w - win * per_window) * items);
         const int64_t t0 = (int64_t)win * window;
-        if (t0 < p.num_tokens) do_runs<kBF16, kInter, BS>(p, t0, window, (int)(k >> 1), (k & 1u) == 0);
+        if (t0 < p.num_tokens)
+            do_runs<kBF16, kInter, BS>(p, stage[threadIdx.x >> 5], meet[threadIdx.x >> 6], t0, window, item0,
+                                       min(item0 + items, (int)all));
     } else {
-        do_rows<kBF16, kInter, true>(p, ((blockIdx.x - kv) * (uint32_t)kRopeThreads + threadIdx.x) >> 4);
+        do_rows<kBF16, kInter, true, R>(p, (blockIdx.x - kv) * (kRopeThreads / 16) + (threadIdx.x >> 4));
     }
 }
 
-template <bool kBF16, bool kInter>
+constexpr int64_t kRunWarps = 6080;  // warps for keys and values that a long call keeps (40 per SM)
+
+template <bool kBF16, bool kInter, int R>
 static cudaError_t launch_rope_append_t(const RopeParams& p, bool fp8, cudaStream_t stream) {
-    const int64_t units =
-        p.num_tokens * ((int64_t)row_units(p.num_q_heads) + (fp8 ? 0 : 2 * (int64_t)row_units(p.num_kv_heads)));
+    const int64_t units = p.num_tokens * ((int64_t)row_units(p.num_q_heads, R) +
+                                          (fp8 ? 0 : 2 * (int64_t)row_units(p.num_kv_heads, R)));
     const int64_t row_blocks = (units + kRopeThreads / 16 - 1) / (kRopeThreads / 16);
-    if (!fp8) return launch_pdl(rope_rows_kernel<kBF16, kInter>, dim3((unsigned)row_blocks), dim3(kRopeThreads), 0, stream, p);
-    int window = 1;
-    while (window < 16 && p.num_tokens * p.num_kv_heads / window > kRunWarps) window *= 2;
-    const int64_t warps = (p.num_tokens + window - 1) / window * 2 * p.num_kv_heads;
-    const int64_t kv_blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-    auto kern = p.block_size == 16 ? rope_fp8_kernel<kBF16, kInter, 16> : rope_fp8_kernel<kBF16, kInter, 32>;
+    if (!fp8)
+        return launch_pdl(rope_rows_kernel<kBF16, kInter, R>, dim3((unsigned)row_blocks), dim3(kRopeThreads), 0, stream,
+                          p);
+    // Few tokens: a warp for each token and item, so that every SM has some.
+    // Many: windows of a block, then items in one warp, which share the search
+    // for the runs and their angles, while kRunWarps are left: 16384 tokens of
+    // 8 KV heads took 80.0 us with 4096 warps, 73.3 with 8192, 777 tokens of
+    // 40 heads 20.0 with 7840, 26.1 with 15680.
+    const int64_t all = 2 * (int64_t)p.num_kv_heads, pair = p.block_size / 16;
+    int window = 1, items = 1;
+    const auto warps = [&](int w, int n) { return (p.num_tokens + w - 1) / w * ((all + n - 1) / n) * pair; };
+    while (window < 16 && warps(2 * window, 1) >= kRunWarps) window *= 2;
+    while (items < 32 && warps(window, 2 * items) >= kRunWarps) items *= 2;
+    const int64_t kv_blocks = (warps(window, items) + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    auto kern = p.block_size == 16 ? rope_fp8_kernel<kBF16, kInter, 16, R> : rope_fp8_kernel<kBF16, kInter, 32, R>;
     const uint64_t blocks = (uint64_t)(kv_blocks + row_blocks);
     const uint64_t kv_rate = (((uint64_t)kv_blocks << 32) + blocks - 1) / blocks;
-    return launch_pdl(kern, dim3((unsigned)blocks), dim3(kRopeThreads), 0, stream, p, kv_rate, window);
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(kRopeThreads), 0, stream, p, kv_rate, window, items);
+}
+
+template <bool kBF16, bool kInter>
+static cudaError_t launch_rope_append_r(const RopeParams& p, bool fp8, cudaStream_t stream) {
+    const int64_t rows = (int64_t)p.num_q_heads + (fp8 ? 0 : 2 * (int64_t)p.num_kv_heads);
+    return p.num_tokens * rows >= 8 * kManyUnits ? launch_rope_append_t<kBF16, kInter, 8>(p, fp8, stream)
+                                                 : launch_rope_append_t<kBF16, kInter, 4>(p, fp8, stream);
 }
 
 cudaError_t launch_rope_append(const RopeParams& p, int dtype, bool fp8, cudaStream_t stream, int* launches) {
-    const cudaError_t e =
-        dtype == PKV_BF16
-            ? (p.interleaved ? launch_rope_append_t<true, true>(p, fp8, stream) : launch_rope_append_t<true, false>(p, fp8, stream))
-            : (p.interleaved ? launch_rope_append_t<false, true>(p, fp8, stream) : launch_rope_append_t<false, false>(p, fp8, stream));
+    const bool bf16 = dtype == PKV_BF16;
+    const cudaError_t e = bf16 ? (p.interleaved ? launch_rope_append_r<true, true>(p, fp8, stream)
+                                                : launch_rope_append_r<true, false>(p, fp8, stream))
+                               : (p.interleaved ? launch_rope_append_r<false, true>(p, fp8, stream)
+                                                : launch_rope_append_r<false, false>(p, fp8, stream));
     if (e == cudaSuccess) ++*launches;
     return e;
 }
