@@ -11,7 +11,7 @@
 // The norm's sum of squares is the only exchange, over the 16 lanes.
 //
 // Bytes bound the 16-bit write: each row is read once and written once, 16384
-// normed tokens of 64/8 heads (671 MB) in 106.8 us, 6.4 TB/s.  The 8-bit write
+// normed tokens of 64/8 heads (680 MB) in 103.8 us, 6.5 TB/s.  The 8-bit write
 // waits on more: a block's scale needs all of its new rows before the first
 // byte, a chain of loads and exchanges for each run of tokens: 16384 tokens of
 // 32/8 heads (378 MB) in 70.5 us, 5.4 TB/s.
@@ -193,7 +193,7 @@ __device__ __forceinline__ Token token_at(const RopeParams& p, int64_t t) {
 // keys or values), by one half-warp: the rows are loaded together, and share
 // the token's slot, angles and weights.  With an 8-bit pool (kQOnly) only the
 // queries are done here.  R = 8 rows ask more of the memory at a time, 4 fill
-// the GPU with less work: 106.9 against 117.0 us for 16384 tokens of 64/8
+// the GPU with less work: 103.8 against 117.0 us for 16384 tokens of 64/8
 // heads, 16.1 against 15.8 us for 1537 of 40/40, 2.6 against 2.0 us for 64 of
 // 32/8.
 __host__ __device__ __forceinline__ uint32_t row_units(int heads, int R) { return (heads + R - 1) / R; }
@@ -273,7 +273,7 @@ __device__ __forceinline__ void do_rows(const RopeParams& p, uint32_t unit) {
 constexpr int kRopeThreads = 128;
 
 template <bool kBF16, bool kInter, int R>
-__global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, R == 8 ? 7 : 8) rope_rows_kernel(const RopeParams p) {
     pdl_launch_dependents();
     pdl_wait();
     do_rows<kBF16, kInter, false, R>(p, blockIdx.x * (kRopeThreads / 16) + (threadIdx.x >> 4));
@@ -514,7 +514,7 @@ __device__ __forceinline__ bool write_run(const RopeParams& p, uint4* stage, flo
     uint8_t* tile = static_cast<uint8_t*>(kKeys ? p.k_cache : p.v_cache) +
                     ((int64_t)blk * p.num_kv_heads + h) * (BS * kHeadDim);
     const float inv = 1.f / settle_scale(p, scale, old, tile, a, first, r0 == 0);
-#pragma unroll 2
+#pragma unroll 1
     for (int j = 0; 2 * j < mine; ++j) {
         const ulonglong2* at = reinterpret_cast<const ulonglong2*>(stage + 64 * j + lane);
         const ulonglong2 lo = at[0], hi = at[32];
