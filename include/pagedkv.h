@@ -291,10 +291,13 @@ pkv_status paged_attention_decode(const void* q, const void* k_cache, const void
  *            finite values, powers of two or not.  Those of blocks outside
  *            the sequences' contexts are never read.
  * cache->dtype is PKV_E4M3.  The other arguments, the workspace
- * (paged_attention_workspace_bytes), the split of the work
- * (paged_attention_plan), the errors and the limits are those of
- * paged_attention_decode.  The values enter the products exactly (as 16-bit
- * floats), the scales as 32-bit factors of the sums.
+ * (paged_attention_workspace_bytes), the errors and the limits are those of
+ * paged_attention_decode.  partition_size is the most tokens of a split-K
+ * partition: a sequence with more is cut into as few equal parts as that
+ * allows; 0 chooses as paged_attention_decode does, counting this kernel's own
+ * resident CTAs, so paged_attention_plan and paged_attention_partition_size
+ * need not agree.  The values enter the products exactly (as 16-bit floats),
+ * the scales as 32-bit factors.
  */
 pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
                                       const float* k_scales, const float* v_scales, const int32_t* block_tables,

@@ -181,9 +181,10 @@ static int sm_count() {
 // max_context_len) still fill the GPU's resident decode CTAs at least twice;
 // longer partitions amortise each CTA's start-up, shorter ones balance the
 // load.  The workspace is always sized for 512 (the smallest choice).
-static int resolve_partition(int32_t partition_size, int64_t rows, int32_t max_context_len) {
+static int resolve_partition(int32_t partition_size, int64_t rows, int32_t max_context_len,
+                             int ctas_per_sm = kDecodeCtasPerSm) {
     if (partition_size != 0) return partition_size;
-    const int64_t slots = (int64_t)(sm_count() > 0 ? sm_count() : 148) * kDecodeCtasPerSm;
+    const int64_t slots = (int64_t)(sm_count() > 0 ? sm_count() : 148) * ctas_per_sm;
     int best = kAutoPartition;
     for (int P = 1024; P <= 4096; P *= 2) {
         const int64_t units = rows * (((int64_t)max_context_len + P - 1) / P);
@@ -214,10 +215,10 @@ struct Plan {
 };
 
 static Plan make_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t head_tiles, int32_t max_context_len,
-                      int32_t partition_size) {
+                      int32_t partition_size, int ctas_per_sm = kDecodeCtasPerSm) {
     Plan pl;
     const int64_t groups = (int64_t)num_seqs * num_kv_heads * head_tiles;  // (sequence, head group) rows
-    pl.partition = resolve_partition(partition_size, groups, max_context_len);
+    pl.partition = resolve_partition(partition_size, groups, max_context_len, ctas_per_sm);
     pl.max_parts = max_context_len == 0 ? 1 : (max_context_len + pl.partition - 1) / pl.partition;
     if (pl.max_parts <= 1)
         pl.kind = PKV_PLAN_SINGLE;
@@ -624,7 +625,8 @@ pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
         !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
         return PKV_ERR_INVALID_ARG;
-    const Plan pl = make_plan(num_seqs, cache->num_kv_heads, head_tiles, max_context_len, partition_size);
+    const Plan pl = make_plan(num_seqs, cache->num_kv_heads, head_tiles, max_context_len, partition_size,
+                              kDecodeFp8CtasPerSm);
     const bool split = pl.kind != PKV_PLAN_SINGLE;
     const size_t need =
         paged_attention_workspace_bytes(num_seqs, num_q_heads, kHeadDim, max_context_len, partition_size);
@@ -638,6 +640,7 @@ pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void
     fp.k_scales = k_scales;
     fp.v_scales = v_scales;
     fp.q_bf16 = q_dtype == PKV_BF16;
+    fp.block_bytes = (int64_t)cache->num_kv_heads * cache->block_size * kHeadDim;
     DecodeParams& p = fp.d;
     p.q = q;
     p.block_tables = block_tables;

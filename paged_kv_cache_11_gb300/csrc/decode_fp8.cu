@@ -41,7 +41,7 @@ namespace pkv {
 
 constexpr int kF8Warps = 4;             // warps per CTA, each with a ring of its own
 constexpr int kF8Stages = 2;            // pairs of units: one in use, the others in flight
-constexpr int kF8CtasPerSm = 3;
+constexpr int kF8CtasPerSm = kDecodeFp8CtasPerSm;
 constexpr float kF8Lift = 7.f;          // log2; kLazyMargin + kF8Lift stays below fp16's 2^16
 constexpr int kF8UnitBytes = 2 * 16 * kHeadDim;       // 16 tokens of K and V
 constexpr int kF8StageBytes = 2 * kF8UnitBytes + 16;  // two units and their scales: ks, vs, ks, vs
@@ -118,8 +118,13 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
         for (int i = tid; i < rows * D; i += blockDim.x) store_out(p, s, h0 + i / D, i % D, 0.f);
         return;
     }
-    const int tok0 = part * p.partition_size;
-    const int len = min(L - tok0, p.partition_size);  // tokens of this partition
+    // The row's blocks in nparts even parts: no part is longer than
+    // partition_size, and none is a short rest that leaves the others waiting.
+    // (part < nparts, and nparts - 1 full parts hold less than the row, so
+    // every part has a token.)
+    const int per = (((L - 1) / p.block_size + nparts) / nparts) * p.block_size;
+    const int tok0 = part * per;
+    const int len = min(L - tok0, per);  // tokens of this part
     const int npairs = (len + 31) / 32;
     const bool whole = p.block_size == 32;  // a pair is one block (else two)
     const bool write_partial = p.split && nparts > 1;
@@ -133,7 +138,6 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks_per_seq + tok0 / p.block_size;
     const int nblk = (len - 1) / p.block_size + 1;  // blocks of this partition
     const uint64_t policy = l2_policy_evict_first();
-    const int64_t tile_bytes = (int64_t)p.block_size * D;
     uint8_t* ring = smem + warp * (NST * kF8StageBytes);
     const uint32_t ring_sa = smem_addr(ring);
 
@@ -160,12 +164,9 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     // A copy instruction brings four whole rows; lane l has chunk l % 8 of row
     // l / 8.  Chunk c of row r goes to chunk c ^ (r % 8) of its row in shared
     // memory, which keeps the reads below free of bank conflicts.
-    const uint8_t* kbase = fp.k8 + kvh * tile_bytes + lane * 16;
-    const uint8_t* vbase = fp.v8 + kvh * tile_bytes + lane * 16;
+    const int own = kvh * (p.block_size * D) + lane * 16;  // of the KV head's tile in a block, and of the lane in it
     const int r8 = lane >> 3, put = (lane >> 3) * D;
     const uint32_t put0 = put + (((lane & 7) ^ r8) << 4), put1 = put + (((lane & 7) ^ (r8 + 4)) << 4) + 4 * D;
-    const float* sbase = ((lane & 1) ? fp.v_scales : fp.k_scales) + kvh;
-    const int64_t block_bytes = p.num_kv_heads * tile_bytes;
     const int second = whole ? 16 * D : 0;  // where a pair's second unit starts in its block
     auto issue = [&](int n, int st) {       // pair n into stage st
         if (n < mine) {
@@ -174,9 +175,9 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
             const uint32_t sa = ring_sa + st * kF8StageBytes;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int64_t off = (u ? id1 : id0) * block_bytes + (u ? second : 0);
-                const uint8_t* kr = kbase + off;
-                const uint8_t* vr = vbase + off;
+                const int64_t off = (u ? id1 : id0) * fp.block_bytes + (own + (u ? second : 0));
+                const uint8_t* kr = fp.k8 + off;
+                const uint8_t* vr = fp.v8 + off;
                 const uint32_t dst = sa + u * kF8UnitBytes;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {  // rows 8i .. 8i + 7 of K and of V
@@ -187,7 +188,8 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
                 }
             }
             if (lane < 4)
-                cp_async4(sa + 2 * kF8UnitBytes + 4 * lane, sbase + (int64_t)(lane < 2 ? id0 : id1) * p.num_kv_heads);
+                cp_async4(sa + 2 * kF8UnitBytes + 4 * lane, ((lane & 1) ? fp.v_scales : fp.k_scales) +
+                                                                (int64_t)(lane < 2 ? id0 : id1) * p.num_kv_heads + kvh);
             __syncwarp();
         }
         cp_async_commit();

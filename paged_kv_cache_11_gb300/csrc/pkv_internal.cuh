@@ -17,6 +17,7 @@ namespace pkv {
 constexpr int kHeadDim = 128;          // supported head_dim
 constexpr int kAutoPartition = 512;    // smallest automatic split-K partition (tokens)
 constexpr int kDecodeCtasPerSm = 5;    // resident decode CTAs per SM the kernel is tuned for
+constexpr int kDecodeFp8CtasPerSm = 3; // and of the 8-bit decode kernel
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bound on any in-CTA wait (2 s)
 // Split-K calls with at most this many partitions per sequence merge inside
 // the decode kernel (the last partition to finish merges); longer ones use
@@ -204,6 +205,7 @@ struct DecodeFp8Params {
     const uint8_t* v8;
     const float* k_scales;       // [num_blocks][num_kv_heads]
     const float* v_scales;
+    int64_t block_bytes;         // of one block of one cache
     int q_bf16;                  // q is bf16 (else fp16)
 };
 cudaError_t launch_decode_fp8(const DecodeFp8Params& p, cudaStream_t stream, int* launches);
