@@ -8,6 +8,7 @@ no fallback of any kind.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import operator
 from pathlib import Path
@@ -87,7 +88,7 @@ def _lib() -> ctypes.CDLL:
     lib.paged_attention_decode_fp8.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, ctypes.c_float,
                                                vp, i32, desc_p, i32, vp, sz, vp]
     lib.paged_attention_decode_fp8.restype = ctypes.c_int
-    lib.copy_blocks_fp8.argtypes = [ctypes.POINTER(vp)] * 4 + [i32, vp, i32, desc_p, vp]
+    lib.copy_blocks_fp8.argtypes = [vp, vp, vp, vp, i32, vp, i32, desc_p, vp]
     lib.copy_blocks_fp8.restype = ctypes.c_int
     lib.paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     lib.paged_attention_workspace_bytes.restype = sz
@@ -593,9 +594,9 @@ def copy_blocks_fp8(k_caches: torch.Tensor | Sequence[torch.Tensor], v_caches: t
     _require(set(map(_numel, scales)) == {desc.num_blocks * desc.num_kv_heads} and
              set(map(_dtype_of, scales)) == {_F32}, "scales must be fp32 [num_blocks, num_kv_heads]")
     _require(src_dst_pairs.dtype == _I64 and src_dst_pairs.numel() % 2 == 0, "src_dst_pairs must be int64 [n, 2]")
-    ptrs = ctypes.c_void_p * n
-    addr = list(map(torch.Tensor.data_ptr, caches + scales))
-    _check(_lib().copy_blocks_fp8(*[ptrs(*addr[i:i + n]) for i in range(0, 4 * n, n)], n, src_dst_pairs.data_ptr(),
+    ptrs = array.array("Q", map(torch.Tensor.data_ptr, caches + scales))  # the four host arrays, one after the other
+    at, step = ptrs.buffer_info()[0], n * ptrs.itemsize
+    _check(_lib().copy_blocks_fp8(at, at + step, at + 2 * step, at + 3 * step, n, src_dst_pairs.data_ptr(),
                                   src_dst_pairs.numel() // 2, desc, _raw_stream(dev)), "copy_blocks_fp8")
 
 

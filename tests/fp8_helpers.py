@@ -183,7 +183,7 @@ class Case:
                     # the choices below must not hang on the last bits of a
                     for edge in ([448 * old] if first and usable else []) + [448 * p2_scale(a), 224 * p2_scale(a)]:
                         exact = which == "v" or not (self.rot or self.k_norm is not None)
-                        assert exact or a == 0 or abs(a / edge - 1) > 2.0 ** -18
+                        assert exact or a in (0, edge) or abs(a / edge - 1) > 2.0 ** -18  # (equal: a value that is not turned)
                     if first and usable and a <= 448 * old:
                         s = old
                     else:
@@ -294,6 +294,7 @@ def decode_ref(inp, scale, out_dtype, heads=None):
             S = abs(scale) * (np.abs(kh) @ np.abs(qh)).max()
             e_s = 11 * 2.0 ** -23 * S + 2.0 ** -25 * abs(scale) * np.abs(qh).max() * np.abs(kh).sum(axis=1).max()
             spread = (w @ np.abs(vh)) / l
-            tol[s, h] = ((2 * e_s + 2.0 ** -20 + (L / 32 + 80) * 2.0 ** -24) * spread + np.minimum(w, 2.0 ** -26) @ np.abs(vh) / l)
+            tol[s, h] = ((2 * e_s + 2.0 ** -20 + (L / 32 + 80) * 2.0 ** -24) * spread +
+                         np.minimum(w, 2.0 ** -26) @ np.abs(vh) / l)
     tol += HALF[out_dtype] * np.abs(out) + TINY[out_dtype]
     return out, tol

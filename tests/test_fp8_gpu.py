@@ -143,6 +143,41 @@ def test_nan_in_the_context_comes_through(gpu):
             assert not out[0, :4].isnan().any() and not out[1].isnan().any()
 
 
+def test_queries_that_are_not_finite(gpu):
+    """A head whose query holds a NaN or an infinity is NaN; the other heads of its group are not touched."""
+    for bad in (math.nan, math.inf, -math.inf):
+        for P in (0, 64, 16):
+            inp = decode_inputs(25, (400, 30), 8, 2, 16, BF)
+            clean = pkv.paged_attention_decode_fp8(**_dev(inp, gpu), scale=SCALE, partition_size=P)
+            inp["q"][0, 5, 17] = bad
+            out = pkv.paged_attention_decode_fp8(**_dev(inp, gpu), scale=SCALE, partition_size=P)
+            assert out[0, 5].isnan().all()
+            keep = torch.ones(2, 8, dtype=torch.bool)
+            keep[0, 5] = False
+            assert torch.equal(out.cpu()[keep], clean.cpu()[keep])
+
+
+@pytest.mark.parametrize("scale", [0.0, -SCALE, 2.0])
+def test_softmax_scales(gpu, scale):
+    _check(decode_inputs(26, (300, 17), 8, 2, 32, FP), gpu, scale=scale)
+    _check(decode_inputs(26, (300, 17), 8, 2, 32, FP), gpu, scale=scale, partition_size=32)
+
+
+def test_tables_wider_than_the_contexts(gpu):
+    """max_context_len far above the lengths: most partitions have nothing, entries past a context are never read."""
+    inp = decode_inputs(27, (40, 700, 0), 8, 2, 16, BF)
+    wide = torch.full((3, 2000), 2 ** 31 - 1, dtype=torch.int32)
+    for s, L in enumerate((40, 700, 0)):
+        n = -(-L // 16)
+        wide[s, :n] = inp["block_tables"][s, :n]
+    ref = _check(inp, gpu, partition_size=512)
+    out = pkv.paged_attention_decode_fp8(**{**_dev(inp, gpu), "block_tables": wide.to(gpu)}, scale=SCALE,
+                                         partition_size=512)
+    assert pkv.check_device_error() == 0
+    assert (out - ref).abs().max().item() <= 2.0 ** -18    # merged by the other kernel: another order of sums
+    _check({**inp, "block_tables": wide}, gpu)
+
+
 def test_physical_order_is_invisible(gpu):
     a = decode_inputs(12, (700, 90, 333), 8, 2, 16, BF)
     nb = a["k_cache"].shape[0]

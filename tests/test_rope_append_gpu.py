@@ -219,6 +219,47 @@ def test_broadcast_rows(gpu):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_one_of_the_norms(gpu, which, fp8):
+    slots, pos = runs_of_tokens(np.random.default_rng(2), [(0, 20), (7, 3)], 16, 6)
+    c = Case(34, 4, 2, 16, BF, 128, False, True, slots, pos, 6, fp8=fp8)
+    setattr(c, "k_norm" if which == "q" else "q_norm", None)
+    _check(c, gpu)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bs", [16, 32])
+def test_long_ragged_batches(gpu, bs, fp8):
+    """Enough tokens for windows of 16 tokens and several heads per warp, with runs of every length and offset."""
+    rng = np.random.default_rng(bs)
+    spans = [(int(rng.integers(0, 60)), int(n)) for n in rng.integers(1, 3 * bs, 60)]
+    slots, pos = runs_of_tokens(rng, spans, bs, 400)
+    c = Case(35 + bs, 0, 3, bs, BF, 32, False, False, slots, pos, 400, fp8=fp8)
+    _check(c, gpu)
+    # many more tokens than the checked ones, in front of them: the same rows give the same bytes
+    n, reps = len(slots), 8
+    d = c.to_dev(gpu)
+    big = {}
+    for x in ("k", "v", "positions", "slot_mapping"):
+        t = d[x]
+        big[x] = torch.cat([t] * reps, dim=0) if x != "slot_mapping" else torch.cat(
+            [t + i * 400 * bs for i in range(reps)])
+    for x in ("k_cache", "v_cache", "k_scales", "v_scales"):
+        if x in d:
+            t = d[x].view(torch.uint8) if d[x].dtype == torch.float8_e4m3fn else d[x]
+            big[x] = torch.cat([t] * reps, dim=0).view(d[x].dtype)
+    fn = pkv.paged_kv_append_rope_fp8 if fp8 else pkv.paged_kv_append_rope
+    fn(**{**d, **big})
+    fn(**d)
+    assert pkv.check_device_error() == 0 and n * reps > 8 * bs
+    for x in ("k_cache", "v_cache", "k_scales", "v_scales"):
+        if x in d:
+            raw = (lambda t: t.view(torch.uint8) if t.element_size() == 1 else t)
+            for i in range(reps):
+                assert torch.equal(raw(big[x])[400 * i:400 * (i + 1)], raw(d[x])), (x, i)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_far_positions(gpu, fp8):
     """Positions up to 131071: the angle is the table's, so nothing is lost on the way to them."""
     slots, _ = runs_of_tokens(np.random.default_rng(2), [(0, 8)], 16, 2)
