@@ -83,7 +83,7 @@ enum {
     PKV_DEVERR_GROUP = 7,       /* grouped decode: group_starts out of order or range, or a sequence
                                    with a shared prefix in no group or beyond max_group_size members */
     PKV_DEVERR_POSITION = 8,    /* append_rope: positions[t] outside [0, max_position) */
-    PKV_DEVERR_SCALE = 9        /* append_rope_fp8: rows join a block whose scale is not a positive finite number */
+    PKV_DEVERR_SCALE = 9        /* append_rope_fp8: rows join a block whose scale is not finite and at least 2^-126 */
 };
 
 /* Shape of one layer's paged cache (host struct, read during the call). */
@@ -179,9 +179,9 @@ pkv_status paged_kv_append_rope(const void* q, const void* k, const void* v, con
  *   - otherwise the rows join those that the block holds: the scale is kept
  *     while a <= 448 * scale; else it becomes P(a), and the rows below the
  *     first written one are moved to it, each value rounded once to the
- *     nearest e4m3 value of b * (old / new).  A scale that is not a positive
- *     finite number is recorded as PKV_DEVERR_SCALE and replaced by P(a),
- *     with the held bytes left as they are.
+ *     nearest e4m3 value of b * (old / new).  A scale that is not a finite
+ *     number of at least 2^-126 is recorded as PKV_DEVERR_SCALE and replaced
+ *     by P(a), with the held bytes left as they are.
  * The new rows are stored as the nearest e4m3 values of y / scale, ties to
  * even; infinities and NaN are stored as NaN.  A scale that is a power of two
  * loses nothing when it is applied and keeps the relative precision of e4m3

@@ -334,7 +334,7 @@ __device__ __forceinline__ float settle_scale(const RopeParams& p, float* scale,
     const int lane = threadIdx.x & 31;
     const float s = power_scale(a);
     if (first > 0) {
-        if (!(old > 0.f && finite(old))) {
+        if (!(old >= 0x1p-126f && finite(old))) {  // (a smaller one has no finite reciprocal)
             if (writes && lane == 0) record_error(p.err, PKV_DEVERR_SCALE);
         } else if (a <= 448.f * old) {
             return old;

@@ -179,7 +179,7 @@ class Case:
                     first = min(rows)
                     a = max([np.abs(y[np.isfinite(y)]).max() for y, _ in rows.values() if np.isfinite(y).any()] or [0.0])
                     old = old_s[b, h]
-                    usable = 0 < old < np.inf
+                    usable = 2.0 ** -126 <= old < np.inf
                     # the choices below must not hang on the last bits of a
                     for edge in ([448 * old] if first and usable else []) + [448 * p2_scale(a), 224 * p2_scale(a)]:
                         exact = which == "v" or not (self.rot or self.k_norm is not None)

@@ -150,11 +150,17 @@ def test_scales_that_are_no_powers_of_two(gpu):
 
 def test_unusable_scales_are_recorded_and_replaced(gpu):
     pkv.check_device_error()
-    for bad in (float("nan"), 0.0, -1.0, float("inf"), -float("inf")):
+    for bad in (float("nan"), 0.0, -1.0, float("inf"), -float("inf"), 2.0 ** -127):
         slots, pos = runs_of_tokens(np.random.default_rng(1), [(5, 3), (0, 4)], 16, 4)
         c = Case(23, 2, 1, 16, BF, 128, False, False, slots, pos, 4, fp8=True)
         c.ks.fill_(bad)
         _check(c, gpu, expect=9)
+    c = Case(23, 2, 1, 16, BF, 128, False, False, slots[:3], pos[:3], 4, fp8=True)
+    c.ks.fill_(2.0 ** -126)                                           # the smallest that counts: raised by the first row
+    c.vs.fill_(2.0 ** -126)
+    _check(c, gpu)
+    c.rows.zero_()                                                    # and kept by rows of zeros
+    _check(c, gpu)
     c = Case(23, 2, 1, 16, BF, 128, False, False, slots[3:], pos[3:], 4, fp8=True)
     c.ks.fill_(float("nan"))                                          # a fresh block never reads its scale
     c.vs.fill_(0.0)
