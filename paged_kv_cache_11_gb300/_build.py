@@ -3,6 +3,8 @@
 * ``libpagedkv.so`` -- the CUDA library behind ``include/pagedkv.h``, compiled
   for sm_103a only (``-gencode arch=compute_103a,code=sm_103a``); the
   translation units compile in parallel and link with the static CUDA runtime.
+* ``_marshal.so`` -- the binding's argument marshalling for the calls on
+  rotated rows and 8-bit pools (C++ against the installed torch).
 * ``libpkvgen.so`` -- the seeded input generator (plain C, no CUDA).
 
 Nothing here runs at import time: ``paged_kv_cache_11_gb300`` loads the
@@ -13,6 +15,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -50,6 +53,14 @@ def _stale(target: Path, deps: list[Path]) -> bool:
 
 def build_library(force: bool = False, verbose: bool = False) -> Path:
     LIBDIR.mkdir(exist_ok=True)
+    with ThreadPoolExecutor(1) as ex:  # beside the library's own compilation
+        marshal = ex.submit(build_marshal, force)
+        out = _build_cuda(force, verbose)
+        marshal.result()
+    return out
+
+
+def _build_cuda(force: bool, verbose: bool) -> Path:
     out = LIBDIR / "libpagedkv.so"
     deps = [CSRC / s for s in CUDA_SOURCES] + [CSRC / "pkv_internal.cuh", CSRC / "decode_common.cuh",
                                                 PKG.parent / "include" / "pagedkv.h"]
@@ -65,6 +76,24 @@ def build_library(force: bool = False, verbose: bool = False) -> Path:
                     zip(CUDA_SOURCES, objs)))
     tmp = out.with_suffix(".so.tmp")
     _run([nvcc, *ARCH, "-shared", "-o", str(tmp), *map(str, objs)])
+    os.replace(tmp, out)
+    return out
+
+
+def build_marshal(force: bool = False) -> Path:
+    import torch
+    src = CSRC / "marshal.cpp"
+    out = LIBDIR / "_marshal.so"
+    if not force and not _stale(out, [src, PKG.parent / "include" / "pagedkv.h"]):
+        return out
+    home = Path(torch.__file__).resolve().parent
+    inc = [sysconfig.get_paths()["include"], home / "include", home / "include" / "torch" / "csrc" / "api" / "include",
+           Path(_nvcc()).parent.parent / "include"]
+    tmp = out.with_suffix(".so.tmp")
+    _run(["g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in inc], str(src), "-o",
+          str(tmp), f"-L{home / 'lib'}", f"-Wl,-rpath,{home / 'lib'}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+          "-lc10", "-lc10_cuda", "-ldl"])
     os.replace(tmp, out)
     return out
 

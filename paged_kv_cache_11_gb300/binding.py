@@ -8,9 +8,9 @@ no fallback of any kind.
 """
 from __future__ import annotations
 
-import array
 import ctypes
-import operator
+import importlib.machinery
+import importlib.util
 from pathlib import Path
 from typing import Sequence
 
@@ -183,99 +183,39 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor
                                   _ptr(v_cache), ctypes.byref(desc), _stream(stream)), "paged_kv_append")
 
 
-# A step's calls are short against the GPU's work: the checks below read each property of a tensor once.
-_get_device, _is_contiguous, _numel = torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.numel
-_dtype_of = operator.attrgetter("dtype")
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_MARSHAL = None
 
 
-def _one_device(tensors) -> int:
-    """The index of the CUDA device that all the tensors are on, each of them contiguous."""
-    devs = set(map(_get_device, tensors))
-    dev = devs.pop()
-    if devs or dev < 0:
-        raise ValueError("tensors must be on one CUDA device")
-    if not all(map(_is_contiguous, tensors)):
-        raise ValueError("tensors must be contiguous")
-    return dev
+def _marshal():
+    """The compiled marshalling of the calls below (csrc/marshal.cpp), bound to the library."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        path = LIB_PATH.parent / "_marshal.so"
+        if not path.exists():
+            raise RuntimeError(f"{path} is not built; run `python -m paged_kv_cache_11_gb300._build` first")
+        _lib()
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", str(path))
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+        loader.exec_module(mod)
+        mod.bind(str(LIB_PATH))
+        _MARSHAL = mod
+    return _MARSHAL
 
 
-def _context(dev: int, stream):
-    """What a call runs in where its device is not the current one or a stream is given: the device is current, and
-    the call's allocations belong to the stream it launches on, so that none is handed out again while it still runs."""
+def _call(name: str, stream, first: torch.Tensor, fn, *args):
+    """fn(*args), on ``stream`` (None: the tensors' device's current stream).  Within a given stream the call's
+    allocations belong to it too: none is handed out again while the call still runs."""
     if stream is None:
-        return torch.cuda.device(dev)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    _require(stream.device.index == dev, "stream belongs to another device")
-    return torch.cuda.stream(stream)
-
-
-def _token_stride(t: torch.Tensor, want: tuple, dtype, dev: int) -> int:
-    """Elements from one token's row to the next of q, k or v, shaped ``want`` = (tokens, heads, head_dim)."""
-    if t.shape != want or t.dtype != dtype or t.get_device() != dev:
-        raise ValueError("q is [num_tokens, num_q_heads, head_dim], k and v [num_tokens, num_kv_heads, head_dim], "
-                         "of one dtype, on the caches' device")
-    s0, s1, s2 = t.stride()
-    n, heads, d = want
-    if (s2 != 1 and d != 1) or (s1 != d and heads != 1):
-        raise ValueError("a token's heads must be contiguous in q, k and v")
-    return s0 if n > 1 else heads * d
-
-
-def _append_rope(fn, name, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, scales, q_norm, k_norm, norm_eps,
-                 interleaved, q_out, stream):
-    rest = [k_cache, v_cache, slot_mapping, *scales]
-    rest += [t for t in (positions, cos_sin, q_norm, k_norm, q_out) if t is not None]
-    dev = _one_device(rest)
-    if stream is not None or _current_device() != dev:
-        with _context(dev, stream):
-            return _append_rope(fn, name, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, scales, q_norm,
-                                k_norm, norm_eps, interleaved, q_out, None)
-    shape, dt, cache_dt = k_cache.shape, k.dtype, k_cache.dtype
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != cache_dt:
-        raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, head_dim], K as V")
-    nb, hkv, bs, d = shape
-    if slot_mapping.dtype != _I64 or slot_mapping.dim() != 1:
-        raise ValueError("slot_mapping must be int64 [num_tokens]")
-    n = slot_mapping.numel()
-    k_stride, v_stride = _token_stride(k, (n, hkv, d), dt, dev), _token_stride(v, (n, hkv, d), dt, dev)
-    hq = q_stride = q_ptr = 0
-    if q is not None:
-        hq, q_ptr = q.shape[1] if q.dim() == 3 else -1, q.data_ptr()
-        q_stride = _token_stride(q, (n, hq, d), dt, dev)
-        if q_out is not None and (q_out.shape != q.shape or q_out.dtype != dt):
-            raise ValueError("q_out is as q")
-    elif q_out is not None or q_norm is not None:
-        raise ValueError("q_out and q_norm belong to q")
-    rot = max_position = 0
-    if cos_sin is not None:
-        if positions is None or positions.dtype != _I64 or positions.dim() != 1 or positions.numel() != n:
-            raise ValueError("positions must be int64 [num_tokens] where there is a cos_sin")
-        if cos_sin.dtype != _F32 or cos_sin.dim() != 2 or cos_sin.shape[1] == 0:
-            raise ValueError("cos_sin must be fp32 [max_position, rot_dim] (None: no rotation)")
-        max_position, rot = cos_sin.shape
-    elif positions is not None:
-        raise ValueError("positions without cos_sin")
-    for w in (q_norm, k_norm):
-        if w is not None and (w.dtype != dt or w.shape != (d,)):
-            raise ValueError("norm weights are [head_dim], of k's dtype")
-    for s in scales:
-        if s.dtype != _F32 or s.shape != (nb, hkv):
-            raise ValueError("scales must be fp32 [num_blocks, num_kv_heads]")
-    desc = CacheDesc(nb, hkv, bs, d, _DTYPE_CODE.get(cache_dt, -1))
-    rope = RopeDesc(hq, _DTYPE_CODE.get(dt, -1), q_stride, k_stride, v_stride, max_position, rot, bool(interleaved),
-                    float(norm_eps))
-
-    if q_out is None and q is not None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
-    st = fn(q_ptr, k.data_ptr(), v.data_ptr(), _ptr(positions), _ptr(cos_sin), _ptr(q_norm), _ptr(k_norm),
-            slot_mapping.data_ptr(), n, _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
-            *[s.data_ptr() for s in scales], desc, rope, _raw_stream(dev))
-    if st != PKV_OK:
-        raise PagedKVError(st, name)
-    return q_out
+        r = fn(*args)
+    else:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+        _require(stream.device == first.device, "stream belongs to another device")
+        with torch.cuda.stream(stream):
+            r = fn(*args)
+    if type(r) is int:
+        raise PagedKVError(r, name)
+    return r
 
 
 def paged_kv_append_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
@@ -291,8 +231,9 @@ def paged_kv_append_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tenso
     a position's rot_dim / 2 angles before their sines (None: no rotation).  Rows of padding tokens (negative slots)
     are left as they were; ``q_out`` may be ``q`` where that is contiguous.
     """
-    return _append_rope(_lib().paged_kv_append_rope, "paged_kv_append_rope", q, k, v, positions, cos_sin, slot_mapping,
-                        k_cache, v_cache, (), q_norm, k_norm, norm_eps, interleaved, q_out, stream)
+    return _call("paged_kv_append_rope", stream, k_cache, (_MARSHAL or _marshal()).append_rope, False, q, k, v,
+                 positions, cos_sin, slot_mapping, k_cache, v_cache, None, None, q_norm, k_norm, norm_eps, interleaved,
+                 q_out)
 
 
 def paged_kv_append_rope_fp8(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
@@ -307,9 +248,9 @@ def paged_kv_append_rope_fp8(q: torch.Tensor | None, k: torch.Tensor, v: torch.T
     A block starts afresh when its first row is written, and its scales follow the rows it takes on (the header has
     the rule); a block's tokens stand together in ``slot_mapping``.
     """
-    return _append_rope(_lib().paged_kv_append_rope_fp8, "paged_kv_append_rope_fp8", q, k, v, positions, cos_sin,
-                        slot_mapping, k_cache, v_cache, (k_scales, v_scales), q_norm, k_norm, norm_eps, interleaved,
-                        q_out, stream)
+    return _call("paged_kv_append_rope_fp8", stream, k_cache, (_MARSHAL or _marshal()).append_rope, True, q, k, v,
+                 positions, cos_sin, slot_mapping, k_cache, v_cache, k_scales, v_scales, q_norm, k_norm, norm_eps,
+                 interleaved, q_out)
 
 
 def paged_attention_workspace_bytes(num_seqs: int, num_q_heads: int, head_dim: int, max_context_len: int,
@@ -378,49 +319,9 @@ def paged_attention_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                                out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """paged_attention_decode over float8_e4m3fn caches with one fp32 scale per (block, KV head)
     (paged_kv_append_rope_fp8); q is bf16 or fp16."""
-    given = [q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens]
-    given += [t for t in (out, workspace) if t is not None]
-    dev = _one_device(given)
-    if stream is not None or _current_device() != dev:
-        with _context(dev, stream):
-            return paged_attention_decode_fp8(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-                                              scale, out, max_context_len, partition_size, workspace, out_dtype)
-    shape, qshape, tables, cache_dt = k_cache.shape, q.shape, block_tables.shape, k_cache.dtype
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != cache_dt:
-        raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, head_dim], K as V")
-    nb, hkv, bs, d = shape
-    if len(qshape) != 3 or qshape[2] != d or (out is not None and out.shape != qshape):
-        raise ValueError("q and out are [num_seqs, num_q_heads, head_dim]")
-    num_seqs, hq, _ = qshape
-    if block_tables.dtype != _I32 or len(tables) != 2 or tables[0] != num_seqs:
-        raise ValueError("block_tables must be int32 [num_seqs, max_blocks_per_seq]")
-    if context_lens.dtype != _I32 or context_lens.shape != (num_seqs,):
-        raise ValueError("context_lens must be int32 [num_seqs]")
-    for s in (k_scales, v_scales):
-        if s.dtype != _F32 or s.shape != (nb, hkv):
-            raise ValueError("scales must be fp32 [num_blocks, num_kv_heads]")
-    max_blocks = tables[1]
-    max_context_len = max_blocks * bs if max_context_len is None else int(max_context_len)
-    partition_size = int(partition_size)
-    desc = CacheDesc(nb, hkv, bs, d, _DTYPE_CODE.get(cache_dt, -1))
-    lib = _lib()
-
-    if out is None:
-        out = torch.empty(qshape, dtype=out_dtype, device=q.device)
-    if workspace is None:
-        need = lib.paged_attention_workspace_bytes(num_seqs, hq, d, max_context_len, partition_size)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                            workspace.numel() * workspace.element_size())
-    st = lib.paged_attention_decode_fp8(
-        q.data_ptr(), _DTYPE_CODE.get(q.dtype, -1), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
-        v_scales.data_ptr(), block_tables.data_ptr(), max_blocks, context_lens.data_ptr(), num_seqs, hq,
-        max_context_len, float(scale), out.data_ptr(), _DTYPE_CODE.get(out.dtype, -1), desc, partition_size, ws_ptr,
-        ws_bytes, _raw_stream(dev))
-    if st != PKV_OK:
-        raise PagedKVError(st, "paged_attention_decode_fp8")
-    return out
+    return _call("paged_attention_decode_fp8", stream, q, (_MARSHAL or _marshal()).decode_fp8, q, k_cache, v_cache,
+                 k_scales, v_scales, block_tables, context_lens, scale, out, max_context_len, partition_size, workspace,
+                 out_dtype)
 
 
 def paged_attention_append_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -581,23 +482,8 @@ def copy_blocks_fp8(k_caches: torch.Tensor | Sequence[torch.Tensor], v_caches: t
                     src_dst_pairs: torch.Tensor, stream=None) -> None:
     """copy_blocks for float8_e4m3fn caches: block dst := block src in every layer, K and V, with its scales."""
     k, v, ks, vs = ([t] if isinstance(t, torch.Tensor) else list(t) for t in (k_caches, v_caches, k_scales, v_scales))
-    n = len(k)
-    _require(n == len(v) == len(ks) == len(vs) > 0, "need one K and one V cache per layer, and their scales")
-    caches, scales = k + v, ks + vs
-    dev = _one_device(caches + scales + [src_dst_pairs])
-    if stream is not None or _current_device() != dev:
-        with _context(dev, stream):
-            return copy_blocks_fp8(k, v, ks, vs, src_dst_pairs)
-    desc = cache_desc(k[0])
-    # whole tensors of one size and type: nothing lies outside them
-    _require(len(set(map(_numel, caches))) == 1 == len(set(map(_dtype_of, caches))), "the caches differ")
-    _require(set(map(_numel, scales)) == {desc.num_blocks * desc.num_kv_heads} and
-             set(map(_dtype_of, scales)) == {_F32}, "scales must be fp32 [num_blocks, num_kv_heads]")
-    _require(src_dst_pairs.dtype == _I64 and src_dst_pairs.numel() % 2 == 0, "src_dst_pairs must be int64 [n, 2]")
-    ptrs = array.array("Q", map(torch.Tensor.data_ptr, caches + scales))  # the four host arrays, one after the other
-    at, step = ptrs.buffer_info()[0], n * ptrs.itemsize
-    _check(_lib().copy_blocks_fp8(at, at + step, at + 2 * step, at + 3 * step, n, src_dst_pairs.data_ptr(),
-                                  src_dst_pairs.numel() // 2, desc, _raw_stream(dev)), "copy_blocks_fp8")
+    _call("copy_blocks_fp8", stream, src_dst_pairs, (_MARSHAL or _marshal()).copy_blocks_fp8, k, v, ks, vs,
+          src_dst_pairs)
 
 
 def swap_blocks(src_k: torch.Tensor | Sequence[torch.Tensor], src_v: torch.Tensor | Sequence[torch.Tensor],
