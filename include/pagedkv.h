@@ -146,7 +146,8 @@ pkv_status paged_kv_append(const void* k, const void* v, const int64_t* slot_map
  *                contiguous inside the row: slices of one fused projection
  *                are passed as they are.  16-byte aligned; the cache's dtype.
  *                q and q_out may be NULL when num_q_heads is 0.
- * positions:     [num_tokens] int64 device memory; NULL when rot_dim is 0.
+ * positions:     [num_tokens] int64 device memory; not read, NULL allowed, when
+ *                rot_dim is 0.
  * cos_sin:       [max_position][rot_dim] fp32 device memory, 16-byte
  *                aligned; NULL when rot_dim is 0.
  * q_norm, k_norm: [head_dim] device memory, 16-byte aligned, or NULL.

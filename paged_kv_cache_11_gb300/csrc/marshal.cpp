@@ -141,10 +141,11 @@ PyObject* append_rope(PyObject* const* a) {
     } else {
         require(!q_out && !q_norm, "q_out and q_norm belong to q");
     }
-    require(!positions == !cos_sin, "positions and cos_sin belong together");
+    // without cos_sin positions may stand there (a layer that rotates nothing, called like its neighbours) unread
+    require(!positions || (positions->scalar_type() == c10::ScalarType::Long && shaped(*positions, {n})),
+            "positions must be int64 [num_tokens]");
     if (cos_sin) {
-        require(positions->scalar_type() == c10::ScalarType::Long && shaped(*positions, {n}),
-                "positions must be int64 [num_tokens]");
+        require(positions, "cos_sin needs positions");
         require(cos_sin->scalar_type() == c10::ScalarType::Float && cos_sin->dim() == 2 && cos_sin->size(1) > 0,
                 "cos_sin must be fp32 [max_position, rot_dim] (None: no rotation)");
         rope.max_position = cos_sin->size(0);

@@ -346,7 +346,7 @@ def test_binding_refusals(gpu):
     d = c.to_dev(gpu)
     launches = pkv.launch_count()
     bad = [dict(k=d["k"].float()), dict(k=d["k"][:3]), dict(v=d["v"][:, :1]), dict(q=d["q"].transpose(1, 2)),
-           dict(slot_mapping=d["slot_mapping"].int()), dict(positions=None), dict(cos_sin=None),
+           dict(slot_mapping=d["slot_mapping"].int()), dict(positions=None),
            dict(positions=d["positions"].int()), dict(cos_sin=d["cos_sin"].double()), dict(cos_sin=d["cos_sin"][:, :0]),
            dict(q_norm=d["q_norm"].float()), dict(k_norm=d["k_norm"][:64]), dict(q_out=d["q_out"][:, :1]), dict(q=None),
            dict(k_scales=d["k_scales"].half()), dict(v_scales=d["v_scales"].t()), dict(v_cache=d["v_cache"][:1]),
@@ -360,6 +360,22 @@ def test_binding_refusals(gpu):
     with pytest.raises(pkv.PagedKVError):
         pkv.paged_kv_append_rope(**x)                                 # an e4m3 pool needs the other call
     assert pkv.launch_count() == launches
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_positions_without_a_table_are_not_read(gpu, fp8):
+    slots, pos = runs_of_tokens(np.random.default_rng(4), [(0, 40), (3, 9)], 16, 8)
+    c = Case(34, 4, 2, 16, FP, 0, False, True, slots, pos, 8, fp8=fp8)
+    call = pkv.paged_kv_append_rope_fp8 if fp8 else pkv.paged_kv_append_rope
+    names = ("q_out", "k_cache", "v_cache", "k_scales", "v_scales") if fp8 else ("q_out", "k_cache", "v_cache")
+    a, b = c.to_dev(gpu), c.to_dev(gpu)
+    far = torch.full((len(slots),), 1 << 62, device=gpu)
+    call(**{**a, "positions": None, "cos_sin": None})
+    call(**{**b, "positions": far, "cos_sin": None})
+    for n in names:
+        assert torch.equal(a[n].view(torch.uint8), b[n].view(torch.uint8))
+    c.check_q(b["q_out"])
+    pkv.check_device_error()
 
 
 def test_the_plain_block_write_agrees(gpu):
