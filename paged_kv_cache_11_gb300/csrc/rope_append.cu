@@ -11,11 +11,16 @@
 // The norm's sum of squares is the only exchange, over the 16 lanes.
 //
 // Bytes bound the 16-bit write: each row is read once and written once, 16384
-// normed tokens of 64/8 heads (680 MB) in 103.8 us, 6.5 TB/s.  The 8-bit write
+// normed tokens of 64/8 heads (680 MB) in 104 us, 6.5 TB/s.  The 8-bit write
 // waits on more: a block's scale needs all of its new rows before the first
 // byte, a chain of loads and exchanges for each run of tokens: 16384 tokens of
-// 32/8 heads (378 MB) in 70.5 us, 5.4 TB/s.
+// 32/8 heads (378 MB) in 67.9 us, 5.6 TB/s; 777 normed ones of 40/40 heads (40
+// MB) in 16.4 us, 12.9 of them the keys' and values' (issue slots 37% used,
+// three warps to a scheduler); a step of 256 sequences in 3.0 us.
 #include <cuda_fp8.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "pkv_internal.cuh"
 
@@ -59,67 +64,72 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
-__device__ __forceinline__ f32x2 swapped(f32x2 v) {
-    float lo, hi;
-    unpack_f32x2(v, lo, hi);
-    return pack_f32x2(hi, lo);
-}
-
-// A lane's eight values of a head row: quad A in v[0], v[1], quad B in v[2], v[3].
+// A lane's eight values of a head row: the first members of its four pairs in
+// v[0], v[1], the second members in v[2], v[3], so that both kinds of pairs
+// are turned alike (quad A and quad B, or their even and odd values).
 struct Row {
     f32x2 v[4];
 };
 
-template <bool kBF16>
-__device__ __forceinline__ f32x2 widen(uint32_t w) {
-    if constexpr (kBF16) {
-        return pack_f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        return pack_f32x2(f.x, f.y);
+// ... from and to the order of quad A, quad B.
+template <bool kInter>
+__device__ __forceinline__ Row row_of(const float (&f)[8]) {
+    Row x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int lo = kInter ? 4 * (k & 1) + (k >> 1) : 2 * k;
+        x.v[k] = pack_f32x2(f[lo], f[lo + (kInter ? 2 : 1)]);
+    }
+    return x;
+}
+template <bool kInter>
+__device__ __forceinline__ void values_of(const Row& x, float (&f)[8]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int lo = kInter ? 4 * (k & 1) + (k >> 1) : 2 * k;
+        unpack_f32x2(x.v[k], f[lo], f[lo + (kInter ? 2 : 1)]);
     }
 }
 
-template <bool kBF16>
+template <bool kBF16, bool kInter>
 __device__ __forceinline__ Row widen_row(uint2 a, uint2 b) {
-    Row x;
-    x.v[0] = widen<kBF16>(a.x), x.v[1] = widen<kBF16>(a.y);
-    x.v[2] = widen<kBF16>(b.x), x.v[3] = widen<kBF16>(b.y);
-    return x;
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (kBF16) {
+            f[2 * k] = __uint_as_float(w[k] << 16);
+            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        } else {
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+            f[2 * k] = h.x, f[2 * k + 1] = h.y;
+        }
+    }
+    return row_of<kInter>(f);
 }
 
 __device__ __forceinline__ uint2 ldg8(const uint16_t* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
 
-// What turns the lane's values: y[k] = v[k] c[k] + (the other members of the
-// pairs) s[k], the sines negative for the first members.
+// The cosines and sines of a lane's four angles, and the sines' negatives.
 struct Turn {
-    f32x2 c[4], s[4];
+    f32x2 c[2], s[2], n[2];
 };
 
-template <bool kInter>
 __device__ __forceinline__ Turn load_turn(const RopeParams& p, const QuadPos& qp, int64_t pos, int i) {
     Turn t;
     if (qp.rotates) {
         const float* row = p.cos_sin + pos * p.rot_dim + 4 * i;
         const float4 c = __ldg(reinterpret_cast<const float4*>(row));
         const float4 s = __ldg(reinterpret_cast<const float4*>(row + p.rot_dim / 2));
-        if constexpr (kInter) {
-            t.c[0] = pack_f32x2(c.x, c.x), t.c[1] = pack_f32x2(c.y, c.y);
-            t.c[2] = pack_f32x2(c.z, c.z), t.c[3] = pack_f32x2(c.w, c.w);
-            t.s[0] = pack_f32x2(-s.x, s.x), t.s[1] = pack_f32x2(-s.y, s.y);
-            t.s[2] = pack_f32x2(-s.z, s.z), t.s[3] = pack_f32x2(-s.w, s.w);
-        } else {
-            t.c[0] = t.c[2] = pack_f32x2(c.x, c.y), t.c[1] = t.c[3] = pack_f32x2(c.z, c.w);
-            t.s[0] = pack_f32x2(-s.x, -s.y), t.s[1] = pack_f32x2(-s.z, -s.w);
-            t.s[2] = pack_f32x2(s.x, s.y), t.s[3] = pack_f32x2(s.z, s.w);
-        }
+        t.c[0] = pack_f32x2(c.x, c.y), t.c[1] = pack_f32x2(c.z, c.w);
+        t.s[0] = pack_f32x2(s.x, s.y), t.s[1] = pack_f32x2(s.z, s.w);
+        t.n[0] = pack_f32x2(-s.x, -s.y), t.n[1] = pack_f32x2(-s.z, -s.w);
     }
     return t;
 }
 
 // Norm (where there is a weight) and turn of a head row, in 32 bits.  All 16
 // lanes of the row's half-warp take part (`half` is their mask).
-template <bool kInter>
 __device__ __forceinline__ void norm_turn(const RopeParams& p, const QuadPos& qp, bool norm, const Row& weight,
                                           const Turn& t, uint32_t half, Row& x) {
     if (norm) {
@@ -138,29 +148,22 @@ __device__ __forceinline__ void norm_turn(const RopeParams& p, const QuadPos& qp
     }
     if (qp.rotates) {
         Row y;
-        if constexpr (kInter) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y.v[k] = fma2(swapped(x.v[k]), t.s[k], mul2(x.v[k], t.c[k]));
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y.v[k] = fma2(x.v[k ^ 2], t.s[k], mul2(x.v[k], t.c[k]));
+        for (int k = 0; k < 2; ++k) {
+            y.v[k] = fma2(x.v[k + 2], t.n[k], mul2(x.v[k], t.c[k]));
+            y.v[k + 2] = fma2(x.v[k], t.s[k], mul2(x.v[k + 2], t.c[k]));
         }
         x = y;
     }
 }
 
 // The one rounding of a row to 16 bits.
-template <bool kBF16>
-__device__ __forceinline__ uint32_t narrow(f32x2 v) {
-    float lo, hi;
-    unpack_f32x2(v, lo, hi);
-    return pack2<kBF16>(lo, hi);
-}
-
-template <bool kBF16>
+template <bool kBF16, bool kInter>
 __device__ __forceinline__ void store_row(uint16_t* row, const QuadPos& qp, const Row& x) {
-    *reinterpret_cast<uint2*>(row + qp.a) = make_uint2(narrow<kBF16>(x.v[0]), narrow<kBF16>(x.v[1]));
-    *reinterpret_cast<uint2*>(row + qp.b) = make_uint2(narrow<kBF16>(x.v[2]), narrow<kBF16>(x.v[3]));
+    float f[8];
+    values_of<kInter>(x, f);
+    *reinterpret_cast<uint2*>(row + qp.a) = make_uint2(pack2<kBF16>(f[0], f[1]), pack2<kBF16>(f[2], f[3]));
+    *reinterpret_cast<uint2*>(row + qp.b) = make_uint2(pack2<kBF16>(f[4], f[5]), pack2<kBF16>(f[6], f[7]));
 }
 
 // What becomes of a token: padding, an error (recorded once by the caller), or
@@ -197,7 +200,7 @@ __device__ __forceinline__ Token token_at(const RopeParams& p, int64_t t) {
 // heads, 16.1 against 15.8 us for 1537 of 40/40, 2.6 against 2.0 us for 64 of
 // 32/8.
 __host__ __device__ __forceinline__ uint32_t row_units(int heads, int R) { return (heads + R - 1) / R; }
-constexpr int64_t kManyUnits = 65536;  // units of 8 rows from which on R = 8
+constexpr int64_t kManyRows = 524288;  // from which on R = 8
 
 template <bool kBF16, bool kInter, bool kQOnly, int R>
 __device__ __forceinline__ void do_rows(const RopeParams& p, uint32_t unit) {
@@ -231,7 +234,7 @@ __device__ __forceinline__ void do_rows(const RopeParams& p, uint32_t unit) {
         }
     const uint16_t* wp = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
     Row weight;
-    if (wp) weight = widen_row<kBF16>(ldg8(wp + qp.a), ldg8(wp + qp.b));
+    if (wp) weight = widen_row<kBF16, kInter>(ldg8(wp + qp.a), ldg8(wp + qp.b));
     if (slot < 0) return;  // padding
     uint16_t* to = p.q_out + (t * p.num_q_heads + h0) * kHeadDim;
     int64_t to_step = kHeadDim;
@@ -252,13 +255,13 @@ __device__ __forceinline__ void do_rows(const RopeParams& p, uint32_t unit) {
              off * kHeadDim;
     }
     if (kQOnly || kind < 2) {
-        const Turn turn = load_turn<kInter>(p, qp, pos, i);
+        const Turn turn = load_turn(p, qp, pos, i);
 #pragma unroll
         for (int r = 0; r < R; ++r)
             if (r < n) {
-                Row x = widen_row<kBF16>(ra[r], rb[r]);
-                norm_turn<kInter>(p, qp, wp != nullptr, weight, turn, half, x);
-                store_row<kBF16>(to + r * to_step, qp, x);
+                Row x = widen_row<kBF16, kInter>(ra[r], rb[r]);
+                norm_turn(p, qp, wp != nullptr, weight, turn, half, x);
+                store_row<kBF16, kInter>(to + r * to_step, qp, x);
             }
     } else {  // values pass through as they are
 #pragma unroll
@@ -290,25 +293,21 @@ __device__ __forceinline__ float power_scale(float a) {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
-// Two values (at most 448 in magnitude, but for the last bit, or NaN) to two
-// e4m3 bytes, nearest, ties to even.
-__device__ __forceinline__ uint32_t e4m3_pair(f32x2 v) {
-    float lo, hi;
-    unpack_f32x2(v, lo, hi);
-    uint16_t w;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(w) : "f"(hi), "f"(lo));
-    return w;
+// Four values (at most 448 in magnitude, but for the last bit, or NaN) to e4m3
+// bytes, nearest, ties to even.
+__device__ __forceinline__ uint32_t e4m3_quad(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return lo | ((uint32_t)hi << 16);
 }
 
-__device__ __forceinline__ uint32_t e4m3_quad(f32x2 a, f32x2 b, f32x2 inv) {
-    return e4m3_pair(mul2(a, inv)) | (e4m3_pair(mul2(b, inv)) << 16);
-}
-
-// The move of a block's held rows 0 .. first - 1 to another scale, by a warp:
-// 8 lanes per row, 16 bytes each.
-__device__ __forceinline__ void move_rows(uint8_t* tile, int first, float ratio, int lane) {
+// The move of a block's held rows 0 .. first - 1 to another scale, by `kLanes`
+// lanes: 8 per row, 16 bytes each.
+template <int kLanes>
+__device__ __noinline__ void move_rows(uint8_t* tile, int first, float ratio, int lane) {
 #pragma unroll 1
-    for (int r = lane >> 3; r < first; r += 4) {
+    for (int r = lane >> 3; r < first; r += kLanes / 8) {
         uint4* at = reinterpret_cast<uint4*>(tile + r * kHeadDim) + (lane & 7);
         uint4 v = *at;
         uint32_t* w = reinterpret_cast<uint32_t*>(&v);
@@ -319,7 +318,7 @@ __device__ __forceinline__ void move_rows(uint8_t* tile, int first, float ratio,
             for (int e = 0; e < 4; ++e)
                 f[e] = __half2float(
                     __half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)((w[j] >> (8 * e)) & 0xffu), __NV_E4M3)));
-            w[j] = e4m3_quad(pack_f32x2(f[0], f[1]), pack_f32x2(f[2], f[3]), pack_f32x2(ratio, ratio));
+            w[j] = e4m3_quad(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
         }
         *at = v;
     }
@@ -339,7 +338,7 @@ __device__ __forceinline__ float settle_scale(const RopeParams& p, float* scale,
         } else if (a <= 448.f * old) {
             return old;
         } else if (writes) {
-            move_rows(tile, first, old / s, lane);
+            move_rows<32>(tile, first, old / s, lane);
         }
     }
     if (writes && lane == 0) *scale = s;
@@ -363,10 +362,15 @@ __device__ __forceinline__ float warp_max(float a) {
     return a;
 }
 
-__device__ __forceinline__ void store_e4m3(uint8_t* row, const QuadPos& qp, const Row& x, float inv) {
+template <bool kInter>
+__device__ __forceinline__ void store_e4m3(uint8_t* row, const QuadPos& qp, Row x, float inv) {
     const f32x2 ii = pack_f32x2(inv, inv);
-    *reinterpret_cast<uint32_t*>(row + qp.a) = e4m3_quad(x.v[0], x.v[1], ii);
-    *reinterpret_cast<uint32_t*>(row + qp.b) = e4m3_quad(x.v[2], x.v[3], ii);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x.v[k] = mul2(x.v[k], ii);
+    float f[8];
+    values_of<kInter>(x, f);
+    *reinterpret_cast<uint32_t*>(row + qp.a) = e4m3_quad(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<uint32_t*>(row + qp.b) = e4m3_quad(f[4], f[5], f[6], f[7]);
 }
 
 // Infinities of a row to NaN, as they are stored (and counted).
@@ -391,7 +395,7 @@ __device__ __noinline__ void write_any_run(const RopeParams& p, int64_t t0, int 
     uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
                     ((int64_t)blk * p.num_kv_heads + h) * p.block_size * kHeadDim;
     Row weight;
-    if (p.k_norm) weight = widen_row<kBF16>(ldg8(p.k_norm + qp.a), ldg8(p.k_norm + qp.b));
+    if (p.k_norm) weight = widen_row<kBF16, kInter>(ldg8(p.k_norm + qp.a), ldg8(p.k_norm + qp.b));
     float a = 0.f;              // pass 0: the largest finite magnitude; pass 1: the reciprocal of the scale
     int first = p.block_size;  // first row written
     for (int pass = 0; pass < 2; ++pass) {
@@ -418,17 +422,17 @@ __device__ __noinline__ void write_any_run(const RopeParams& p, int64_t t0, int 
                     const int off = slot - blk * p.block_size;
                     const uint16_t* row =
                         is_k ? p.k + t * p.k_stride + h * kHeadDim : p.v + t * p.v_stride + h * kHeadDim;
-                    Row x = widen_row<kBF16>(ldg8(row + qp.a), ldg8(row + qp.b));
+                    Row x = widen_row<kBF16, kInter>(ldg8(row + qp.a), ldg8(row + qp.b));
                     if (is_k) {
-                        const Turn turn = load_turn<kInter>(p, qp, pos, i);
-                        norm_turn<kInter>(p, qp, p.k_norm != nullptr, weight, turn, half, x);
+                        const Turn turn = load_turn(p, qp, pos, i);
+                        norm_turn(p, qp, p.k_norm != nullptr, weight, turn, half, x);
                     }
                     infinite_to_nan(x);
                     if (pass == 0) {
                         first = min(first, off);
                         a = top(a, x);
                     } else {
-                        store_e4m3(tile + off * kHeadDim, qp, x, a);
+                        store_e4m3<kInter>(tile + off * kHeadDim, qp, x, a);
                     }
                 }
                 __syncwarp();
@@ -459,16 +463,15 @@ __device__ __noinline__ void write_any_run(const RopeParams& p, int64_t t0, int 
 // magnitudes meeting in shared memory, took 61 us for keys and values against
 // 45.)  The two warps of a 32-row block meet at a barrier, `meet` is where they
 // leave their magnitudes.
-template <bool kBF16, bool kInter, bool kKeys, int BS>
+template <bool kBF16, bool kInter, int BS>
 __device__ __forceinline__ bool write_run(const RopeParams& p, uint4* stage, float* meet, int64_t t0, int count,
-                                          int off_l, int pos_l, int first, int blk, int h) {
+                                          int off_l, int pos_l, int first, int blk, int h, bool is_k) {
     const int lane = threadIdx.x & 31, i = lane & 15, hf = lane >> 4, warp = threadIdx.x >> 5;
     const int r0 = BS == 32 ? 16 * (warp & 1) : 0;  // the warp's first row
     const int mine = min(count - r0, 16);           // its rows (none: <= 0)
-    QuadPos qp = quad_pos<kInter>(p, i);
-    if (!kKeys) qp.rotates = false, qp.a = 8 * i, qp.b = 8 * i + 4;
-    const int64_t stride = kKeys ? p.k_stride : p.v_stride;
-    const uint16_t* from = (kKeys ? p.k : p.v) + (t0 + r0 + hf) * stride + h * kHeadDim + 8 * i;
+    const QuadPos qp = quad_pos<kInter>(p, i);
+    const int64_t stride = is_k ? p.k_stride : p.v_stride;
+    const uint16_t* from = (is_k ? p.k : p.v) + (t0 + r0 + hf) * stride + h * kHeadDim + 8 * i;
     const uint32_t to = smem_addr(stage + lane);
     __syncwarp();  // the warp is done with what the stage held
 #pragma unroll
@@ -476,11 +479,11 @@ __device__ __forceinline__ bool write_run(const RopeParams& p, uint4* stage, flo
         if (2 * j + hf < mine)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512 * j), "l"(from + 2 * j * stride)
                          : "memory");
-    float* scale = (kKeys ? p.k_scales : p.v_scales) + (int64_t)blk * p.num_kv_heads + h;
+    float* scale = (is_k ? p.k_scales : p.v_scales) + (int64_t)blk * p.num_kv_heads + h;
     const float old = first > 0 ? *scale : 0.f;
-    const bool norm = kKeys && p.k_norm;
+    const bool norm = is_k && p.k_norm;
     Row weight;
-    if (norm) weight = widen_row<kBF16>(ldg8(p.k_norm + qp.a), ldg8(p.k_norm + qp.b));
+    if (norm) weight = widen_row<kBF16, kInter>(ldg8(p.k_norm + qp.a), ldg8(p.k_norm + qp.b));
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();  // every lane has read `old`, too
     // Pair j of rows lies in bytes 512j .. 512j + 511 of the stage, its 32-bit
@@ -491,11 +494,11 @@ __device__ __forceinline__ bool write_run(const RopeParams& p, uint4* stage, flo
     for (int j = (mine - 1) >> 1; j >= 0; --j) {
         const int r = min(2 * j + hf, mine - 1);
         const uint16_t* row = reinterpret_cast<const uint16_t*>(stage) + r * kHeadDim;
-        Row y = widen_row<kBF16>(*reinterpret_cast<const uint2*>(row + qp.a),
-                                 *reinterpret_cast<const uint2*>(row + qp.b));
-        if constexpr (kKeys) {
-            const Turn turn = load_turn<kInter>(p, qp, __shfl_sync(0xffffffffu, pos_l, r0 + r), i);
-            norm_turn<kInter>(p, qp, norm, weight, turn, 0xffffffffu, y);
+        Row y = widen_row<kBF16, kInter>(*reinterpret_cast<const uint2*>(row + qp.a),
+                                         *reinterpret_cast<const uint2*>(row + qp.b));
+        if (is_k) {
+            const Turn turn = load_turn(p, qp, __shfl_sync(0xffffffffu, pos_l, r0 + r), i);
+            norm_turn(p, qp, norm, weight, turn, 0xffffffffu, y);
         }
         a = top(a, y);
         __syncwarp();
@@ -511,7 +514,7 @@ __device__ __forceinline__ bool write_run(const RopeParams& p, uint4* stage, flo
         a = fmaxf(meet[0], meet[1]);
     }
     if (a == INFINITY) return false;
-    uint8_t* tile = static_cast<uint8_t*>(kKeys ? p.k_cache : p.v_cache) +
+    uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
                     ((int64_t)blk * p.num_kv_heads + h) * (BS * kHeadDim);
     const float inv = 1.f / settle_scale(p, scale, old, tile, a, first, r0 == 0);
 #pragma unroll 1
@@ -520,41 +523,86 @@ __device__ __forceinline__ bool write_run(const RopeParams& p, uint4* stage, flo
         const ulonglong2 lo = at[0], hi = at[32];
         Row y;
         y.v[0] = lo.x, y.v[1] = lo.y, y.v[2] = hi.x, y.v[3] = hi.y;
-        store_e4m3(tile + __shfl_sync(0xffffffffu, off_l, r0 + min(2 * j + hf, mine - 1)) * kHeadDim, qp, y, inv);
+        store_e4m3<kInter>(tile + __shfl_sync(0xffffffffu, off_l, r0 + min(2 * j + hf, mine - 1)) * kHeadDim, qp, y, inv);
     }
     return true;
 }
 
+// A run of one token, as a decode step has: its keys of KV head h by the warp's
+// first half, its values by the second, in registers (write_run, one after the
+// other, took 6.0 us for 256 sequences of 8 KV heads, this 3.0).  Returns which of the two are left to
+// write_any_run (bit 0: keys, 1: values), as write_run does.
+template <bool kBF16, bool kInter, int BS>
+__device__ __forceinline__ uint32_t write_one(const RopeParams& p, int64_t t, int off, int pos, int blk, int h) {
+    const int lane = threadIdx.x & 31, i = lane & 15;
+    const bool is_v = lane >> 4;
+    const QuadPos qp = quad_pos<kInter>(p, i);
+    const uint16_t* row = (is_v ? p.v + t * p.v_stride : p.k + t * p.k_stride) + h * kHeadDim;
+    const int64_t tile_no = (int64_t)blk * p.num_kv_heads + h;
+    float* scale = (is_v ? p.v_scales : p.k_scales) + tile_no;
+    uint8_t* tile = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + tile_no * (BS * kHeadDim);
+    const float old = off > 0 ? *scale : 0.f;
+    Row y = widen_row<kBF16, kInter>(ldg8(row + qp.a), ldg8(row + qp.b)), weight;
+    if (p.k_norm) weight = widen_row<kBF16, kInter>(ldg8(p.k_norm + qp.a), ldg8(p.k_norm + qp.b));
+    const Row as_is = y;
+    norm_turn(p, qp, p.k_norm != nullptr, weight, load_turn(p, qp, pos, i), 0xffffffffu, y);
+    if (is_v) y = as_is;
+    float a = top(0.f, y);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    __syncwarp();  // every lane has read `old`
+    if (a < INFINITY) {
+        float s = power_scale(a);
+        if (off > 0 && old >= 0x1p-126f && finite(old)) {
+            if (a <= 448.f * old)
+                s = old;
+            else
+                move_rows<16>(tile, off, old / s, i);
+        } else if (off > 0 && i == 0) {
+            record_error(p.err, PKV_DEVERR_SCALE);
+        }
+        if (i == 0) *scale = s;
+        store_e4m3<kInter>(tile + off * kHeadDim, qp, y, 1.f / s);
+    }
+    const uint32_t rest = __ballot_sync(0xffffffffu, !(a < INFINITY));
+    return (rest & 1u) | ((rest >> 15) & 2u);
+}
+
 // The keys and values of some KV heads (items item0 .. item1 - 1, 32 at most:
 // item 2h is the keys of head h, 2h + 1 its values) of the runs that start
-// among the tokens t0 .. t0 + window - 1 (window <= 31), by one warp (BS = 16)
-// or two that go through it together.  A run is the tokens of one block, which
-// stand together in slot_mapping but for padding.  The warp looks at 64 tokens,
-// from the one before t0 on, so that a run ends among them (but for long
-// padding inside, or slots named twice).  The search takes 3 us of a call.
+// among the tokens t0 .. t0 + window - 1, by one warp (BS = 16) or two that go
+// through it together.  A run is the tokens of one block, which stand together
+// in slot_mapping but for padding.  The warp looks at the 2 BS tokens from the
+// one before t0 on; window < BS, so that a run's end is among them (but for
+// padding inside, or slots named twice).
 template <bool kBF16, bool kInter, int BS>
 __device__ __forceinline__ void do_runs(const RopeParams& p, uint4* stage, float (*meet)[2], int64_t t0, int window,
                                         int item0, int item1) {
+    constexpr int W = BS / 16;  // words of 32 tokens
+    using Bits = typename std::conditional<W == 1, uint32_t, uint64_t>::type;
     const int lane = threadIdx.x & 31;
     const bool second = BS == 32 && ((threadIdx.x >> 5) & 1);  // the second warp of two: leaves the rest to the first
     int turn = 0;                                              // which of the meeting places is next
-    Token tok[2];  // tokens t0 - 1 + lane and t0 + 31 + lane: bits lane and 32 + lane below
-    uint32_t in[2];
+    Token tok[W];  // token t0 - 1 + 32u + lane: bit 32u + lane below
+    Bits present = 0, wrong = 0, leaders = 0;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < W; ++u) {
         const int64_t t = t0 - 1 + 32 * u + lane;
         tok[u].slot = -1, tok[u].pos = 0, tok[u].err = 0;
         if (t >= 0 && t < p.num_tokens) tok[u] = token_at(p, t);
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) in[u] = __ballot_sync(0xffffffffu, tok[u].slot >= 0);
+    for (int u = 0; u < W; ++u) {
+        present |= (Bits)__ballot_sync(0xffffffffu, tok[u].slot >= 0) << (32 * u);
+        wrong |= (Bits)__ballot_sync(0xffffffffu, tok[u].err != 0) << (32 * u);
+    }
     if (tok[0].err == PKV_DEVERR_SLOT && lane >= 1 && lane <= window && item0 == 0 && !second)
         record_error(p.err, PKV_DEVERR_SLOT);
     const uint32_t inside = (2u << window) - 2u;
-    if (!(in[0] & inside)) return;
+    if (!((uint32_t)present & inside)) return;
     // the block of the last token in the pool before t0, over any padding
     int before = __shfl_sync(0xffffffffu, tok[0].slot, 0) / BS;
-    if (!(in[0] & 1u)) {
+    if (!(present & 1u)) {
         before = -1;
         for (int64_t c = t0 - 2; c >= 0; c -= 32) {
             const int64_t s = c - lane >= 0 ? __ldg(p.slot_mapping + (c - lane)) : -1;
@@ -565,66 +613,83 @@ __device__ __forceinline__ void do_runs(const RopeParams& p, uint4* stage, float
             }
         }
     }
-    uint32_t starts[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < W; ++u) {
         const int blk = tok[u].slot / BS;
-        const uint32_t prior = in[u] & ((1u << lane) - 1u);
+        const uint32_t in = (uint32_t)(present >> (32 * u)), prior = in & ((1u << lane) - 1u);
         const int prev = __shfl_sync(0xffffffffu, blk, prior ? 31 - __clz(prior) : 0);
-        starts[u] = __ballot_sync(0xffffffffu, tok[u].slot >= 0 && blk != (prior ? prev : before) && (u || lane));
-        if (in[u]) before = __shfl_sync(0xffffffffu, blk, 31 - __clz(in[u]));
+        leaders |= (Bits)__ballot_sync(0xffffffffu, tok[u].slot >= 0 && blk != (prior ? prev : before) && (u || lane))
+                   << (32 * u);
+        if (u + 1 < W && in) before = __shfl_sync(0xffffffffu, blk, 31 - __clz(in));
     }
-    const uint64_t leaders = starts[0] | (uint64_t)starts[1] << 32, present = in[0] | (uint64_t)in[1] << 32;
-    for (uint32_t own = starts[0] & inside; own; own &= own - 1u) {
+    uint32_t undone = 0;  // lane x: items of the run that starts at bit x, left to write_any_run
+    for (uint32_t own = (uint32_t)leaders & inside; own; own &= own - 1u) {
         const int x = __ffs(own) - 1;
-        const uint64_t later = leaders & ~((2ull << x) - 1ull);
-        const uint64_t upto = later ? (later & (0ull - later)) - 1ull : ~0ull;  // bits below the next run's first
-        const uint64_t run = (present & upto) >> x;
-        const int count = __popcll(run);
+        const Bits later = leaders & ~(((Bits)2 << x) - 1u);
+        const Bits upto = later ? (later & (0u - later)) - 1u : (Bits)0 - 1u;  // bits below the next run's first
+        const Bits run = (present & upto) >> x;
+        const int count = W == 1 ? __popc((uint32_t)run) : __popcll(run);
         // lane l: the run's token l
-        const int src = (x + lane) & 31;
-        const bool hi = x + lane >= 32;
-        const int sl0 = __shfl_sync(0xffffffffu, tok[0].slot, src), sl1 = __shfl_sync(0xffffffffu, tok[1].slot, src);
-        const int ps0 = __shfl_sync(0xffffffffu, tok[0].pos, src), ps1 = __shfl_sync(0xffffffffu, tok[1].pos, src);
-        const int er0 = __shfl_sync(0xffffffffu, tok[0].err, src), er1 = __shfl_sync(0xffffffffu, tok[1].err, src);
-        const bool good = __all_sync(0xffffffffu, lane >= count || (hi ? er1 : er0) == 0);
-        const int slot = hi ? sl1 : sl0, pos = hi ? ps1 : ps0, off = slot & (BS - 1);
-        const int blk = __shfl_sync(0xffffffffu, slot, 0) / BS;
-        uint32_t left = 0xffffffffu;  // items that write_any_run has to do
-        // neighbouring tokens, the run's end in sight
-        if (good && count <= BS && run == (1ull << count) - 1ull && (later || t0 + 63 >= p.num_tokens)) {
-            const int first = __reduce_min_sync(0xffffffffu, lane < count ? off : BS);
-#pragma unroll 1
-            for (int item = item0; item < item1; ++item) {
-                turn ^= 1;  // one meeting's barrier lies between two uses of a place
-                const bool done =
-                    (item & 1) ? write_run<kBF16, kInter, false, BS>(p, stage, meet[turn], t0 + x - 1, count, off, pos,
-                                                                     first, blk, item >> 1)
-                               : write_run<kBF16, kInter, true, BS>(p, stage, meet[turn], t0 + x - 1, count, off, pos,
-                                                                    first, blk, item >> 1);
-                if (done) left &= ~(1u << (item - item0));
-            }
+        int slot = __shfl_sync(0xffffffffu, tok[0].slot, (x + lane) & 31);
+        int pos = __shfl_sync(0xffffffffu, tok[0].pos, (x + lane) & 31);
+        if constexpr (W == 2) {
+            const int s1 = __shfl_sync(0xffffffffu, tok[W - 1].slot, (x + lane) & 31);
+            const int p1 = __shfl_sync(0xffffffffu, tok[W - 1].pos, (x + lane) & 31);
+            if (x + lane >= 32) slot = s1, pos = p1;
         }
-        for (int item = item0; item < item1; ++item)
-            if (((left >> (item - item0)) & 1u) && !second)
-                write_any_run<kBF16, kInter>(p, t0 + x - 1, blk, item >> 1, (item & 1) == 0);
+        const int off = slot & (BS - 1);
+        const int blk = __shfl_sync(0xffffffffu, slot, 0) / BS;
+        uint32_t left = item1 - item0 < 32 ? (1u << (item1 - item0)) - 1u : 0xffffffffu;
+        // neighbouring tokens, all good, the run's end in sight
+        if (count <= BS && run == ((Bits)1 << count) - 1u && !(wrong & (run << x)) &&
+            (later || t0 + 32 * W - 1 >= p.num_tokens)) {
+            left = 0;
+            if (count == 1) {  // a head's keys and values fall to who has its keys
+                const int off0 = __shfl_sync(0xffffffffu, off, 0), pos0 = __shfl_sync(0xffffffffu, pos, 0);
+#pragma unroll 1
+                for (int item = (item0 + 1) & ~1; item < item1; item += 2)
+                    if (BS == 16 || second == ((item >> 1) & 1))
+                        left |= write_one<kBF16, kInter, BS>(p, t0 + x - 1, off0, pos0, blk, item >> 1) << (item - item0);
+            } else {
+                const int first = __reduce_min_sync(0xffffffffu, lane < count ? off : BS);
+#pragma unroll 1
+                for (int item = item0; item < item1; ++item) {
+                    turn ^= 1;  // one meeting's barrier lies between two uses of a place
+                    if (!write_run<kBF16, kInter, BS>(p, stage, meet[turn], t0 + x - 1, count, off, pos, first, blk,
+                                                      item >> 1, (item & 1) == 0) &&
+                        !second)
+                        left |= 1u << (item - item0);
+                }
+            }
+        } else if (second) {
+            left = 0;
+        }
+        if (lane == x) undone = left;
+    }
+    for (uint32_t runs = __ballot_sync(0xffffffffu, undone != 0); runs; runs &= runs - 1u) {
+        const int x = __ffs(runs) - 1, blk = __shfl_sync(0xffffffffu, tok[0].slot, x) / BS;
+        for (uint32_t left = __shfl_sync(0xffffffffu, undone, x); left; left &= left - 1u) {
+            const int item = item0 + __ffs(left) - 1;
+            write_any_run<kBF16, kInter>(p, t0 + x - 1, blk, item >> 1, (item & 1) == 0);
+        }
     }
 }
 
-// kv_blocks of the CTAs write keys and values, a warp for each window of
-// tokens and `items` items; the others turn the query heads.  The two kinds
-// are spread evenly over the grid: the first wait on a chain of loads (slots,
-// rows and scale), the second stream, and side by side they fill each other's
-// pauses.  kv_rate = ceil(kv_blocks 2^32 / CTAs).
+// kv_blocks of the CTAs write keys and values, a warp (or two) for each window
+// of tokens and `items` items; the others turn the query heads.  Of the first
+// CTAs kv_rate / 2^32 are of the first kind, until there are no more: these
+// wait on a chain of loads (slots, rows and scale), the others stream, and
+// side by side they fill each other's pauses.
 template <bool kBF16, bool kInter, int BS, int R>
 __global__ void __launch_bounds__(kRopeThreads, BS == 16 ? 5 : 4)
-    rope_fp8_kernel(const RopeParams p, uint64_t kv_rate, int window, int items) {
+    rope_fp8_kernel(const RopeParams p, uint32_t kv_blocks, uint64_t kv_rate, int window, int items) {
     __shared__ uint4 stage[kRopeThreads / 32][16 * kHeadDim / 4];  // 16 rows of 32-bit values for each warp
     __shared__ float meet[kRopeThreads / 64][2][2];                // for each pair of warps
     pdl_launch_dependents();
     pdl_wait();
-    const uint32_t kv = (uint32_t)((blockIdx.x * kv_rate) >> 32);  // CTAs of the first kind before this one
-    if ((uint32_t)(((blockIdx.x + 1ull) * kv_rate) >> 32) > kv) {
+    // CTAs of the first kind before this one and before the next
+    const uint32_t kv = min(kv_blocks, (uint32_t)((blockIdx.x * kv_rate) >> 32));
+    if (min(kv_blocks, (uint32_t)(((blockIdx.x + 1ull) * kv_rate) >> 32)) > kv) {
         const uint32_t w = kv * (kRopeThreads / (2 * BS)) + threadIdx.x / (2 * BS);  // one or two warps together
         const uint32_t all = 2 * (uint32_t)p.num_kv_heads, per_window = (all + items - 1) / items;
         const uint32_t win = w / per_window;
@@ -638,46 +703,67 @@ __global__ void __launch_bounds__(kRopeThreads, BS == 16 ? 5 : 4)
     }
 }
 
-constexpr int64_t kRunWarps = 6080;  // warps for keys and values that a long call keeps (40 per SM)
+template <bool kBF16, bool kInter>
+static cudaError_t launch_rope_fp8(const RopeParams& p, cudaStream_t stream) {
+    // Eight rows of queries at a time whatever the call's size: keys and
+    // values hold most of the places, and half the loads in flight cost 43.4 -> 50.2
+    // us for 5000 tokens of 64/8 heads, 3.0 -> 3.5 for 256 of 32/8.
+    constexpr int R = 8;
+    const int64_t q_units = p.num_tokens * (int64_t)row_units(p.num_q_heads, R);
+    const int64_t q_blocks = (q_units + kRopeThreads / 16 - 1) / (kRopeThreads / 16);
+    // Teams of a warp, or of two, for keys and values.  As long as all are
+    // resident at once, one for each token and item.  With more, a head's keys
+    // and values share one (256 sequences' next tokens: 3.0 us, 4.4 without;
+    // but 5.5 us, 7.3 with, for a chunk of 100 tokens, which has few runs);
+    // then windows grow towards a block's tokens, and items again, while
+    // enough teams are left: 16384 tokens of 8 KV heads in blocks of 16 took
+    // 67.9 us with 8192 teams, 70.9 with 4096, 777 of 40 heads in blocks of 32
+    // 16.4 with 1960, 18.4 with 1040, 19.5 with 3920.
+    constexpr int64_t kResident = 2432;
+    const int64_t enough = p.block_size == 16 ? 6080 : 1520;
+    const int64_t all = 2 * (int64_t)p.num_kv_heads, pair = p.block_size / 16;
+    const auto teams = [&](int w, int n) { return (p.num_tokens + w - 1) / w * ((all + n - 1) / n); };
+    int window = 1, items = teams(1, 1) * pair > kResident ? 2 : 1;
+    for (int w = 2; w < 2 * (int)p.block_size; w *= 2) {
+        const int most = std::min(w, (int)p.block_size - 1);
+        if (teams(most, items) >= enough) window = most;
+    }
+    while (items < 32 && teams(window, 2 * items) >= enough) items *= 2;
+    const int64_t kv_blocks = (teams(window, items) * pair + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    const uint64_t blocks = (uint64_t)(kv_blocks + q_blocks);
+    // Keys and values are spread over the first two thirds of the grid: their
+    // teams take longest, and none should start last.  (Spread over all of it
+    // 69.8, 18.6 and 43.3 us for 16384, 777 and 5000 tokens; so 67.9, 16.4,
+    // 39.1; all of them first 73.3, 16.4, 40.5.)
+    const uint64_t even = (((uint64_t)kv_blocks << 32) + blocks - 1) / blocks;
+    const uint64_t kv_rate = std::min<uint64_t>(even + even / 2, 1ull << 32);
+    auto kern = p.block_size == 16 ? rope_fp8_kernel<kBF16, kInter, 16, R> : rope_fp8_kernel<kBF16, kInter, 32, R>;
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(kRopeThreads), 0, stream, p, (uint32_t)kv_blocks, kv_rate, window,
+                      items);
+}
 
 template <bool kBF16, bool kInter, int R>
-static cudaError_t launch_rope_append_t(const RopeParams& p, bool fp8, cudaStream_t stream) {
-    const int64_t units = p.num_tokens * ((int64_t)row_units(p.num_q_heads, R) +
-                                          (fp8 ? 0 : 2 * (int64_t)row_units(p.num_kv_heads, R)));
-    const int64_t row_blocks = (units + kRopeThreads / 16 - 1) / (kRopeThreads / 16);
-    if (!fp8)
-        return launch_pdl(rope_rows_kernel<kBF16, kInter, R>, dim3((unsigned)row_blocks), dim3(kRopeThreads), 0, stream,
-                          p);
-    // Few tokens: a warp for each token and item, so that every SM has some.
-    // Many: windows of a block, then items in one warp, which share the search
-    // for the runs and their angles, while kRunWarps are left: 16384 tokens of
-    // 8 KV heads took 80.0 us with 4096 warps, 73.3 with 8192, 777 tokens of
-    // 40 heads 20.0 with 7840, 26.1 with 15680.
-    const int64_t all = 2 * (int64_t)p.num_kv_heads, pair = p.block_size / 16;
-    int window = 1, items = 1;
-    const auto warps = [&](int w, int n) { return (p.num_tokens + w - 1) / w * ((all + n - 1) / n) * pair; };
-    while (window < 16 && warps(2 * window, 1) >= kRunWarps) window *= 2;
-    while (items < 32 && warps(window, 2 * items) >= kRunWarps) items *= 2;
-    const int64_t kv_blocks = (warps(window, items) + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-    auto kern = p.block_size == 16 ? rope_fp8_kernel<kBF16, kInter, 16, R> : rope_fp8_kernel<kBF16, kInter, 32, R>;
-    const uint64_t blocks = (uint64_t)(kv_blocks + row_blocks);
-    const uint64_t kv_rate = (((uint64_t)kv_blocks << 32) + blocks - 1) / blocks;
-    return launch_pdl(kern, dim3((unsigned)blocks), dim3(kRopeThreads), 0, stream, p, kv_rate, window, items);
+static cudaError_t launch_rope_rows(const RopeParams& p, cudaStream_t stream) {
+    const int64_t units =
+        p.num_tokens * ((int64_t)row_units(p.num_q_heads, R) + 2 * (int64_t)row_units(p.num_kv_heads, R));
+    const int64_t blocks = (units + kRopeThreads / 16 - 1) / (kRopeThreads / 16);
+    return launch_pdl(rope_rows_kernel<kBF16, kInter, R>, dim3((unsigned)blocks), dim3(kRopeThreads), 0, stream, p);
 }
 
 template <bool kBF16, bool kInter>
-static cudaError_t launch_rope_append_r(const RopeParams& p, bool fp8, cudaStream_t stream) {
-    const int64_t rows = (int64_t)p.num_q_heads + (fp8 ? 0 : 2 * (int64_t)p.num_kv_heads);
-    return p.num_tokens * rows >= 8 * kManyUnits ? launch_rope_append_t<kBF16, kInter, 8>(p, fp8, stream)
-                                                 : launch_rope_append_t<kBF16, kInter, 4>(p, fp8, stream);
+static cudaError_t launch_rope_append_t(const RopeParams& p, bool fp8, cudaStream_t stream) {
+    if (fp8) return launch_rope_fp8<kBF16, kInter>(p, stream);
+    const int64_t rows = (int64_t)p.num_q_heads + 2 * (int64_t)p.num_kv_heads;
+    return p.num_tokens * rows >= kManyRows ? launch_rope_rows<kBF16, kInter, 8>(p, stream)
+                                            : launch_rope_rows<kBF16, kInter, 4>(p, stream);
 }
 
 cudaError_t launch_rope_append(const RopeParams& p, int dtype, bool fp8, cudaStream_t stream, int* launches) {
     const bool bf16 = dtype == PKV_BF16;
-    const cudaError_t e = bf16 ? (p.interleaved ? launch_rope_append_r<true, true>(p, fp8, stream)
-                                                : launch_rope_append_r<true, false>(p, fp8, stream))
-                               : (p.interleaved ? launch_rope_append_r<false, true>(p, fp8, stream)
-                                                : launch_rope_append_r<false, false>(p, fp8, stream));
+    const cudaError_t e = bf16 ? (p.interleaved ? launch_rope_append_t<true, true>(p, fp8, stream)
+                                                : launch_rope_append_t<true, false>(p, fp8, stream))
+                               : (p.interleaved ? launch_rope_append_t<false, true>(p, fp8, stream)
+                                                : launch_rope_append_t<false, false>(p, fp8, stream));
     if (e == cudaSuccess) ++*launches;
     return e;
 }

@@ -387,3 +387,79 @@ def test_the_plain_block_write_agrees(gpu):
     pkv.paged_kv_append(b["k"], b["v"], b["slot_mapping"], b["k_cache"], b["v_cache"])
     assert torch.equal(a["k_cache"], b["k_cache"]) and torch.equal(a["v_cache"], b["v_cache"])
     assert np.isfinite(to64(a["k_cache"])).all()
+
+
+def _with_ends(c, kinds):
+    """Puts rows at the ends of the range among c's (unfused) rows, a kind per token in turn."""
+    for t in range(len(c.slots)):
+        kind = kinds[t % len(kinds)]
+        if kind == "zero":
+            c.k[t], c.v[t] = 0, 0
+        elif kind == "k inf":
+            c.k[t, :, 3] = float("inf")
+        elif kind == "v inf":
+            c.v[t, 0, 126] = float("-inf")
+        elif kind == "nan":
+            c.k[t, :, ::2], c.v[t] = float("nan"), float("nan")
+        elif kind == "large":
+            c.k[t] *= 50.0
+            c.v[t] *= 1e4
+        elif kind == "small":
+            c.k[t] *= 1e-3
+            c.v[t] *= 1e-6
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bs", [16, 32])
+@pytest.mark.parametrize("rot", [0, 64])
+def test_steps_of_one_token(gpu, bs, rot, inter):
+    """A token of each sequence, at every row of a block: joining rows that keep or raise the scale, infinities in
+    the keys or the values alone, unusable scales."""
+    rng = np.random.default_rng(bs + rot)
+    spans = [(p % (2 * bs), 1) for p in range(3 * bs)]
+    slots, pos = runs_of_tokens(rng, spans, bs, 4 * bs + 8)
+    c = Case(41 + bs, 4, 3, bs, FP if inter else BF, rot, inter, False, slots, pos, 4 * bs + 8, fused=False, fp8=True)
+    _check(c, gpu)
+    c = Case(42 + bs, 4, 3, bs, BF, rot, inter, False, slots, pos, 4 * bs + 8, fused=False, fp8=True)
+    _with_ends(c, ["", "large", "small", "zero", "nan"] + ([] if rot else ["k inf", "v inf"]))
+    _check(c, gpu)
+    pkv.check_device_error()
+    c.ks[::3] = float("nan")
+    c.vs[1::3] = 2.0 ** -127
+    _check(c, gpu, expect=9)
+
+
+def test_steps_of_one_token_with_norm(gpu):
+    slots, pos = runs_of_tokens(np.random.default_rng(1), [(p, 1) for p in range(70)], 16, 400)
+    _check(Case(43, 4, 3, 16, BF, 128, False, True, slots, pos, 400, fp8=True), gpu)
+
+
+@pytest.mark.parametrize("hkv", [1, 3, 20])
+@pytest.mark.parametrize("bs", [16, 32])
+@pytest.mark.parametrize("single", [False, True])
+def test_runs_found_in_wide_windows(gpu, bs, hkv, single):
+    """A checked batch repeated until a warp's window is a block and it has several heads: runs of every length, steps
+    of one token, padding and rows with infinities among them give the bytes that the batch alone gives."""
+    rng = np.random.default_rng(bs + hkv)
+    lens = np.ones(40, dtype=int) if single else rng.choice([1, 1, 2, 7, bs - 1, bs, bs + 1, 3 * bs], 40)
+    spans = [(int(rng.integers(0, 2 * bs)), int(n)) for n in lens]
+    slots, pos = runs_of_tokens(rng, spans, bs, 240)
+    for at, n in ((7, 3), (20, 1), (30, 50)):
+        slots[at:at], pos[at:at] = [-1] * n, [0] * n
+    c = Case(50 + hkv, 0, hkv, bs, BF, 0, False, False, slots, pos, 240, fused=False, fp8=True)
+    _with_ends(c, [""] * 11 + ["k inf"] + [""] * 6 + ["v inf"])
+    if hkv < 20:
+        _check(c, gpu)
+    d = c.to_dev(gpu)
+    reps = -(-31 * 2 * 6080 // (hkv * len(slots)))
+    big = {x: torch.cat([d[x]] * reps) for x in ("k", "v", "k_scales", "v_scales")}
+    for x in ("k_cache", "v_cache"):
+        big[x] = torch.cat([d[x].view(torch.uint8)] * reps).view(torch.float8_e4m3fn)
+    s = d["slot_mapping"]
+    big["slot_mapping"] = torch.cat([torch.where(s < 0, s, s + i * 240 * bs) for i in range(reps)])
+    pkv.paged_kv_append_rope_fp8(**{**d, **big})
+    pkv.paged_kv_append_rope_fp8(**d)
+    assert pkv.check_device_error() == 0
+    for x in ("k_cache", "v_cache", "k_scales", "v_scales"):
+        one, all_ = (t.view(torch.uint8) if t.element_size() == 1 else t for t in (d[x], big[x]))
+        assert (all_.view(reps, *one.shape) == one).all(), x
