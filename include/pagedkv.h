@@ -295,9 +295,10 @@ pkv_status paged_attention_decode(const void* q, const void* k_cache, const void
  * (paged_attention_workspace_bytes), the errors and the limits are those of
  * paged_attention_decode.  partition_size is the most tokens of a split-K
  * partition: a sequence with more is cut into as few equal parts as that
- * allows; 0 chooses as paged_attention_decode does, counting this kernel's own
- * resident CTAs, so paged_attention_plan and paged_attention_partition_size
- * need not agree.  The values enter the products exactly (as 16-bit floats),
+ * allows; 0 chooses 512 to 4096 tokens by num_seqs, the heads and
+ * max_context_len, for this kernel's own resident CTAs, so
+ * paged_attention_plan and paged_attention_partition_size need not agree
+ * (a max_context_len near the longest context chooses best).  The values enter the products exactly (as 16-bit floats),
  * the scales as 32-bit factors.
  */
 pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,

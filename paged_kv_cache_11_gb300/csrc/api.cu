@@ -1,7 +1,9 @@
 // api.cu -- the C ABI declared in include/pagedkv.h: argument checks on the
 // host, TMA descriptor encoding, the per-device error word, and dispatch to
 // the kernels in decode.cu and append_copy.cu.
+#include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <atomic>
 #include <mutex>
@@ -181,10 +183,9 @@ static int sm_count() {
 // max_context_len) still fill the GPU's resident decode CTAs at least twice;
 // longer partitions amortise each CTA's start-up, shorter ones balance the
 // load.  The workspace is always sized for 512 (the smallest choice).
-static int resolve_partition(int32_t partition_size, int64_t rows, int32_t max_context_len,
-                             int ctas_per_sm = kDecodeCtasPerSm) {
+static int resolve_partition(int32_t partition_size, int64_t rows, int32_t max_context_len) {
     if (partition_size != 0) return partition_size;
-    const int64_t slots = (int64_t)(sm_count() > 0 ? sm_count() : 148) * ctas_per_sm;
+    const int64_t slots = (int64_t)(sm_count() > 0 ? sm_count() : 148) * kDecodeCtasPerSm;
     int best = kAutoPartition;
     for (int P = 1024; P <= 4096; P *= 2) {
         const int64_t units = rows * (((int64_t)max_context_len + P - 1) / P);
@@ -207,6 +208,43 @@ static int resolve_prefix_partition(int64_t tiles, int32_t max_prefix_len) {
     return best;
 }
 
+// Tokens per partition of the 8-bit decode: the cheapest of a few sizes, by a
+// cost in tokens that a resident CTA streams.  A part costs its tokens and 400
+// more for its start and end.  The host knows only the longest context, so it
+// weighs two guesses: all rows that long (0.7), which run in waves, a wave
+// filled to f taking 0.4 + f of a full one, at most 1; and rows evenly spread
+// up to it (0.3), which keep every CTA busy but for a tail of 0.9 of the
+// longest part.  Over 28 batches the choice is 2% above the best of these
+// sizes, resolve_partition's rule 13%; us, that rule and this: 48 rows of 1024
+// tokens of 8 KV heads 28.4, 20.4; 8 of 8192 36.5, 28.6; 1 of 32768 21.6,
+// 17.3; 4 of 65536 103.3, 94.0; 40 of 100 to 3000 35.0, 29.6; 64 of 512 to
+// 4096 the same; it lost most at 12 of 3000 to 9000: 38.7, 42.1.
+static int resolve_partition_fp8(int32_t partition_size, int64_t rows, int32_t max_context_len, int ctas_per_sm) {
+    if (partition_size != 0) return partition_size;
+    const double slots = (double)(sm_count() > 0 ? sm_count() : 148) * ctas_per_sm;
+    const auto wave = [](double f) { return std::min(1.0, 0.4 + f); };
+    int best = kAutoPartition;
+    double least = 0;
+    for (const int P : {512, 640, 768, 896, 1024, 1280, 1536, 2048, 4096}) {
+        const auto parts = [&](double len) { return std::ceil(std::max(len, 1.0) / P); };
+        const double most = parts(max_context_len);
+        const double waves = rows * most / slots, full = std::floor(waves);
+        const double equal = (full + (waves > full ? wave(waves - full) : 0)) * (max_context_len / most + 400);
+        double units = 0, tokens = 0, longest = 0;
+        for (int k = 1; k <= 8; ++k) {  // eighths of the longest context
+            const double len = max_context_len * (k / 8.0), n = parts(len);
+            units += n, tokens += len, longest = std::max(longest, len / n);
+        }
+        const double load = rows * units / 8 / slots;
+        const double spread = load > 1 ? load * (tokens / units + 400) + 0.9 * (longest + 400)
+                                       : wave(load) * (longest + 400);
+        const double cost = 0.7 * equal + 0.3 * spread;
+        if (P == kAutoPartition || cost < least) best = P, least = cost;
+        if (most <= 1) break;  // larger ones change nothing
+    }
+    return best;
+}
+
 // How a decode call divides its work (see paged_attention_plan).
 struct Plan {
     int kind;        // PKV_PLAN_*
@@ -214,17 +252,21 @@ struct Plan {
     int max_parts;   // split-K partitions of the longest sequence
 };
 
-static Plan make_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t head_tiles, int32_t max_context_len,
-                      int32_t partition_size, int ctas_per_sm = kDecodeCtasPerSm) {
+static Plan plan_of(int partition, int32_t max_context_len) {
     Plan pl;
-    const int64_t groups = (int64_t)num_seqs * num_kv_heads * head_tiles;  // (sequence, head group) rows
-    pl.partition = resolve_partition(partition_size, groups, max_context_len, ctas_per_sm);
+    pl.partition = partition;
     pl.max_parts = max_context_len == 0 ? 1 : (max_context_len + pl.partition - 1) / pl.partition;
     if (pl.max_parts <= 1)
         pl.kind = PKV_PLAN_SINGLE;
     else
         pl.kind = pl.max_parts <= kFuseMergeMaxParts ? PKV_PLAN_SPLIT : PKV_PLAN_SPLIT_REDUCE;
     return pl;
+}
+
+static Plan make_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t head_tiles, int32_t max_context_len,
+                      int32_t partition_size) {
+    const int64_t groups = (int64_t)num_seqs * num_kv_heads * head_tiles;  // (sequence, head group) rows
+    return plan_of(resolve_partition(partition_size, groups, max_context_len), max_context_len);
 }
 
 }  // namespace pkv
@@ -625,8 +667,11 @@ pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
         !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
         return PKV_ERR_INVALID_ARG;
-    const Plan pl = make_plan(num_seqs, cache->num_kv_heads, head_tiles, max_context_len, partition_size,
-                              kDecodeFp8CtasPerSm);
+    // (tiles of 16 heads hold one CTA less on an SM)
+    const int per_sm = decode_head_tile(group) == 16 ? kDecodeFp8CtasPerSm - 1 : kDecodeFp8CtasPerSm;
+    const Plan pl = plan_of(resolve_partition_fp8(partition_size, (int64_t)num_seqs * cache->num_kv_heads * head_tiles,
+                                                  max_context_len, per_sm),
+                            max_context_len);
     const bool split = pl.kind != PKV_PLAN_SINGLE;
     const size_t need =
         paged_attention_workspace_bytes(num_seqs, num_q_heads, kHeadDim, max_context_len, partition_size);
