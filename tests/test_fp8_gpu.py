@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import paged_kv_cache_11_gb300 as pkv
-from tests.fp8_helpers import D, Case, cos_sin_table, decode_inputs, decode_ref, to64
+from tests.fp8_helpers import D, Case, cos_sin_table, decode_inputs, decode_ref, runs_of_tokens, to64
 
 pytestmark = pytest.mark.gpu
 BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -45,6 +45,19 @@ def test_head_groups(gpu, hq, hkv, bs):
 def test_partitions(gpu, P):
     inp = decode_inputs(P, (1500, 0, 700, 33, 1), 8, 2, 16, BF)
     _check(inp, gpu, partition_size=P)
+
+
+@pytest.mark.parametrize("P", [640, 768, 896, 1280, 1536, 2048])
+def test_partitions_that_the_automatic_choice_takes(gpu, P):
+    _check(decode_inputs(P, (P - 1, P, P + 1, 2 * P + 17, 0, 1), 4, 1, 16, BF), gpu, partition_size=P)
+    _check(decode_inputs(P + 1, (3 * P + 33, 5), 2, 2, 32, FP), gpu, partition_size=P)
+
+
+@pytest.mark.parametrize("n,longest,hq,hkv,bs", [(1, 9000, 8, 1, 16), (40, 700, 4, 2, 32), (9, 3000, 16, 1, 16), (3, 6000, 3, 3, 32)])
+def test_automatic_partitions_of_ragged_batches(gpu, n, longest, hq, hkv, bs):
+    lens = np.random.default_rng(n).integers(0, longest + 1, n).tolist()
+    lens[0] = longest
+    _check(decode_inputs(n + 60, lens, hq, hkv, bs, BF), gpu)
 
 
 @pytest.mark.parametrize("out_dtype", [F32, BF, FP])
@@ -263,6 +276,32 @@ def test_streams(gpu):
             for i in range(4) for s in streams]                        # calls at once, a workspace each
     torch.cuda.synchronize()
     assert all(torch.equal(o, ref) for o in outs)
+
+
+def test_calls_on_two_streams_at_once(gpu):
+    """Writes into two pools and split decodes of both, issued to two streams side by side, as alone."""
+    lens = (1200, 900, 40, 1)
+    ins = [_dev(decode_inputs(70 + i, lens, 8, 2, 16, BF), gpu) for i in range(2)]
+    alone = [pkv.paged_attention_decode_fp8(**x, scale=SCALE, partition_size=128) for x in ins]
+    slots, pos = runs_of_tokens(np.random.default_rng(5), [(0, 70), (16, 1), (3, 40)], 16, 12)
+    cases = [Case(80 + i, 4, 2, 16, BF, 64, False, True, slots, pos, 12, fp8=True) for i in range(2)]
+    rows = [c.to_dev(gpu) for c in cases]
+    for d, c in zip(rows, cases):
+        pkv.paged_kv_append_rope_fp8(**d)
+    fresh = [[c.to_dev(gpu) for _ in range(6)] for c in cases]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream(gpu) for _ in range(2)], [[], []]
+    for r in range(6):
+        for i, st in enumerate(streams):
+            pkv.paged_kv_append_rope_fp8(**fresh[i][r], stream=st)
+            outs[i].append(pkv.paged_attention_decode_fp8(**ins[i], scale=SCALE, partition_size=128, stream=st))
+    torch.cuda.synchronize()
+    assert pkv.check_device_error() == 0
+    for i in range(2):
+        for r in range(6):
+            assert torch.equal(outs[i][r], alone[i])
+            for n in ("q_out", "k_cache", "v_cache", "k_scales", "v_scales"):
+                assert torch.equal(fresh[i][r][n].view(torch.uint8), rows[i][n].view(torch.uint8)), n
 
 
 def test_blocks_past_4_gib(gpu):
