@@ -14,9 +14,9 @@
 // normed tokens of 64/8 heads (680 MB) in 104 us, 6.5 TB/s.  The 8-bit write
 // waits on more: a block's scale needs all of its new rows before the first
 // byte, a chain of loads and exchanges for each run of tokens: 16384 tokens of
-// 32/8 heads (378 MB) in 67.9 us, 5.6 TB/s; 777 normed ones of 40/40 heads (40
-// MB) in 16.4 us, 12.9 of them the keys' and values' (issue slots 37% used,
-// three warps to a scheduler); a step of 256 sequences in 3.0 us.
+// 32/8 heads (378 MB) in 64.2 us, 5.9 TB/s; 777 normed ones of 40/40 heads (40
+// MB) in 14.5 us (issue slots some 40% used, three or four warps to a
+// scheduler); a step of 256 sequences in 3.0 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -91,10 +91,9 @@ __device__ __forceinline__ void values_of(const Row& x, float (&f)[8]) {
     }
 }
 
-template <bool kBF16, bool kInter>
-__device__ __forceinline__ Row widen_row(uint2 a, uint2 b) {
-    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
-    float f[8];
+template <bool kBF16>
+__device__ __forceinline__ void widen8(uint4 x, float (&f)[8]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         if constexpr (kBF16) {
@@ -105,6 +104,12 @@ __device__ __forceinline__ Row widen_row(uint2 a, uint2 b) {
             f[2 * k] = h.x, f[2 * k + 1] = h.y;
         }
     }
+}
+
+template <bool kBF16, bool kInter>
+__device__ __forceinline__ Row widen_row(uint2 a, uint2 b) {
+    float f[8];
+    widen8<kBF16>(make_uint4(a.x, a.y, b.x, b.y), f);
     return row_of<kInter>(f);
 }
 
@@ -450,82 +455,144 @@ __device__ __noinline__ void write_any_run(const RopeParams& p, int64_t t0, int 
     }
 }
 
-// A run of `count` <= BS neighbouring tokens from t0 on, all of them good, of
-// keys (kKeys) or values of KV head h; `off` and `pos` are lane l's token t0 +
-// l's row and position.  False, and nothing written, where a value is
-// infinite.
+// The largest magnitude among a warp's eight words of 16-bit pairs so far: NaN
+// counts for nothing, an infinity does.
+template <bool kBF16>
+__device__ __forceinline__ uint32_t top16(uint32_t a, uint32_t w) {
+    uint32_t r;
+    if constexpr (kBF16)
+        asm("{\n\t.reg .b32 m;\n\tabs.bf16x2 m, %2;\n\tmax.bf16x2 %0, %1, m;\n\t}" : "=r"(r) : "r"(a), "r"(w));
+    else
+        asm("{\n\t.reg .b32 m;\n\tabs.f16x2 m, %2;\n\tmax.f16x2 %0, %1, m;\n\t}" : "=r"(r) : "r"(a), "r"(w));
+    return r;
+}
+
+// A lane's 16 bytes of every other row of `rows` to shared memory, 512 bytes
+// apart, asynchronously.
+__device__ __forceinline__ void copy_rows(uint32_t to, const uint16_t* from, int64_t step, int rows) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (2 * j < rows)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512 * j), "l"(from + j * step) : "memory");
+}
+
+// The larger of the magnitudes that the two warps of a 32-row block found.
+__device__ __forceinline__ float meet_max(float a, float (*meet)[2], int& turn) {
+    const int warp = threadIdx.x >> 5;
+    turn ^= 1;  // one meeting's barrier lies between two uses of a place
+    if ((threadIdx.x & 31) == 0) meet[turn][warp & 1] = a;
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+    return fmaxf(meet[turn][0], meet[turn][1]);
+}
+
+// A run of `count` <= BS neighbouring tokens from t0 on, all of them good, its
+// keys (do_k), its values (do_v) or both, of KV head h; `off_l` and `pos_l` are
+// lane l's token t0 + l's row and position.  Returns which are left to
+// write_any_run, nothing written (bit 0: keys, 1: values): those with an
+// infinity.
 //
-// A warp has 16 rows of a run at most.  They are copied to shared memory
-// (`stage`, the warp's own 8 KiB) together, turned there into 32-bit values,
-// which take the place of the rows, and become bytes once the largest
-// magnitude is known.  (Turning them twice cost 17 us more for 16384 tokens of
-// 8 KV heads; kept in registers they spilled; a CTA for each window, its runs'
-// magnitudes meeting in shared memory, took 61 us for keys and values against
-// 45.)  The two warps of a 32-row block meet at a barrier, `meet` is where they
-// leave their magnitudes.
+// A warp has 16 rows of a run at most.  Values and keys are copied to the two
+// halves of `stage`, the warp's own 8 KiB, at once; the values become bytes as
+// they are while the keys are still on the way.  The keys are turned into
+// 32-bit values, which take the whole stage, and become bytes once the largest
+// magnitude is known.  (One after the other through the same code, values as
+// 32-bit too: 777 tokens of 40 heads 16.5 us against 14.5, 16384 of 8 heads
+// 68.0 against 64.2.  Turning keys twice cost 17 us more for the latter; kept
+// in registers they spilled; a CTA for each window, its runs' magnitudes
+// meeting in shared memory, took 61 us for keys and values against 45.)  The two warps of a 32-row block meet at a
+// barrier, `meet` is where they leave their magnitudes.
 template <bool kBF16, bool kInter, int BS>
-__device__ __forceinline__ bool write_run(const RopeParams& p, uint4* stage, float* meet, int64_t t0, int count,
-                                          int off_l, int pos_l, int first, int blk, int h, bool is_k) {
+__device__ __forceinline__ uint32_t write_run(const RopeParams& p, uint4* stage, float (*meet)[2], int& turn,
+                                              int64_t t0, int count, int off_l, int pos_l, int first, int blk, int h,
+                                              bool do_k, bool do_v) {
     const int lane = threadIdx.x & 31, i = lane & 15, hf = lane >> 4, warp = threadIdx.x >> 5;
     const int r0 = BS == 32 ? 16 * (warp & 1) : 0;  // the warp's first row
     const int mine = min(count - r0, 16);           // its rows (none: <= 0)
-    const QuadPos qp = quad_pos<kInter>(p, i);
-    const int64_t stride = is_k ? p.k_stride : p.v_stride;
-    const uint16_t* from = (is_k ? p.k : p.v) + (t0 + r0 + hf) * stride + h * kHeadDim + 8 * i;
-    const uint32_t to = smem_addr(stage + lane);
+    const int64_t tile_no = (int64_t)blk * p.num_kv_heads + h;
+    uint32_t left = 0;
     __syncwarp();  // the warp is done with what the stage held
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (2 * j + hf < mine)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512 * j), "l"(from + 2 * j * stride)
-                         : "memory");
-    float* scale = (is_k ? p.k_scales : p.v_scales) + (int64_t)blk * p.num_kv_heads + h;
-    const float old = first > 0 ? *scale : 0.f;
-    const bool norm = is_k && p.k_norm;
-    Row weight;
-    if (norm) weight = widen_row<kBF16, kInter>(ldg8(p.k_norm + qp.a), ldg8(p.k_norm + qp.b));
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncwarp();  // every lane has read `old`, too
-    // Pair j of rows lies in bytes 512j .. 512j + 511 of the stage, its 32-bit
-    // values go to 1024j .. 1024j + 1023: from the last pair down, over rows
-    // that are done.  An odd last row is done by both halves.
-    float a = 0.f;
+    const uint32_t to = smem_addr(stage + lane);
+    if (do_v) copy_rows(to, p.v + (t0 + r0 + hf) * p.v_stride + h * kHeadDim + 8 * i, 2 * p.v_stride, mine - hf);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (do_k) copy_rows(to + 4096, p.k + (t0 + r0 + hf) * p.k_stride + h * kHeadDim + 8 * i, 2 * p.k_stride, mine - hf);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (do_v) {
+        float* scale = p.v_scales + tile_no;
+        const float old = first > 0 ? *scale : 0.f;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();  // every lane has read `old`, too
+        uint32_t m = 0u;
 #pragma unroll 1
-    for (int j = (mine - 1) >> 1; j >= 0; --j) {
-        const int r = min(2 * j + hf, mine - 1);
-        const uint16_t* row = reinterpret_cast<const uint16_t*>(stage) + r * kHeadDim;
-        Row y = widen_row<kBF16, kInter>(*reinterpret_cast<const uint2*>(row + qp.a),
-                                         *reinterpret_cast<const uint2*>(row + qp.b));
-        if (is_k) {
-            const Turn turn = load_turn(p, qp, __shfl_sync(0xffffffffu, pos_l, r0 + r), i);
-            norm_turn(p, qp, norm, weight, turn, 0xffffffffu, y);
+        for (int j = 0; 2 * j < mine; ++j) {
+            const uint4 x = stage[16 * min(2 * j + hf, mine - 1) + i];
+            m = top16<kBF16>(top16<kBF16>(top16<kBF16>(top16<kBF16>(m, x.x), x.y), x.z), x.w);
         }
-        a = top(a, y);
-        __syncwarp();
-        ulonglong2* at = reinterpret_cast<ulonglong2*>(stage + 64 * j + lane);
-        at[0] = make_ulonglong2(y.v[0], y.v[1]);
-        at[32] = make_ulonglong2(y.v[2], y.v[3]);
-        __syncwarp();
-    }
-    a = warp_max(a);
-    if constexpr (BS == 32) {
-        if (lane == 0) meet[warp & 1] = a;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
-        a = fmaxf(meet[0], meet[1]);
-    }
-    if (a == INFINITY) return false;
-    uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
-                    ((int64_t)blk * p.num_kv_heads + h) * (BS * kHeadDim);
-    const float inv = 1.f / settle_scale(p, scale, old, tile, a, first, r0 == 0);
+        float f[8];
+        widen8<kBF16>(make_uint4(m, 0u, 0u, 0u), f);
+        float a = warp_max(fmaxf(f[0], f[1]));
+        if constexpr (BS == 32) a = meet_max(a, meet, turn);
+        if (a == INFINITY) {
+            left = 2u;
+        } else {
+            uint8_t* tile = static_cast<uint8_t*>(p.v_cache) + tile_no * (BS * kHeadDim) + 8 * i;
+            const float inv = 1.f / settle_scale(p, scale, old, tile - 8 * i, a, first, r0 == 0);
+            const f32x2 ii = pack_f32x2(inv, inv);
 #pragma unroll 1
-    for (int j = 0; 2 * j < mine; ++j) {
-        const ulonglong2* at = reinterpret_cast<const ulonglong2*>(stage + 64 * j + lane);
-        const ulonglong2 lo = at[0], hi = at[32];
-        Row y;
-        y.v[0] = lo.x, y.v[1] = lo.y, y.v[2] = hi.x, y.v[3] = hi.y;
-        store_e4m3<kInter>(tile + __shfl_sync(0xffffffffu, off_l, r0 + min(2 * j + hf, mine - 1)) * kHeadDim, qp, y, inv);
+            for (int j = 0; 2 * j < mine; ++j) {
+                const int r = min(2 * j + hf, mine - 1);
+                widen8<kBF16>(stage[16 * r + i], f);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) unpack_f32x2(mul2(pack_f32x2(f[e], f[e + 1]), ii), f[e], f[e + 1]);
+                *reinterpret_cast<uint2*>(tile + __shfl_sync(0xffffffffu, off_l, r0 + r) * kHeadDim) =
+                    make_uint2(e4m3_quad(f[0], f[1], f[2], f[3]), e4m3_quad(f[4], f[5], f[6], f[7]));
+            }
+        }
+        __syncwarp();  // the keys' values may take the rows' place
     }
-    return true;
+    if (do_k) {
+        const QuadPos qp = quad_pos<kInter>(p, i);
+        float* scale = p.k_scales + tile_no;
+        const float old = first > 0 ? *scale : 0.f;
+        Row weight;
+        if (p.k_norm) weight = widen_row<kBF16, kInter>(ldg8(p.k_norm + qp.a), ldg8(p.k_norm + qp.b));
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();  // every lane has read `old`, too
+        // Pair j of rows lies in bytes 512j .. 512j + 511 of the stage's second
+        // half, its 32-bit values go to 1024j .. 1024j + 1023 of the whole: over
+        // the values' rows and pairs that are done.  An odd last row is done
+        // by both halves.
+        float a = 0.f;
+#pragma unroll 1
+        for (int j = 0; 2 * j < mine; ++j) {
+            const int r = min(2 * j + hf, mine - 1);
+            const uint16_t* row = reinterpret_cast<const uint16_t*>(stage + 256) + r * kHeadDim;
+            Row y = widen_row<kBF16, kInter>(*reinterpret_cast<const uint2*>(row + qp.a),
+                                             *reinterpret_cast<const uint2*>(row + qp.b));
+            const Turn tn = load_turn(p, qp, __shfl_sync(0xffffffffu, pos_l, r0 + r), i);
+            norm_turn(p, qp, p.k_norm != nullptr, weight, tn, 0xffffffffu, y);
+            a = top(a, y);
+            __syncwarp();
+            ulonglong2* at = reinterpret_cast<ulonglong2*>(stage + 64 * j + lane);
+            at[0] = make_ulonglong2(y.v[0], y.v[1]);
+            at[32] = make_ulonglong2(y.v[2], y.v[3]);
+            __syncwarp();
+        }
+        a = warp_max(a);
+        if constexpr (BS == 32) a = meet_max(a, meet, turn);
+        if (a == INFINITY) return left | 1u;
+        uint8_t* tile = static_cast<uint8_t*>(p.k_cache) + tile_no * (BS * kHeadDim);
+        const float inv = 1.f / settle_scale(p, scale, old, tile, a, first, r0 == 0);
+#pragma unroll 1
+        for (int j = 0; 2 * j < mine; ++j) {
+            const ulonglong2* at = reinterpret_cast<const ulonglong2*>(stage + 64 * j + lane);
+            const ulonglong2 lo = at[0], hi = at[32];
+            Row y;
+            y.v[0] = lo.x, y.v[1] = lo.y, y.v[2] = hi.x, y.v[3] = hi.y;
+            store_e4m3<kInter>(tile + __shfl_sync(0xffffffffu, off_l, r0 + min(2 * j + hf, mine - 1)) * kHeadDim, qp, y,
+                               inv);
+        }
+    }
+    return left;
 }
 
 // A run of one token, as a decode step has: its keys of KV head h by the warp's
@@ -653,12 +720,12 @@ __device__ __forceinline__ void do_runs(const RopeParams& p, uint4* stage, float
             } else {
                 const int first = __reduce_min_sync(0xffffffffu, lane < count ? off : BS);
 #pragma unroll 1
-                for (int item = item0; item < item1; ++item) {
-                    turn ^= 1;  // one meeting's barrier lies between two uses of a place
-                    if (!write_run<kBF16, kInter, BS>(p, stage, meet[turn], t0 + x - 1, count, off, pos, first, blk,
-                                                      item >> 1, (item & 1) == 0) &&
-                        !second)
-                        left |= 1u << (item - item0);
+                for (int item = item0; item < item1;) {
+                    const bool do_k = !(item & 1), do_v = !do_k || item + 1 < item1;
+                    const uint32_t rest = write_run<kBF16, kInter, BS>(p, stage, meet, turn, t0 + x - 1, count, off, pos,
+                                                                       first, blk, item >> 1, do_k, do_v);
+                    if (!second) left |= (do_k ? rest : rest >> 1) << (item - item0);
+                    item += do_k && do_v ? 2 : 1;
                 }
             }
         } else if (second) {
@@ -714,13 +781,14 @@ static cudaError_t launch_rope_fp8(const RopeParams& p, cudaStream_t stream) {
     // Teams of a warp, or of two, for keys and values.  As long as all are
     // resident at once, one for each token and item.  With more, a head's keys
     // and values share one (256 sequences' next tokens: 3.0 us, 4.4 without;
-    // but 5.5 us, 7.3 with, for a chunk of 100 tokens, which has few runs);
+    // but 5.2 us, 6.3 with, for a chunk of 100 tokens, which has few runs);
     // then windows grow towards a block's tokens, and items again, while
     // enough teams are left: 16384 tokens of 8 KV heads in blocks of 16 took
     // 67.9 us with 8192 teams, 70.9 with 4096, 777 of 40 heads in blocks of 32
-    // 16.4 with 1960, 18.4 with 1040, 19.5 with 3920.
+    // 16.4 with 1960, 18.4 with 1040, 19.5 with 3920 (5000 tokens of 8 heads
+    // 36.5 us with 4560 as the bound, 37.8 with 6080).
     constexpr int64_t kResident = 2432;
-    const int64_t enough = p.block_size == 16 ? 6080 : 1520;
+    const int64_t enough = p.block_size == 16 ? 4560 : 1520;
     const int64_t all = 2 * (int64_t)p.num_kv_heads, pair = p.block_size / 16;
     const auto teams = [&](int w, int n) { return (p.num_tokens + w - 1) / w * ((all + n - 1) / n); };
     int window = 1, items = teams(1, 1) * pair > kResident ? 2 : 1;
