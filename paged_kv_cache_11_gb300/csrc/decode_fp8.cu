@@ -431,6 +431,10 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
             }
         // ---- O^T += vs V8^T P^T, unit by unit
         uint32_t vw[4][4], ph[NH][2], pl[NH][2];
+        if (vref == 0.f) {  // the first unit that has one: the larger of the pair's, so that both ratios fit
+            const float big = fmaxf(fabsf(scl.y), fabsf(scl.w));
+            if (big > 0.f && big < INFINITY) vref = big, vinv = 1.f / big;
+        }
         float r0 = scl.y * vinv, r1 = scl.w * vinv;
         const bool keep = fabsf(r0) <= 1.f && fabsf(r0) >= 0x1p-6f && fabsf(r1) <= 1.f && fabsf(r1) >= 0x1p-6f;
         if (!keep) {  // the first unit by itself, at the unit that its scale sets
