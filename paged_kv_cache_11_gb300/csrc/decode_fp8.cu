@@ -128,26 +128,23 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     // partition_size, and none is a short rest that leaves the others waiting.
     // (part < nparts, and nparts - 1 full parts hold less than the row, so
     // every part has a token.)
-    const int per = (((L - 1) / p.block_size + nparts) / nparts) * p.block_size;
-    const int tok0 = part * per;
-    const int len = min(L - tok0, per);  // tokens of this part
+    const bool whole = p.block_size == 32;  // a pair is one block (else two of 16)
+    const int sh = whole ? 5 : 4;
+    const int per_blocks = (((L - 1) >> sh) + nparts) / nparts, first_block = part * per_blocks;
+    const int len = min(L - (first_block << sh), per_blocks << sh);  // tokens of this part
     const int npairs = (len + 31) / 32;
-    const bool whole = p.block_size == 32;  // a pair is one block (else two)
     const bool write_partial = p.split && nparts > 1;
-
-    int* flags = reinterpret_cast<int*>(smem + S::kFlags);  // [0]: bad block id, [1]: last-arrival verdict
-    if (tid == 0) flags[0] = 0;
-    __syncthreads();
 
     // ---- this warp's pairs: warp, warp + NW, ...
     const int mine = npairs > warp ? (npairs - 1 - warp) / NW + 1 : 0;
-    const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks_per_seq + tok0 / p.block_size;
-    const int nblk = (len - 1) / p.block_size + 1;  // blocks of this partition
+    const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks_per_seq + first_block;
+    const int nblk = ((len - 1) >> sh) + 1;  // blocks of this partition
     const uint64_t policy = l2_policy_evict_first();
     uint8_t* ring = smem + warp * (NST * kF8StageBytes);
     const uint32_t ring_sa = smem_addr(ring);
 
     int ids0 = 0, ids1 = 0;
+    bool bad_id = false;
     // Block ids of the warp's n-th pair: 32 pairs are read at a time, a lane
     // each.  A pair without a second unit names its first block twice (its
     // tokens are masked).
@@ -162,8 +159,8 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
             bad = ids0 < 0 || (int64_t)ids0 >= p.num_blocks || ids1 < 0 || (int64_t)ids1 >= p.num_blocks;
             if (bad) ids0 = ids1 = 0;  // the output is zeroed below
         }
-        if (__any_sync(0xffffffffu, bad) && lane == 0) {
-            atomicOr(flags, 1);
+        if (bad) {
+            bad_id = true;
             record_error(p.err, PKV_DEVERR_BLOCK_ID);
         }
     };
@@ -457,10 +454,10 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     }
     acc_finish(a);
     cp_async_wait<0>();
-    __syncthreads();  // every ring is free: its memory takes the warps' states
+    // every ring is free: its memory takes the warps' states
+    const int fl = __syncthreads_or(bad_id);
 
     // ---- merge the warps' states, as the decode kernel does
-    const int fl = flags[0];
     float* red = reinterpret_cast<float*>(smem);  // [NW][HT][kRedStride]
     float* ml = red + NW * HT * kRedStride;       // [NW][HT][3]: m, l, vref
     float* wts = ml + NW * HT * 3;                // [HT][NW + 1]: weights, then the row's lse
@@ -528,16 +525,17 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
         }
     }
     if (write_partial && p.fuse_merge) {
+        int* verdict = reinterpret_cast<int*>(smem + S::kFlags);  // is this the last to arrive
         __syncthreads();
         if (tid == 0) {
             fence_acq_rel_gpu();
             const bool last =
                 arrive_last(p.merge_ctr + (int64_t)s * p.num_kv_heads * p.head_tiles + ygrp, p.epoch, nparts);
             if (last) fence_acq_rel_gpu();
-            flags[1] = last ? 1 : 0;
+            *verdict = last ? 1 : 0;
         }
         __syncthreads();
-        if (flags[1]) merge_row_partials(p, s, h0, rows, nparts, reinterpret_cast<float*>(smem));
+        if (*verdict) merge_row_partials(p, s, h0, rows, nparts, reinterpret_cast<float*>(smem));
     }
 }
 
