@@ -197,25 +197,18 @@ def _marshal():
         loader = importlib.machinery.ExtensionFileLoader("_marshal", str(path))
         mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
         loader.exec_module(mod)
-        mod.bind(str(LIB_PATH))
+        mod.bind(str(LIB_PATH), PagedKVError)
         _MARSHAL = mod
     return _MARSHAL
 
 
-def _call(name: str, stream, first: torch.Tensor, fn, *args):
-    """fn(*args), on ``stream`` (None: the tensors' device's current stream).  Within a given stream the call's
-    allocations belong to it too: none is handed out again while the call still runs."""
-    if stream is None:
-        r = fn(*args)
-    else:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=first.device)
-        _require(stream.device == first.device, "stream belongs to another device")
-        with torch.cuda.stream(stream):
-            r = fn(*args)
-    if type(r) is int:
-        raise PagedKVError(r, name)
-    return r
+def _on(stream, first: torch.Tensor):
+    """What a call on ``stream`` runs in: its allocations belong to the stream too, and none is handed out again while
+    the call still runs."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+    _require(stream.device == first.device, "stream belongs to another device")
+    return torch.cuda.stream(stream)
 
 
 def paged_kv_append_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
@@ -232,9 +225,12 @@ def paged_kv_append_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tenso
     are not read).  Rows of padding tokens (negative slots)
     are left as they were; ``q_out`` may be ``q`` where that is contiguous.
     """
-    return _call("paged_kv_append_rope", stream, k_cache, (_MARSHAL or _marshal()).append_rope, False, q, k, v,
-                 positions, cos_sin, slot_mapping, k_cache, v_cache, None, None, q_norm, k_norm, norm_eps, interleaved,
-                 q_out)
+    if stream is not None:
+        with _on(stream, k_cache):
+            return paged_kv_append_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_norm, k_norm,
+                                        norm_eps, interleaved, q_out)
+    return (_MARSHAL or _marshal()).append_rope(False, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, None,
+                                                None, q_norm, k_norm, norm_eps, interleaved, q_out)
 
 
 def paged_kv_append_rope_fp8(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
@@ -249,9 +245,12 @@ def paged_kv_append_rope_fp8(q: torch.Tensor | None, k: torch.Tensor, v: torch.T
     A block starts afresh when its first row is written, and its scales follow the rows it takes on (the header has
     the rule); a block's tokens stand together in ``slot_mapping``.
     """
-    return _call("paged_kv_append_rope_fp8", stream, k_cache, (_MARSHAL or _marshal()).append_rope, True, q, k, v,
-                 positions, cos_sin, slot_mapping, k_cache, v_cache, k_scales, v_scales, q_norm, k_norm, norm_eps,
-                 interleaved, q_out)
+    if stream is not None:
+        with _on(stream, k_cache):
+            return paged_kv_append_rope_fp8(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scales,
+                                            v_scales, q_norm, k_norm, norm_eps, interleaved, q_out)
+    return (_MARSHAL or _marshal()).append_rope(True, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache,
+                                                k_scales, v_scales, q_norm, k_norm, norm_eps, interleaved, q_out)
 
 
 def paged_attention_workspace_bytes(num_seqs: int, num_q_heads: int, head_dim: int, max_context_len: int,
@@ -320,9 +319,12 @@ def paged_attention_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                                out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """paged_attention_decode over float8_e4m3fn caches with one fp32 scale per (block, KV head)
     (paged_kv_append_rope_fp8); q is bf16 or fp16."""
-    return _call("paged_attention_decode_fp8", stream, q, (_MARSHAL or _marshal()).decode_fp8, q, k_cache, v_cache,
-                 k_scales, v_scales, block_tables, context_lens, scale, out, max_context_len, partition_size, workspace,
-                 out_dtype)
+    if stream is not None:
+        with _on(stream, q):
+            return paged_attention_decode_fp8(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale,
+                                              out, max_context_len, partition_size, workspace, out_dtype)
+    return (_MARSHAL or _marshal()).decode_fp8(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale,
+                                               out, max_context_len, partition_size, workspace, out_dtype)
 
 
 def paged_attention_append_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -483,8 +485,10 @@ def copy_blocks_fp8(k_caches: torch.Tensor | Sequence[torch.Tensor], v_caches: t
                     src_dst_pairs: torch.Tensor, stream=None) -> None:
     """copy_blocks for float8_e4m3fn caches: block dst := block src in every layer, K and V, with its scales."""
     k, v, ks, vs = ([t] if isinstance(t, torch.Tensor) else list(t) for t in (k_caches, v_caches, k_scales, v_scales))
-    _call("copy_blocks_fp8", stream, src_dst_pairs, (_MARSHAL or _marshal()).copy_blocks_fp8, k, v, ks, vs,
-          src_dst_pairs)
+    if stream is not None:
+        with _on(stream, src_dst_pairs):
+            return copy_blocks_fp8(k, v, ks, vs, src_dst_pairs)
+    (_MARSHAL or _marshal()).copy_blocks_fp8(k, v, ks, vs, src_dst_pairs)
 
 
 def swap_blocks(src_k: torch.Tensor | Sequence[torch.Tensor], src_v: torch.Tensor | Sequence[torch.Tensor],

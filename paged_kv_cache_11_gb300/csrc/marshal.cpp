@@ -4,9 +4,10 @@
 // A step of a few short sequences takes the GPU 2 to 6 us; the same checks in
 // Python took the host 9 to 18 us, and 52 us for the caches of 40 layers.
 //
-// Every call returns its output (or None), or the pkv_status as an int where
-// the library refused; ValueError where a tensor is not what the call takes.
-// The library itself is libpagedkv.so, whose entry points bind() looks up.
+// Every call returns its output (or None); it raises ValueError where a tensor
+// is not what the call takes, and binding.py's error, which bind() is given,
+// where the library refused.  The library itself is libpagedkv.so, whose entry
+// points bind() looks up.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -30,6 +31,7 @@ decltype(&paged_kv_append_rope_fp8) p_append_rope_fp8 = nullptr;
 decltype(&paged_attention_decode_fp8) p_decode_fp8 = nullptr;
 decltype(&paged_attention_workspace_bytes) p_workspace_bytes = nullptr;
 decltype(&copy_blocks_fp8) p_copy_blocks_fp8 = nullptr;
+PyObject* refused = nullptr;  // exception of (status, call)
 
 // Becomes Python's ValueError.
 struct BadValue : std::runtime_error {
@@ -102,8 +104,15 @@ int64_t token_stride(const at::Tensor& t, int64_t n, int64_t heads, int64_t d, c
     return n > 1 ? t.stride(0) : heads * d;
 }
 
-PyObject* status_or(pkv_status st, const at::Tensor* out) {
-    if (st != PKV_OK) return PyLong_FromLong(st);
+PyObject* result(pkv_status st, const char* call, const at::Tensor* out) {
+    if (st != PKV_OK) {
+        PyObject* e = PyObject_CallFunction(refused, "is", (int)st, call);
+        if (e) {
+            PyErr_SetObject(refused, e);
+            Py_DECREF(e);
+        }
+        return nullptr;
+    }
     if (!out) Py_RETURN_NONE;
     return THPVariable_Wrap(*out);
 }
@@ -181,7 +190,7 @@ PyObject* append_rope(PyObject* const* a) {
                            static_cast<const int64_t*>(ptr(&slots)), n, ptr(q_out), ptr(&k_cache), ptr(&v_cache), &cache,
                            &rope, stream);
     Py_END_ALLOW_THREADS;
-    return status_or(st, q_out);
+    return result(st, fp8 ? "paged_kv_append_rope_fp8" : "paged_kv_append_rope", q_out);
 }
 
 // q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out, max_context_len, partition_size,
@@ -235,7 +244,7 @@ PyObject* decode_fp8(PyObject* const* a) {
                       dtype_code(out->scalar_type()), &cache, part, ptr(workspace), workspace ? workspace->nbytes() : 0,
                       stream);
     Py_END_ALLOW_THREADS;
-    return status_or(st, out);
+    return result(st, "paged_attention_decode_fp8", out);
 }
 
 // k_caches, v_caches, k_scales, v_scales (lists of one tensor per layer), src_dst_pairs
@@ -275,7 +284,7 @@ PyObject* copy_fp8(PyObject* const* a) {
                            reinterpret_cast<float* const*>(ptrs[3].data()), n_layers,
                            static_cast<const int64_t*>(ptr(&pairs)), n_pairs, &cache, stream);
     Py_END_ALLOW_THREADS;
-    return status_or(st, nullptr);
+    return result(st, "copy_blocks_fp8", nullptr);
 }
 
 // No C++ exception passes into Python.
@@ -301,9 +310,10 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
 }
 
-PyObject* bind(PyObject*, PyObject* path) {
-    const char* p = PyUnicode_AsUTF8(path);
-    if (!p) return nullptr;
+PyObject* bind(PyObject*, PyObject* args) {
+    const char* p;
+    PyObject* error;
+    if (!PyArg_ParseTuple(args, "sO", &p, &error)) return nullptr;
     void* lib = dlopen(p, RTLD_NOW | RTLD_LOCAL);  // the handle that ctypes opened
     if (!lib) {
         PyErr_SetString(PyExc_RuntimeError, dlerror());
@@ -320,11 +330,13 @@ PyObject* bind(PyObject*, PyObject* path) {
         PyErr_SetString(PyExc_RuntimeError, "libpagedkv.so lacks an entry point");
         return nullptr;
     }
+    Py_INCREF(error);
+    Py_XSETREF(refused, error);
     Py_RETURN_NONE;
 }
 
 PyMethodDef methods[] = {
-    {"bind", bind, METH_O, "Looks the entry points up in libpagedkv.so (its path)."},
+    {"bind", bind, METH_VARARGS, "Looks the entry points up in libpagedkv.so: its path, and the error of a refusal."},
     {"append_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<append_rope, 16>)), METH_FASTCALL, nullptr},
     {"decode_fp8", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<decode_fp8, 13>)), METH_FASTCALL, nullptr},
     {"copy_blocks_fp8", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<copy_fp8, 5>)), METH_FASTCALL, nullptr},
