@@ -221,9 +221,8 @@ def paged_kv_append_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tenso
 
     q [num_tokens, num_q_heads, 128] (or None), k and v [num_tokens, num_kv_heads, 128] may be slices of one fused
     projection: only a token's heads must be contiguous.  ``cos_sin`` is fp32 [max_position, rot_dim], the cosines of
-    a position's rot_dim / 2 angles before their sines (None: no rotation, positions
-    are not read).  Rows of padding tokens (negative slots)
-    are left as they were; ``q_out`` may be ``q`` where that is contiguous.
+    a position's rot_dim / 2 angles before their sines (None: no rotation, positions are not read).  Rows of padding
+    tokens (negative slots) are left as they were; ``q_out`` may be ``q`` where that is contiguous.
     """
     if stream is not None:
         with _on(stream, k_cache):
