@@ -18,8 +18,8 @@
 // vref and multiplies p by vs / vref, which fp16 holds without loss while the
 // ratio is in [2^-6, 1].  Only a scale outside of that moves O to a new
 // reference (a test that the whole warp passes together), so the products
-// accumulate in O directly.  (Adding each unit's product, times vs, to O took
-// 32 more multiply-adds per unit, and a wait for the products' end.)
+// need no scale after them.  (Adding each unit's product, times vs, to O took
+// 32 more multiply-adds per unit: 83 us against 78 for 64 sequences.)
 //
 // A unit of work is 16 tokens of one (block, KV head) tile: 2 KiB of K and 2
 // KiB of V.  The warps of a CTA take units in turn, each through a ring of its
@@ -36,7 +36,7 @@
 //
 // Bytes bound long contexts: 8 sequences of 131072 tokens, 64/8 heads (2.15 GB)
 // in 327 us, 6.6 TB/s.  Short ones lose to each CTA's start and end, some 6 us:
-// 64 of 512 to 4096 tokens, 32/8 heads (304 MB) in 60 us, 5.1 TB/s.  Other
+// 64 of 512 to 4096 tokens, 32/8 heads (304 MB) in 60.5 us, 5.0 TB/s.  Other
 // shapes of the CTA were slower there (warps, stages, CTAs per SM: 2, 2, 6
 // 64.2 us; 2, 3, 4 67.5; 4, 3, 2 71.5; 3, 2, 4 65.0 against 62.4 then).
 #include <atomic>
@@ -82,6 +82,31 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
         : "r"(w));
 }
 
+// d = a b, the first product of a sum.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// d += a b
+__device__ __forceinline__ void mma_next(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// a += b, two values in one instruction.
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%0, %1};\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "add.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
+
 template <int HT>
 struct DecodeFp8Smem {
     static constexpr int kRing = kF8Warps * kF8Stages * kF8StageBytes;
@@ -92,7 +117,13 @@ struct DecodeFp8Smem {
 };
 
 // NH: 8-head n-tiles per CTA (1: up to 8 query heads of a group, 2: up to 16).
-template <int NH>
+// kRound: for fp32 outputs.  The tensor cores round towards zero with every
+// step, by a part of what they add to; products added to O at once shrink it
+// by 1e-6 over 2048 tokens (7 sequences of 12859 tokens: 1.2e-6 off in all,
+// nothing beside a 16-bit output's rounding).  Summed pair by pair and added to
+// nearest they leave 5.5e-7, for 63.5 us against 60.5 (64 sequences of 512 to
+// 4096 tokens).
+template <int NH, bool kRound>
 __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8CtasPerSm - 1)
     decode_fp8_kernel(const __grid_constant__ DecodeFp8Params fp) {
     const DecodeParams& p = fp.d;
@@ -253,19 +284,54 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     acc_reset(a);
     float vref = 0.f, vinv = 0.f;  // O's unit and its reciprocal; 0: O is zero and has none
 
-    // O^T += V8^T P^T of one unit: tokens 2t, 2t + 1 (k 0-7), 2t + 8, 2t + 9
-    auto pv = [&](const uint32_t (&vw)[4][4], const uint32_t (&ph)[NH][2], const uint32_t (&pl)[NH][2]) {
+    // O^T += V8^T P^T: tokens 2t, 2t + 1 (k 0-7), 2t + 8, 2t + 9 of a unit
+    using V = uint32_t[4][4];
+    using P = uint32_t[NH][2];
+    const auto v_operand = [](const V& vw, int mt, uint32_t (&af)[4]) {
+        const int j = mt >> 1;
+        const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;  // bytes 2, 3 or 0, 1 of both tokens, paired
+        e4m3x4_to_f16(__byte_perm(vw[0][j], vw[1][j], sel), af[0], af[1]);
+        e4m3x4_to_f16(__byte_perm(vw[2][j], vw[3][j], sel), af[2], af[3]);
+    };
+    const auto pv = [&](const V& vw, const P& ph, const P& pl) {
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
-            const int j = mt >> 1;
-            const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;  // bytes 2, 3 or 0, 1 of both tokens, paired
             uint32_t af[4];
-            e4m3x4_to_f16(__byte_perm(vw[0][j], vw[1][j], sel), af[0], af[1]);
-            e4m3x4_to_f16(__byte_perm(vw[2][j], vw[3][j], sel), af[2], af[3]);
+            v_operand(vw, mt, af);
 #pragma unroll
             for (int m = 0; m < NH; ++m) {
                 mma_16816<false>(a.o[mt][m], af, ph[m][0], ph[m][1]);
                 mma_16816<false>(a.o[mt][m], af, pl[m][0], pl[m][1]);
+            }
+        }
+    };
+    // ... kRound: both units of a pair, summed by themselves, two sums side by
+    // side, and added to O to nearest.
+    const auto pv_pair = [&](const V (&vw)[2], const P (&ph)[2], const P (&pl)[2]) {
+#pragma unroll
+        for (int mt = 0; mt < 8; mt += 2) {
+            uint32_t af[2][2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) v_operand(vw[u], mt + k, af[k][u]);
+#pragma unroll
+            for (int m = 0; m < NH; ++m) {
+                float sum[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) mma_first(sum[k], af[k][0], pl[0][m][0], pl[0][m][1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) mma_next(sum[k], af[k][1], pl[1][m][0], pl[1][m][1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) mma_next(sum[k], af[k][0], ph[0][m][0], ph[0][m][1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) mma_next(sum[k], af[k][1], ph[1][m][0], ph[1][m][1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float(&o)[4] = a.o[mt + k][m];
+                    add2(o[0], o[1], sum[k][0], sum[k][1]);
+                    add2(o[2], o[3], sum[k][2], sum[k][3]);
+                }
             }
         }
     };
@@ -426,31 +492,47 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
                     }
                 a.l[m][c] += sum;
             }
-        // ---- O^T += vs V8^T P^T, unit by unit
-        uint32_t vw[4][4], ph[NH][2], pl[NH][2];
+        // ---- O^T += vs V8^T P^T
         if (vref == 0.f) {  // the first unit that has one: the larger of the pair's, so that both ratios fit
             const float big = fmaxf(fabsf(scl.y), fabsf(scl.w));
             if (big > 0.f && big < INFINITY) vref = big, vinv = 1.f / big;
         }
         float r0 = scl.y * vinv, r1 = scl.w * vinv;
         const bool keep = fabsf(r0) <= 1.f && fabsf(r0) >= 0x1p-6f && fabsf(r1) <= 1.f && fabsf(r1) >= 0x1p-6f;
-        if (!keep) {  // the first unit by itself, at the unit that its scale sets
-            r0 = take_scale(scl.y);
-            split(sc[0], r0, ph, pl);
-            load_v(stage, valid, vw);
-            pv(vw, ph, pl);
+        P ph[2], pl[2];
+        if constexpr (kRound) {
+            V vw[2];
+            load_v(stage, valid, vw[0]);
+            load_v(stage + kF8UnitBytes, valid - 16, vw[1]);
+#pragma unroll 1
+            for (int pass = keep ? 1 : 0; pass < 2; ++pass) {  // (not keep: the units one after the other)
+                if (!keep) {
+                    r0 = pass == 0 ? take_scale(scl.y) : 0.f;
+                    r1 = pass == 1 && valid > 16 ? take_scale(scl.w) : 0.f;
+                }
+                split(sc[0], r0, ph[0], pl[0]);
+                split(sc[1], r1, ph[1], pl[1]);
+                pv_pair(vw, ph, pl);
+            }
+        } else {
+            V vw;
+            if (!keep) {  // the first unit by itself, at the unit that its scale sets
+                r0 = take_scale(scl.y);
+                split(sc[0], r0, ph[0], pl[0]);
+                load_v(stage, valid, vw);
+                pv(vw, ph[0], pl[0]);
 #pragma unroll
-            for (int m = 0; m < NH; ++m) sc[0][m][0] = sc[0][m][1] = sc[0][m][2] = sc[0][m][3] = 0.f;
-            r1 = valid > 16 ? take_scale(scl.w) : 0.f;
-            r0 = 0.f;
+                for (int m = 0; m < NH; ++m) sc[0][m][0] = sc[0][m][1] = sc[0][m][2] = sc[0][m][3] = 0.f;
+                r1 = valid > 16 ? take_scale(scl.w) : 0.f;
+                r0 = 0.f;
+            }
+            split(sc[0], r0, ph[0], pl[0]);
+            split(sc[1], r1, ph[1], pl[1]);
+            load_v(stage, valid, vw);
+            pv(vw, ph[0], pl[0]);
+            load_v(stage + kF8UnitBytes, valid - 16, vw);
+            pv(vw, ph[1], pl[1]);
         }
-        uint32_t ph1[NH][2], pl1[NH][2];
-        split(sc[0], r0, ph, pl);
-        split(sc[1], r1, ph1, pl1);
-        load_v(stage, valid, vw);
-        pv(vw, ph, pl);
-        load_v(stage + kF8UnitBytes, valid - 16, vw);
-        pv(vw, ph1, pl1);
     }
     acc_finish(a);
     cp_async_wait<0>();
@@ -539,11 +621,11 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     }
 }
 
-template <int NH>
+template <int NH, bool kRound>
 static cudaError_t launch_decode_fp8_t(const DecodeFp8Params& fp, cudaStream_t stream, int* launches) {
     const DecodeParams& p = fp.d;
     constexpr int kSmem = DecodeFp8Smem<8 * NH>::kTotal;
-    auto kern = decode_fp8_kernel<NH>;
+    auto kern = decode_fp8_kernel<NH, kRound>;
     // the attribute is a device's and stays: set on the first call there
     static std::atomic<uint64_t> set{0};
     int dev = 0;
@@ -564,8 +646,10 @@ static cudaError_t launch_decode_fp8_t(const DecodeFp8Params& fp, cudaStream_t s
 }
 
 cudaError_t launch_decode_fp8(const DecodeFp8Params& p, cudaStream_t stream, int* launches) {
-    return decode_head_tile(p.d.group) == 16 ? launch_decode_fp8_t<2>(p, stream, launches)
-                                             : launch_decode_fp8_t<1>(p, stream, launches);
+    const bool wide = decode_head_tile(p.d.group) == 16;
+    if (p.d.out_dtype == PKV_FP32)
+        return wide ? launch_decode_fp8_t<2, true>(p, stream, launches) : launch_decode_fp8_t<1, true>(p, stream, launches);
+    return wide ? launch_decode_fp8_t<2, false>(p, stream, launches) : launch_decode_fp8_t<1, false>(p, stream, launches);
 }
 
 }  // namespace pkv
