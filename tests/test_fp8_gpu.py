@@ -123,6 +123,16 @@ def test_one_heavy_token_among_many_light_ones(gpu):
     _check(inp, gpu, scale=0.3, partition_size=9008)
 
 
+def test_long_sums_keep_their_size(gpu):
+    """fp32 outputs of one part of 16384 tokens are not smaller than they should be: the products round towards zero,
+    each of the 4 of a pair of units by less than 2^-23 of their sum, and nothing else rounds to one side."""
+    inp = decode_inputs(90, (16384,), 8, 1, 16, BF)
+    out = _check(inp, gpu, partition_size=16384)
+    ref = decode_ref(inp, SCALE, F32)[0]
+    size = (to64(out) * ref).sum() / (ref * ref).sum() - 1
+    assert abs(size) <= 4 * 2.0 ** -23 + 2.0 ** -21      # (the second: 1024 outputs' own rounding, on average)
+
+
 def test_length_one_is_the_scaled_value(gpu):
     inp = decode_inputs(9, (1, 1, 1), 4, 2, 16, BF)
     out = pkv.paged_attention_decode_fp8(**_dev(inp, gpu), scale=SCALE)
