@@ -289,8 +289,13 @@ pkv_status paged_attention_decode(const void* q, const void* k_cache, const void
  *     out[s][h][:] = sum_{t<L} softmax_t(scale * ks * q[s][h] . K[t]) vs V[t]
  * q_dtype:   PKV_BF16 or PKV_FP16, the type of q.
  * k_scales, v_scales: [num_blocks][num_kv_heads] fp32 device memory; any
- *            finite values, powers of two or not.  Those of blocks outside
- *            the sequences' contexts are never read.
+ *            finite values, powers of two or not, of either sign, or zero.
+ *            The V scales that a head meets in one context, but for zeros,
+ *            should lie within 2^64 of one another: beyond that, values of
+ *            small scales may count as zeros where large ones have weight in
+ *            some head.  scale * ks * (the largest q of a head) and the scores
+ *            must lie in fp32's range.  Those of blocks outside the
+ *            sequences' contexts are never read.
  * cache->dtype is PKV_E4M3.  The other arguments, the workspace
  * (paged_attention_workspace_bytes), the errors and the limits are those of
  * paged_attention_decode.  partition_size is the most tokens of a split-K

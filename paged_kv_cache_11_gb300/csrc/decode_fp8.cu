@@ -367,30 +367,44 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
                 if (2 * t + (r & 1) + 8 * (r >> 1) >= valid) vw[r][0] = vw[r][1] = vw[r][2] = vw[r][3] = 0u;
         }
     };
-    // Moves O to the unit of scale vs where it has to; returns vs / vref.
+    // What P is multiplied by for a unit of 16 tokens of scale vs, where a scale
+    // of the pair is not in [2^-6, 1] of O's unit; O moves to a new unit where it
+    // has to.  A larger scale becomes O's unit.  A smaller one does, too, if O,
+    // as it is, stays below 2^110 in it: the scales alone do not tell, as a block
+    // of large scale may have no weight, and moves add up.  (Sums of 2^20 tokens
+    // stay below 2^44 of the largest scale among them, so that scales within 2^64
+    // of one another always move.)  Else it is folded in the unit that O has, and
+    // fp16 keeps of it what it can.
     auto take_scale = [&](float vs) {
-        float ratio = vs * vinv;
-        if (fabsf(ratio) <= 1.f && fabsf(ratio) >= 0x1p-6f) return ratio;
-        if (vref == 0.f) {
-            vref = vs;  // a scale of zero adds nothing and sets nothing
-            vinv = vref == 0.f ? 0.f : 1.f / vref;
-            ratio = vref == 0.f ? 0.f : 1.f;
-        } else if (!(fabsf(ratio) < 0x1p-60f)) {
-            // (a scale 2^-60 times the unit or less is folded as it is: what
-            // it adds is lost beside the unit, and O times the inverse could
-            // leave fp32's range)
-            const float f = vref / vs;
+        if (vs == 0.f) return 0.f;  // adds nothing and sets nothing
+        const float r = vs / vref;
+        float f = vref / vs;
+        if (vref == 0.f || fabsf(r) > 1.f) {
+        } else if (fabsf(r) >= 0x1p-6f) {
+            return r;
+        } else {
+            float top = 0.f;
 #pragma unroll
             for (int m = 0; m < NH; ++m)
 #pragma unroll
                 for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) a.o[mt][m][e] *= f;
-            vref = vs;
-            vinv = 1.f / vref;
-            ratio = 1.f;
+                    for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(a.o[mt][m][e]));
+            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+            if (top == 0.f)
+                f = 1.f;
+            else if (!(top * fabsf(f) <= 0x1p110f))
+                return r;
         }
-        return ratio;
+#pragma unroll
+        for (int m = 0; m < NH; ++m)
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a.o[mt][m][e] *= f;
+        vref = vs;
+        vinv = 1.f / vs;
+        return 1.f;
     };
 
     int st = 0, st_in = NST - 1;  // stage of pair n and of pair n + NST - 1
@@ -576,7 +590,7 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
         }
         const float inv = 1.f / sum;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) wts[tid * (NW + 1) + w] = f[w] * inv * ml[(w * HT + tid) * 3 + 2];
+        for (int w = 0; w < NW; ++w) wts[tid * (NW + 1) + w] = f[w] * inv;
         // A NaN among the scores makes the outputs NaN; the merge would pass
         // over a partition whose lse is one, so it gets a finite lse.
         const float lse = M + log2f(sum) - kF8Lift;
@@ -589,12 +603,13 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
         if (!fl) {
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-                const float ww = wts[hr * (NW + 1) + w];
+                // (weight and unit one after the other: their product may leave fp32's range where the output does not)
+                const float ww = wts[hr * (NW + 1) + w], vr = ml[(w * HT + hr) * 3 + 2];
                 const float4 r = *reinterpret_cast<const float4*>(red + (w * HT + hr) * kRedStride + 4 * c4);
-                o.x += ww * r.x;
-                o.y += ww * r.y;
-                o.z += ww * r.z;
-                o.w += ww * r.w;
+                o.x += vr * (ww * r.x);
+                o.y += vr * (ww * r.y);
+                o.z += vr * (ww * r.z);
+                o.w += vr * (ww * r.w);
             }
         }
         if (write_partial) {

@@ -97,6 +97,73 @@ def test_a_block_of_huge_values_without_weight(gpu, at):
     _check(inp, gpu)
 
 
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+@pytest.mark.parametrize("hq,bs", [(4, 16), (4, 32), (16, 16)])
+@pytest.mark.parametrize("at", [0, 3, 14])
+@pytest.mark.parametrize("kind", ["no weight", "zeros"])
+@pytest.mark.parametrize("e", [62, 64])
+def test_a_block_of_far_larger_scale_that_adds_nothing(gpu, e, kind, at, hq, bs, out_dtype):
+    """A block whose scale is 2^62 or 2^64 times the others', without weight or of zeros: the others keep all they add,
+    whether it comes before them or after."""
+    inp = decode_inputs(61, (500,), hq, 1, bs, BF)
+    b = int(inp["block_tables"][0, at])
+    inp["v_scales"][:] = 1.0
+    inp["v_scales"][b] = 2.0 ** e
+    if kind == "zeros":
+        inp["v_cache"].view(torch.uint8)[b] = 0
+    else:
+        inp["q"][:] = inp["q"][:, :1].abs()
+        inp["k_cache"].view(torch.uint8)[b] |= 0x80                   # every key of the block against the query
+        inp["k_scales"][b] = 2.0
+    _check(inp, gpu, out_dtype=out_dtype)
+    _check(inp, gpu, out_dtype=out_dtype, partition_size=256)
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("vs", [(2.0 ** 60, 2.0, 2.0 ** -56), (2.0 ** 60, 2.0, 2.0 ** -58), (1.0, 2.0 ** -59, 2.0 ** -118),
+                                (2.0 ** -58, 2.0 ** 60, 2.0), (3e18, 7.0, 1e-17, 5e-36)])
+def test_scales_that_fall_step_by_step(gpu, vs, hq, out_dtype):
+    """Scales that fall from one stretch of a context to the next, each by less than 2^64, all with weight: the output is
+    that of the large ones, and finite."""
+    inp = decode_inputs(62, (128 * len(vs) * 2,), hq, 1, 16, BF)
+    n = inp["block_tables"].shape[1]
+    for i, b in enumerate(inp["block_tables"][0].tolist()):
+        inp["v_scales"][b] = vs[i * len(vs) // n]
+    _check(inp, gpu, out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+@pytest.mark.parametrize("hq,bs", [(2, 16), (2, 32), (16, 16)])
+@pytest.mark.parametrize("at", [0, 5, 14])
+def test_heads_that_see_scales_far_apart(gpu, at, hq, bs, out_dtype):
+    """Some heads have all their weight on a block of 2^64 times the others' scale, the others none: each is right."""
+    inp = decode_inputs(63, (480,), hq, 1, bs, BF)
+    b = int(inp["block_tables"][0, at])
+    inp["q"][:] = inp["q"][:, :1].abs()
+    inp["q"][:, 1::2] *= -1
+    inp["k_cache"].view(torch.uint8)[b] &= 0x7F
+    inp["k_scales"][b] = 2.0
+    inp["v_scales"][:] = 2.0 ** -20
+    inp["v_scales"][b] = 2.0 ** 44
+    _check(inp, gpu, out_dtype=out_dtype)
+    _check(inp, gpu, out_dtype=out_dtype, partition_size=160)
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+@pytest.mark.parametrize("vs", [(2.0 ** -130, 0.0, 1.5 * 2.0 ** -130, -(2.0 ** -129)), (0.0, 2.0 ** -149, 2.0 ** -130),
+                                (2.0 ** 118, 0.0, 1.7 * 2.0 ** 117), (2.0 ** -64, 2.0 ** -140, 0.0)])
+def test_scales_at_the_ends_of_fp32(gpu, vs, out_dtype):
+    """Scales without a finite reciprocal, zeros beside them, and scales near the largest number.  (Outputs stay above
+    2^-126: the roundings of a few subnormal terms, 2^-150 each, are nothing beside 2^-20 of the values.)"""
+    inp = decode_inputs(64, (400, 30), 4, 1, 16, BF)
+    n = inp["v_scales"].shape[0]
+    for b in range(n):
+        inp["v_scales"][b] = vs[b % len(vs)]
+    _check(inp, gpu, out_dtype=out_dtype)
+    _check(inp, gpu, out_dtype=out_dtype, partition_size=64)
+
+
 @pytest.mark.parametrize("factor", [1e-30, 1e-4, 20.0])
 def test_small_and_large_queries(gpu, factor):
     inp = decode_inputs(5, (300, 40), 8, 2, 16, BF)
