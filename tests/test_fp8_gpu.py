@@ -130,7 +130,8 @@ def test_scales_that_fall_step_by_step(gpu, vs, hq, out_dtype):
     n = inp["block_tables"].shape[1]
     for i, b in enumerate(inp["block_tables"][0].tolist()):
         inp["v_scales"][b] = vs[i * len(vs) // n]
-    _check(inp, gpu, out_dtype=out_dtype)
+    for P in (0, 4096):                                               # (the second: one part, all falls in each warp)
+        _check(inp, gpu, out_dtype=out_dtype, partition_size=P)
 
 
 @pytest.mark.parametrize("out_dtype", [F32, BF])
