@@ -104,6 +104,19 @@ int64_t token_stride(const at::Tensor& t, int64_t n, int64_t heads, int64_t d, c
     return n > 1 ? t.stride(0) : heads * d;
 }
 
+// Other threads run while a call is issued.  (The calls of the C ABI throw
+// nothing; what may throw -- a tensor without memory of its own has no pointer
+// to give, a size may not fit -- is evaluated before the lock is given up, and
+// the lock comes back however the scope is left.)
+class Unlocked {
+    PyThreadState* const state_ = PyEval_SaveThread();
+
+  public:
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state_); }
+};
+
 PyObject* result(pkv_status st, const char* call, const at::Tensor* out) {
     if (st != PKV_OK) {
         PyObject* e = PyObject_CallFunction(refused, "is", (int)st, call);
@@ -176,20 +189,19 @@ PyObject* append_rope(PyObject* const* a) {
         q_out = &made;
     }
     void* stream = c10::cuda::getCurrentCUDAStream(dev.index).stream();
+    void *p_q = ptr(q), *p_k = ptr(&k), *p_v = ptr(&v), *p_qn = ptr(q_norm), *p_kn = ptr(k_norm), *p_out = ptr(q_out),
+         *p_kc = ptr(&k_cache), *p_vc = ptr(&v_cache);
+    const auto p_pos = static_cast<const int64_t*>(ptr(positions)), p_slots = static_cast<const int64_t*>(ptr(&slots));
+    const auto p_table = static_cast<const float*>(ptr(cos_sin));
+    const auto p_ks = static_cast<float*>(ptr(k_scales)), p_vs = static_cast<float*>(ptr(v_scales));
     pkv_status st;
-    Py_BEGIN_ALLOW_THREADS;
-    if (fp8)
-        st = p_append_rope_fp8(ptr(q), ptr(&k), ptr(&v), static_cast<const int64_t*>(ptr(positions)),
-                               static_cast<const float*>(ptr(cos_sin)), ptr(q_norm), ptr(k_norm),
-                               static_cast<const int64_t*>(ptr(&slots)), n, ptr(q_out), ptr(&k_cache), ptr(&v_cache),
-                               static_cast<float*>(ptr(k_scales)), static_cast<float*>(ptr(v_scales)), &cache, &rope,
-                               stream);
-    else
-        st = p_append_rope(ptr(q), ptr(&k), ptr(&v), static_cast<const int64_t*>(ptr(positions)),
-                           static_cast<const float*>(ptr(cos_sin)), ptr(q_norm), ptr(k_norm),
-                           static_cast<const int64_t*>(ptr(&slots)), n, ptr(q_out), ptr(&k_cache), ptr(&v_cache), &cache,
-                           &rope, stream);
-    Py_END_ALLOW_THREADS;
+    {
+        const Unlocked unlocked;
+        st = fp8 ? p_append_rope_fp8(p_q, p_k, p_v, p_pos, p_table, p_qn, p_kn, p_slots, n, p_out, p_kc, p_vc, p_ks, p_vs,
+                                     &cache, &rope, stream)
+                 : p_append_rope(p_q, p_k, p_v, p_pos, p_table, p_qn, p_kn, p_slots, n, p_out, p_kc, p_vc, &cache, &rope,
+                                 stream);
+    }
     return result(st, fp8 ? "paged_kv_append_rope_fp8" : "paged_kv_append_rope", q_out);
 }
 
@@ -235,15 +247,17 @@ PyObject* decode_fp8(PyObject* const* a) {
         }
     }
     void* stream = c10::cuda::getCurrentCUDAStream(dev.index).stream();
+    void *p_q = ptr(&q), *p_kc = ptr(&k_cache), *p_vc = ptr(&v_cache), *p_out = ptr(out), *p_space = ptr(workspace);
+    const auto p_ks = static_cast<const float*>(ptr(&k_scales)), p_vs = static_cast<const float*>(ptr(&v_scales));
+    const auto p_tables = static_cast<const int32_t*>(ptr(&tables)), p_lens = static_cast<const int32_t*>(ptr(&lens));
+    const int32_t width = narrow(tables.size(1)), q_type = dtype_code(q.scalar_type()), out_type = dtype_code(out->scalar_type());
+    const size_t space_bytes = workspace ? workspace->nbytes() : 0;
     pkv_status st;
-    Py_BEGIN_ALLOW_THREADS;
-    st = p_decode_fp8(ptr(&q), dtype_code(q.scalar_type()), ptr(&k_cache), ptr(&v_cache),
-                      static_cast<const float*>(ptr(&k_scales)), static_cast<const float*>(ptr(&v_scales)),
-                      static_cast<const int32_t*>(ptr(&tables)), narrow(tables.size(1)),
-                      static_cast<const int32_t*>(ptr(&lens)), num_seqs, hq, max_len, (float)scale, ptr(out),
-                      dtype_code(out->scalar_type()), &cache, part, ptr(workspace), workspace ? workspace->nbytes() : 0,
-                      stream);
-    Py_END_ALLOW_THREADS;
+    {
+        const Unlocked unlocked;
+        st = p_decode_fp8(p_q, q_type, p_kc, p_vc, p_ks, p_vs, p_tables, width, p_lens, num_seqs, hq, max_len, (float)scale,
+                          p_out, out_type, &cache, part, p_space, space_bytes, stream);
+    }
     return result(st, "paged_attention_decode_fp8", out);
 }
 
@@ -278,12 +292,13 @@ PyObject* copy_fp8(PyObject* const* a) {
     const c10::cuda::CUDAGuard guard(dev.index);
     void* stream = c10::cuda::getCurrentCUDAStream(dev.index).stream();
     const int32_t n_layers = narrow(layers), n_pairs = narrow(pairs.numel() / 2);
+    const auto p_pairs = static_cast<const int64_t*>(ptr(&pairs));
     pkv_status st;
-    Py_BEGIN_ALLOW_THREADS;
-    st = p_copy_blocks_fp8(ptrs[0].data(), ptrs[1].data(), reinterpret_cast<float* const*>(ptrs[2].data()),
-                           reinterpret_cast<float* const*>(ptrs[3].data()), n_layers,
-                           static_cast<const int64_t*>(ptr(&pairs)), n_pairs, &cache, stream);
-    Py_END_ALLOW_THREADS;
+    {
+        const Unlocked unlocked;
+        st = p_copy_blocks_fp8(ptrs[0].data(), ptrs[1].data(), reinterpret_cast<float* const*>(ptrs[2].data()),
+                               reinterpret_cast<float* const*>(ptrs[3].data()), n_layers, p_pairs, n_pairs, &cache, stream);
+    }
     return result(st, "copy_blocks_fp8", nullptr);
 }
 
