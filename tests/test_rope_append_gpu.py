@@ -463,3 +463,105 @@ def test_runs_found_in_wide_windows(gpu, bs, hkv, single):
     for x in ("k_cache", "v_cache", "k_scales", "v_scales"):
         one, all_ = (t.view(torch.uint8) if t.element_size() == 1 else t for t in (d[x], big[x]))
         assert (all_.view(reps, *one.shape) == one).all(), x
+
+
+def _check_exact(c, gpu):
+    """Keys that are neither turned nor normed and the same numbers as values: values are checked byte for byte (and the
+    scales), keys have to be the same."""
+    c.v, c.vc, c.vs = c.k.clone(), c.kc.clone(), c.ks.clone()
+    _, d = _run(c, gpu)
+    c.check_pools8(d["k_cache"], d["v_cache"], d["k_scales"], d["v_scales"])
+    assert torch.equal(d["k_scales"], d["v_scales"])
+    assert torch.equal(d["k_cache"].view(torch.uint8), d["v_cache"].view(torch.uint8))
+
+
+@pytest.mark.parametrize("single", [False, True])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("bs", [16, 32])
+def test_rows_under_scales_that_are_no_powers_of_two_are_nearest(gpu, bs, dtype, single):
+    """Rows that join a block whose scale is kept: the stored values are the nearest to y / scale, also where y / scale is
+    next to the middle between two of them (scales are y / middle, rounded, for one y of the block)."""
+    rng = np.random.default_rng(bs)
+    blocks, hkv = 24, 3
+    rows = [(p, 1) for p in range(1, blocks + 1)] if single else [(1 + b % 5, 2 + b % 11) for b in range(blocks)]
+    slots, pos = [], []
+    for b, (p, n) in enumerate(rows):
+        p = 1 + (p - 1) % (bs - 1)
+        for o in range(p, min(p + n, bs)):
+            slots.append(b * bs + o), pos.append(o)
+    c = Case(70, 0, hkv, bs, dtype, 0, False, False, slots, pos, blocks, fused=False, fp8=True)
+    bits = 7 if dtype == BF else 10
+    lowest = -100 if dtype == BF else -6
+    for b in range(blocks):
+        for h in range(hkv):
+            y = (1 + int(rng.integers(0, 2 ** bits)) / 2 ** bits) * 2.0 ** int(rng.integers(lowest, 6))
+            middle = (1 + (2 * int(rng.integers(0, 8)) + 1) / 16) * 2.0 ** int(rng.integers(-5, 7))
+            c.ks[b, h] = [y / middle, 0.3 * 2.0 ** int(rng.integers(-3, 3)), 7.0 / 448, y / middle][(b + h) % 4]
+            s = float(c.ks[b, h])
+            for t in [t for t, x in enumerate(slots) if x // bs == b]:
+                v = (1 + rng.integers(0, 2 ** bits, 128) / 2 ** bits) * 2.0 ** rng.integers(-11, 9, 128)
+                v = np.minimum(v * 2.0 ** np.floor(np.log2(s)), min(400 * s, 6e4)) * rng.choice([-1, 1], 128)
+                v[:8] = y * np.array([1, -1, 0.5, -0.5, 0.25, -2 if middle < 200 else 1, 1, 0])
+                c.k[t, h] = torch.from_numpy(v).to(dtype)
+    _check_exact(c, gpu)
+
+
+@pytest.mark.parametrize("single", [False, True])
+def test_rows_moved_from_a_scale_that_is_no_power_of_two(gpu, single):
+    """Held values, every byte among them, go to the nearest of value * (old / new)."""
+    n = 1 if single else 3
+    slots = [b * 16 + 5 + o for b in range(40) for o in range(n)]
+    c = Case(71, 0, 2, 16, BF, 0, False, False, slots, [0] * len(slots), 40, fused=False, fp8=True)
+    raw = c.kc.view(torch.uint8)
+    raw[:, :, 0, :] = torch.arange(128, dtype=torch.uint8)
+    raw[:, :, 1, :] = torch.arange(128, 256).to(torch.uint8)
+    rng = np.random.default_rng(3)
+    for b in range(40):     # old / new = middle / value, rounded, for one value of the held ones
+        value = (1 + int(rng.integers(0, 8)) / 8) * 2.0 ** int(rng.integers(-2, 8))
+        middle = (1 + (2 * int(rng.integers(0, 8)) + 1) / 16) * 2.0 ** -3
+        c.ks[b, :] = middle / value
+        # (the new rows ask for a scale of 1, or a power of two more where the old one is large)
+        c.k[[t for t, s in enumerate(slots) if s // 16 == b], 0] = 300.0
+        c.k[[t for t, s in enumerate(slots) if s // 16 == b], 1] = 448.0
+    _check_exact(c, gpu)
+
+
+@pytest.mark.parametrize("single", [False, True])
+def test_a_scale_is_kept_up_to_448_times_itself_exactly(gpu, single):
+    """Rows just above what the old scale holds, by less than a 32-bit product 448 * scale can tell, raise it."""
+    n = 1 if single else 2
+    picks = []
+    for m in range(128):
+        a = np.float32((1 + m / 128) * 4.0)
+        old = np.float32(float(a) / 448)
+        if float(old) * 448 >= float(a):
+            old = np.nextafter(old, np.float32(0))
+        if np.float32(448) * old >= a:
+            picks.append((float(a), float(old)))
+    assert len(picks) >= 8
+    slots = [b * 16 + 3 + o for b in range(len(picks)) for o in range(n)]
+    c = Case(72, 0, 1, 16, BF, 0, False, False, slots, [0] * len(slots), len(picks), fused=False, fp8=True)
+    for b, (a, old) in enumerate(picks):
+        c.ks[b, 0] = old
+        c.k[b * n:(b + 1) * n, 0] = 0.25
+        c.k[b * n, 0, 7] = -a
+    _check_exact(c, gpu)
+
+
+@pytest.mark.parametrize("single", [False, True])
+def test_kept_scales_at_the_ends_of_fp32(gpu, single):
+    """The smallest and the largest scales that are kept, powers of two and not, with values down to subnormal ones."""
+    n = 1 if single else 4
+    scales = [2.0 ** -126, 1.3 * 2.0 ** -126, 1.9 * 2.0 ** -120, 2.0 ** 127, 1.9 * 2.0 ** 127, 1.1 * 2.0 ** 122]
+    slots = [b * 16 + 2 + o for b in range(len(scales)) for o in range(n)]
+    c = Case(73, 0, 2, 16, BF, 0, False, False, slots, [0] * len(slots), len(scales), fused=False, fp8=True)
+    rng = np.random.default_rng(5)
+    top = float(torch.finfo(BF).max)
+    for b, s in enumerate(scales):
+        c.ks[b] = s
+        lo = -7 if s < 1 else -11
+        v = (1 + rng.integers(0, 128, (n, 2, 128)) / 128) * 2.0 ** rng.integers(lo, 8, (n, 2, 128))
+        c.k[b * n:(b + 1) * n] = torch.from_numpy(np.minimum(v * 2.0 ** np.floor(np.log2(s)), min(440 * s, top))).to(BF)
+    _check_exact(c, gpu)
+    c.k.neg_()
+    _check_exact(c, gpu)
