@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
     const uint32_t get_v0 = 16 * D + 2 * t * D + ((g ^ (2 * t)) << 4);
     const uint32_t get_v1 = 16 * D + (2 * t + 1) * D + ((g ^ (2 * t + 1)) << 4);
     // V8 of one unit: tokens 2t, 2t + 1, 2t + 8, 2t + 9, dims 16g .. 16g + 15;
-    // rows past the context may hold anything (even NaN): zeros
+    // rows past the context may hold anything (even NaN): zeros, chosen by masks
+    // and not by branches, as the products that follow need the whole warp
     auto load_v = [&](const uint8_t* unit, int valid, uint32_t (&vw)[4][4]) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -363,8 +364,11 @@ __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8Cta
         }
         if (valid < 16) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (2 * t + (r & 1) + 8 * (r >> 1) >= valid) vw[r][0] = vw[r][1] = vw[r][2] = vw[r][3] = 0u;
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t in = 2 * t + (r & 1) + 8 * (r >> 1) < valid ? 0xffffffffu : 0u;
+                vw[r][0] &= in, vw[r][1] &= in, vw[r][2] &= in, vw[r][3] &= in;
+            }
+            __syncwarp();
         }
     };
     // What P is multiplied by for a unit of 16 tokens of scale vs, where a scale
