@@ -543,6 +543,7 @@ __device__ __forceinline__ float meet_max(float a, float (*meet)[2], int& turn) 
     const int warp = threadIdx.x >> 5;
     turn ^= 1;  // one meeting's barrier lies between two uses of a place
     if ((threadIdx.x & 31) == 0) meet[turn][warp & 1] = a;
+    __syncwarp();  // bar.sync takes whole warps
     asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
     return fmaxf(meet[turn][0], meet[turn][1]);
 }
