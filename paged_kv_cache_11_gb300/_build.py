@@ -3,8 +3,9 @@
 * ``libpagedkv.so`` -- the CUDA library behind ``include/pagedkv.h``, compiled
   for sm_103a only (``-gencode arch=compute_103a,code=sm_103a``); the
   translation units compile in parallel and link with the static CUDA runtime.
-* ``_marshal.so`` -- the binding's argument marshalling for the calls on
-  rotated rows and 8-bit pools (C++ against the installed torch).
+* ``_marshal.<versions>.so`` -- the binding's argument marshalling for the
+  calls on rotated rows and 8-bit pools: C++ against the headers of the
+  installed torch and the running Python, whose versions are in its name.
 * ``libpkvgen.so`` -- the seeded input generator (plain C, no CUDA).
 
 Nothing here runs at import time: ``paged_kv_cache_11_gb300`` loads the
@@ -18,6 +19,8 @@ import subprocess
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
+
+from .binding import marshal_name
 
 PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
@@ -82,14 +85,15 @@ def _build_cuda(force: bool, verbose: bool) -> Path:
 
 def build_marshal(force: bool = False) -> Path:
     import torch
+    LIBDIR.mkdir(exist_ok=True)
     src = CSRC / "marshal.cpp"
-    out = LIBDIR / "_marshal.so"
+    out = LIBDIR / marshal_name()
     if not force and not _stale(out, [src, PKG.parent / "include" / "pagedkv.h"]):
         return out
     home = Path(torch.__file__).resolve().parent
     inc = [sysconfig.get_paths()["include"], home / "include", home / "include" / "torch" / "csrc" / "api" / "include",
            Path(_nvcc()).parent.parent / "include"]
-    tmp = out.with_suffix(".so.tmp")
+    tmp = out.with_name(out.name + ".tmp")
     _run(["g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in inc], str(src), "-o",
           str(tmp), f"-L{home / 'lib'}", f"-Wl,-rpath,{home / 'lib'}", "-ltorch_python", "-ltorch", "-ltorch_cpu",

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import sysconfig
 from pathlib import Path
 from typing import Sequence
 
@@ -183,6 +184,13 @@ def paged_kv_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor
                                   _ptr(v_cache), ctypes.byref(desc), _stream(stream)), "paged_kv_append")
 
 
+def marshal_name() -> str:
+    """File of the compiled marshalling.  It goes by what it is compiled against, so that another Python or torch never
+    loads it."""
+    return (f"_marshal.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}"
+            f"-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}.so")
+
+
 _MARSHAL = None
 
 
@@ -190,9 +198,10 @@ def _marshal():
     """The compiled marshalling of the calls below (csrc/marshal.cpp), bound to the library."""
     global _MARSHAL
     if _MARSHAL is None:
-        path = LIB_PATH.parent / "_marshal.so"
+        path = LIB_PATH.parent / marshal_name()
         if not path.exists():
-            raise RuntimeError(f"{path} is not built; run `python -m paged_kv_cache_11_gb300._build` first")
+            raise RuntimeError(f"{path} is not built (for this Python and torch); run "
+                               "`python -m paged_kv_cache_11_gb300._build` first")
         _lib()
         loader = importlib.machinery.ExtensionFileLoader("_marshal", str(path))
         mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
