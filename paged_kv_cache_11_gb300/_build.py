@@ -5,7 +5,8 @@
   translation units compile in parallel and link with the static CUDA runtime.
 * ``_marshal.<versions>.so`` -- the binding's argument marshalling for the
   calls on rotated rows and 8-bit pools: C++ against the headers of the
-  installed torch and the running Python, whose versions are in its name.
+  installed torch and the running Python, whose versions are in its name.  The
+  C library needs neither.
 * ``libpkvgen.so`` -- the seeded input generator (plain C, no CUDA).
 
 Nothing here runs at import time: ``paged_kv_cache_11_gb300`` loads the
@@ -56,14 +57,6 @@ def _stale(target: Path, deps: list[Path]) -> bool:
 
 def build_library(force: bool = False, verbose: bool = False) -> Path:
     LIBDIR.mkdir(exist_ok=True)
-    with ThreadPoolExecutor(1) as ex:  # beside the library's own compilation
-        marshal = ex.submit(build_marshal, force)
-        out = _build_cuda(force, verbose)
-        marshal.result()
-    return out
-
-
-def _build_cuda(force: bool, verbose: bool) -> Path:
     out = LIBDIR / "libpagedkv.so"
     deps = [CSRC / s for s in CUDA_SOURCES] + [CSRC / "pkv_internal.cuh", CSRC / "decode_common.cuh",
                                                 PKG.parent / "include" / "pagedkv.h"]
@@ -116,7 +109,10 @@ def build_generator(force: bool = False) -> Path:
 
 def build_all(force: bool = False) -> None:
     build_generator(force)
-    build_library(force)
+    with ThreadPoolExecutor(1) as ex:  # beside the library's own compilation
+        marshal = ex.submit(build_marshal, force)
+        build_library(force)
+        marshal.result()
 
 
 if __name__ == "__main__":

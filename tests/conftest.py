@@ -40,6 +40,7 @@ def gpu():
         pytest.fail("test marked gpu ran without a CUDA device")
     from paged_kv_cache_11_gb300 import _build
     _build.build_library()
+    _build.build_marshal()
     import paged_kv_cache_11_gb300 as pkv
     pkv.binding._lib()
     return torch.device("cuda:0")

@@ -7,6 +7,27 @@ import torch
 from paged_kv_cache_11_gb300 import _build, binding
 
 
+def _refuse(*a, **k):
+    raise AssertionError("not needed for the C library")
+
+
+def test_the_c_library_needs_no_headers_of_torch(monkeypatch, tmp_path):
+    ran = []
+
+    def run(cmd):
+        ran.append(cmd)
+        Path(cmd[cmd.index("-o") + 1]).touch()
+
+    monkeypatch.setattr(_build, "LIBDIR", tmp_path / "lib")
+    monkeypatch.setattr(_build, "_run", run)
+    monkeypatch.setattr(_build, "_nvcc", lambda: "nvcc")
+    monkeypatch.setattr(_build, "build_marshal", _refuse)
+    assert _build.build_library() == tmp_path / "lib" / "libpagedkv.so"
+    assert len(ran) == len(_build.CUDA_SOURCES) + 1 and all(c[0] == "nvcc" for c in ran)
+    home = str(Path(torch.__file__).resolve().parent)
+    assert not any(home in word for c in ran for word in c)
+
+
 def test_the_marshalling_is_made_for_one_python_and_torch(monkeypatch, tmp_path):
     made = []
 
