@@ -565,3 +565,36 @@ def test_kept_scales_at_the_ends_of_fp32(gpu, single):
     _check_exact(c, gpu)
     c.k.neg_()
     _check_exact(c, gpu)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bs,hkv", [(16, 3), (16, 8), (32, 3), (32, 8)])
+def test_turned_and_normed_keys_in_full_windows(gpu, bs, hkv, inter):
+    """A checked batch of rotated and normed keys, repeated until the launch takes windows of a block less a token and four
+    items (two heads) or more per warp, gives the bytes that the batch alone gives."""
+    rng = np.random.default_rng(7 * bs + hkv)
+    lens = rng.choice([1, 2, 7, bs - 1, bs, bs + 1, 3 * bs], 24)
+    spans = [(int(rng.integers(0, 2 * bs)), int(n)) for n in lens]
+    slots, pos = runs_of_tokens(rng, spans, bs, 160)
+    for at, n in ((9, 2), (40, 1)):
+        slots[at:at], pos[at:at] = [-1] * n, [0] * n
+    c = Case(90 + hkv, 0, hkv, bs, FP if inter else BF, 64 if inter else 128, inter, True, slots, pos, 160, fp8=True)
+    c.ks[::5] *= 1.3                                                  # (no powers of two)
+    c.vs[::7] *= 1.7
+    _check(c, gpu)
+    d = c.to_dev(gpu)
+    n, items, enough = len(slots), 4, {16: 4560, 32: 1520}[bs]
+    groups = -(-2 * hkv // items)
+    reps = -(-enough * (bs - 1) // (groups * n)) + 1
+    assert n * reps // (bs - 1) * groups >= enough                    # what the launch asks for that window and 4 items
+    big = {x: torch.cat([d[x]] * reps) for x in ("k", "v", "positions", "k_scales", "v_scales")}
+    for x in ("k_cache", "v_cache"):
+        big[x] = torch.cat([d[x].view(torch.uint8)] * reps).view(torch.float8_e4m3fn)
+    s = d["slot_mapping"]
+    big["slot_mapping"] = torch.cat([torch.where(s < 0, s, s + i * 160 * bs) for i in range(reps)])
+    pkv.paged_kv_append_rope_fp8(**{**d, **big})
+    pkv.paged_kv_append_rope_fp8(**d)
+    assert pkv.check_device_error() == 0
+    for x in ("k_cache", "v_cache", "k_scales", "v_scales"):
+        one, all_ = (t.view(torch.uint8) if t.element_size() == 1 else t for t in (d[x], big[x]))
+        assert (all_.view(reps, *one.shape) == one).all(), x
