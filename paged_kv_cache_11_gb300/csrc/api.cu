@@ -613,6 +613,7 @@ static pkv_status append_rope_impl(const void* q, const void* k, const void* v, 
     p.rot_dim = rope->rot_dim;
     p.interleaved = rope->interleaved != 0;
     p.norm_eps = rope->norm_eps;
+    p.sms = sm_count() > 0 ? sm_count() : 148;
     int launches = 0;
     const cudaError_t e = launch_rope_append(p, rope->dtype, fp8, static_cast<cudaStream_t>(stream), &launches);
     g_launches += launches;

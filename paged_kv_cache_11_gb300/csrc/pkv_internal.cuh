@@ -178,6 +178,7 @@ struct RopeParams {
     int num_q_heads, num_kv_heads, block_size;
     int rot_dim, interleaved;
     float norm_eps;
+    int sms;                     // of the device
 };
 // dtype: PKV_BF16 or PKV_FP16; fp8: the pool is e4m3 with scales.
 cudaError_t launch_rope_append(const RopeParams& p, int dtype, bool fp8, cudaStream_t stream, int* launches);

@@ -201,8 +201,8 @@ __device__ __forceinline__ Token token_at(const RopeParams& p, int64_t t) {
 // keys or values), by one half-warp: the rows are loaded together, and share
 // the token's slot, angles and weights.  With an 8-bit pool (kQOnly) only the
 // queries are done here.  R = 8 rows ask more of the memory at a time, 4 fill
-// the GPU with less work: 103.8 against 117.0 us for 16384 tokens of 64/8
-// heads, 16.1 against 15.8 us for 1537 of 40/40, 2.6 against 2.0 us for 64 of
+// the GPU with less work: 103.9 against 114.9 us for 16384 tokens of 64/8
+// heads, 16.1 against 15.8 us for 1537 of 40/40, 2.5 against 1.9 us for 64 of
 // 32/8.
 __host__ __device__ __forceinline__ uint32_t row_units(int heads, int R) { return (heads + R - 1) / R; }
 constexpr int64_t kManyRows = 524288;  // from which on R = 8
@@ -855,25 +855,27 @@ __global__ void __launch_bounds__(kRopeThreads, BS == 16 ? 5 : 4)
 template <bool kBF16, bool kInter>
 static cudaError_t launch_rope_fp8(const RopeParams& p, cudaStream_t stream) {
     // Eight rows of queries at a time whatever the call's size: keys and
-    // values hold most of the places, and half the loads in flight cost 43.4 -> 50.2
-    // us for 5000 tokens of 64/8 heads, 3.0 -> 3.5 for 256 of 32/8.
+    // values hold most of the places, and half the loads in flight cost 36.7 -> 42.0
+    // us for 5000 tokens of 64/8 heads, 64.4 -> 72.6 for 16384 of 32/8 (3.0 either
+    // way for 256).
     constexpr int R = 8;
     const int64_t q_units = p.num_tokens * (int64_t)row_units(p.num_q_heads, R);
     const int64_t q_blocks = (q_units + kRopeThreads / 16 - 1) / (kRopeThreads / 16);
     // Teams of a warp, or of two, for keys and values.  As long as all are
-    // resident at once, one for each token and item.  With more, a head's keys
-    // and values share one (256 sequences' next tokens: 3.0 us, 4.4 without;
-    // but 5.2 us, 6.3 with, for a chunk of 100 tokens, which has few runs);
-    // then windows grow towards a block's tokens, and items again, while
-    // enough teams are left: 16384 tokens of 8 KV heads in blocks of 16 took
-    // 67.9 us with 8192 teams, 70.9 with 4096, 777 of 40 heads in blocks of 32
-    // 16.4 with 1960, 18.4 with 1040, 19.5 with 3920 (5000 tokens of 8 heads
-    // 36.5 us with 4560 as the bound, 37.8 with 6080).
-    constexpr int64_t kResident = 2432;
-    const int64_t enough = p.block_size == 16 ? 4560 : 1520;
+    // resident at once (16 warps on an SM), one for each token and item.  With
+    // more, a head's keys and values share one (256 sequences' next tokens: 3.0
+    // us, 4.4 without; but 5.3 us, 6.4 with, for a chunk of 100 tokens, which has
+    // few runs); then windows grow towards a block's tokens, and items again,
+    // while enough teams are left, 30 to an SM, or 10 of two warps: half as many
+    // as the bound cost 777 tokens of 40 heads in blocks of 32 14.7 -> 16.0 us,
+    // 16384 normed ones of 8 heads there 82.4 -> 98.1, 5000 of 8 heads in blocks
+    // of 16 36.7 -> 37.5; twice as many 17.4, 82.9 and 37.9, and 64.4 -> 67.1 for
+    // 16384 of 8 heads in blocks of 16.  (Short chunks in blocks of 32 would take
+    // half as many: 256 and 512 tokens of 8 heads 7.9 -> 7.1 and 8.1 -> 7.2.)
+    const int64_t resident = 16 * (int64_t)p.sms, enough = (p.block_size == 16 ? 30 : 10) * (int64_t)p.sms;
     const int64_t all = 2 * (int64_t)p.num_kv_heads, pair = p.block_size / 16;
     const auto teams = [&](int w, int n) { return (p.num_tokens + w - 1) / w * ((all + n - 1) / n); };
-    int window = 1, items = teams(1, 1) * pair > kResident ? 2 : 1;
+    int window = 1, items = teams(1, 1) * pair > resident ? 2 : 1;
     for (int w = 2; w < 2 * (int)p.block_size; w *= 2) {
         const int most = std::min(w, (int)p.block_size - 1);
         if (teams(most, items) >= enough) window = most;
@@ -883,8 +885,8 @@ static cudaError_t launch_rope_fp8(const RopeParams& p, cudaStream_t stream) {
     const uint64_t blocks = (uint64_t)(kv_blocks + q_blocks);
     // Keys and values are spread over the first two thirds of the grid: their
     // teams take longest, and none should start last.  (Spread over all of it
-    // 69.8, 18.6 and 43.3 us for 16384, 777 and 5000 tokens; so 67.9, 16.4,
-    // 39.1; all of them first 73.3, 16.4, 40.5.)
+    // 65.4, 16.5 and 40.8 us for 16384, 777 and 5000 tokens; so 64.4, 14.7,
+    // 36.7; all of them first 70.0, 14.7, 38.3.)
     const uint64_t even = (((uint64_t)kv_blocks << 32) + blocks - 1) / blocks;
     const uint64_t kv_rate = std::min<uint64_t>(even + even / 2, 1ull << 32);
     auto kern = p.block_size == 16 ? rope_fp8_kernel<kBF16, kInter, 16, R> : rope_fp8_kernel<kBF16, kInter, 32, R>;
