@@ -36,7 +36,7 @@
 //
 // Bytes bound long contexts: 8 sequences of 131072 tokens, 64/8 heads (2.15 GB)
 // in 327 us, 6.6 TB/s.  Short ones lose to each CTA's start and end, some 6 us:
-// 64 of 512 to 4096 tokens, 32/8 heads (304 MB) in 60.5 us, 5.0 TB/s.  Other
+// 64 of 512 to 4096 tokens, 32/8 heads (304 MB) in 59.8 us, 5.1 TB/s.  Other
 // shapes of the CTA were slower there (warps, stages, CTAs per SM: 2, 2, 6
 // 64.2 us; 2, 3, 4 67.5; 4, 3, 2 71.5; 3, 2, 4 65.0 against 62.4 then).
 #include <atomic>
@@ -121,7 +121,7 @@ struct DecodeFp8Smem {
 // step, by a part of what they add to; products added to O at once shrink it
 // by 1e-6 over 2048 tokens (7 sequences of 12859 tokens: 1.2e-6 off in all,
 // nothing beside a 16-bit output's rounding).  Summed pair by pair and added to
-// nearest they leave 5.5e-7, for 63.5 us against 60.5 (64 sequences of 512 to
+// nearest they leave 5.5e-7, for 63.3 us against 59.8 (64 sequences of 512 to
 // 4096 tokens).
 template <int NH, bool kRound>
 __global__ void __launch_bounds__(kF8Warps * 32, NH == 1 ? kF8CtasPerSm : kF8CtasPerSm - 1)

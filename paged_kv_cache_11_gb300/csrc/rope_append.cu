@@ -14,8 +14,8 @@
 // normed tokens of 64/8 heads (680 MB) in 104 us, 6.5 TB/s.  The 8-bit write
 // waits on more: a block's scale needs all of its new rows before the first
 // byte, a chain of loads and exchanges for each run of tokens: 16384 tokens of
-// 32/8 heads (378 MB) in 64.2 us, 5.9 TB/s; 777 normed ones of 40/40 heads (40
-// MB) in 14.5 us (issue slots some 40% used, three or four warps to a
+// 32/8 heads (378 MB) in 64.4 us, 5.9 TB/s; 777 normed ones of 40/40 heads (40
+// MB) in 14.7 us (issue slots some 35 to 40% used, three or four warps to a
 // scheduler); a step of 256 sequences in 3.0 us.
 #include <cuda_fp8.h>
 
