@@ -304,7 +304,9 @@ pkv_status paged_attention_decode(const void* q, const void* k_cache, const void
  * max_context_len, for this kernel's own resident CTAs, so
  * paged_attention_plan and paged_attention_partition_size need not agree
  * (a max_context_len near the longest context chooses best).  The values enter the products exactly (as 16-bit floats),
- * the scales as 32-bit factors.
+ * the scales as 32-bit factors, a token's weight to within 2^-20 of itself
+ * and 2^-26 of its head's largest: one further below than that counts as
+ * nothing, whatever the scale of its value.
  */
 pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
                                       const float* k_scales, const float* v_scales, const int32_t* block_tables,
