@@ -83,7 +83,9 @@ enum {
     PKV_DEVERR_GROUP = 7,       /* grouped decode: group_starts out of order or range, or a sequence
                                    with a shared prefix in no group or beyond max_group_size members */
     PKV_DEVERR_POSITION = 8,    /* append_rope: positions[t] outside [0, max_position) */
-    PKV_DEVERR_SCALE = 9        /* append_rope_fp8: rows join a block whose scale is not finite and at least 2^-126 */
+    PKV_DEVERR_SCALE = 9,       /* append_rope_fp8: rows join a block whose scale is not finite and at least 2^-126 */
+    PKV_DEVERR_QUERY = 10       /* attention of drafted tokens, prompts: query_starts (or key_starts) out of order or
+                                   range, or more tokens of a sequence than the call takes */
 };
 
 /* Shape of one layer's paged cache (host struct, read during the call). */
@@ -107,6 +109,42 @@ typedef struct {
     int32_t interleaved;  /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
     float norm_eps;       /* added to the mean square; >= 0 */
 } pkv_rope_desc;
+
+/* A paged latent cache, [num_blocks][block_size][latent_dim + rope_dim] (host struct, read during the call). */
+typedef struct {
+    int64_t num_blocks;  /* >= 1 */
+    int32_t block_size;  /* tokens per block: 16 or 32 */
+    int32_t latent_dim;  /* 512 */
+    int32_t rope_dim;    /* 64 */
+    int32_t dtype;       /* PKV_BF16 or PKV_FP16 */
+} pkv_latent_desc;
+
+/* The new rows of paged_latent_append_rope (host struct, read during the call); strides in elements, multiples of 8. */
+typedef struct {
+    int32_t num_heads;         /* query heads; 0: no queries */
+    int32_t interleaved;       /* 0: pairs (i, i + rope_dim / 2); 1: pairs (2i, 2i + 1) */
+    int64_t q_stride;          /* from one token's queries to the next */
+    int64_t q_head_stride;     /* from one head to the next */
+    int64_t q_out_stride;
+    int64_t q_out_head_stride;
+    int64_t kv_stride;
+    int64_t max_position;      /* rows of cos_sin */
+    float norm_eps;            /* added to the mean square; >= 0 */
+} pkv_latent_rope_desc;
+
+/* The prompts of latent_attention_prefill (host struct, read during the call); strides in elements, multiples of 8. */
+typedef struct {
+    int32_t num_heads;
+    int32_t dtype;             /* of q, kv, k_rope and out: PKV_BF16 or PKV_FP16 */
+    int32_t nope_dim;          /* 128 */
+    int32_t rope_dim;          /* 64 */
+    int32_t value_dim;         /* 128 */
+    int64_t q_stride;          /* from one token to the next */
+    int64_t q_head_stride;     /* from one head to the next */
+    int64_t kv_stride;
+    int64_t kv_head_stride;
+    int64_t k_rope_stride;
+} pkv_prompt_desc;
 
 /* Human-readable name of a status. Never NULL. */
 const char* pkv_status_string(pkv_status status);
@@ -314,6 +352,153 @@ pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void
                                       int32_t num_q_heads, int32_t max_context_len, float scale, void* out,
                                       int32_t out_dtype, const pkv_cache_desc* cache, int32_t partition_size,
                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of several query tokens of each sequence, the drafted tokens of
+ * a speculative step, over the paged cache.  Sequence s's query tokens are
+ * rows query_starts[s] .. query_starts[s+1]-1 of q, n of them, and stand for
+ * the last n positions of its context of L = context_lens[s] tokens, whose K
+ * and V are in the cache already.  With base = L - n, query token i attends
+ * every position before base, and of the drafted positions base + j those
+ * with bit j of its mask set (a tree: itself and what it descends from), or,
+ * without masks, those with j <= i (a chain):
+ *     out[i][h][:] = sum_t softmax_t(scale * q[i][h] . K[t]) V[t]   over the attended t
+ * A query token that attends nothing gets zeros, and so does every query
+ * token of a sequence with L == 0.
+ *
+ * q:            [num_tokens][num_q_heads][head_dim], cache dtype, 16-byte aligned.
+ * query_starts: [num_seqs + 1] int32 device memory, in order, n <= 64; NULL:
+ *               one token a sequence (num_tokens == num_seqs).  Rows of q and
+ *               out outside the sequences are left alone.
+ * tree_masks:   [num_tokens] int64 device memory, bits n and above ignored; or
+ *               NULL.
+ * context_lens: [num_seqs] int32, L == 0 or n <= L <= max_blocks_per_seq * bs.
+ * out:          [num_tokens][num_q_heads][head_dim], cache dtype, 16-byte
+ *               aligned, not q.
+ * workspace:    at least paged_attention_tree_workspace_bytes() bytes, 256-byte
+ *               aligned; contents on entry are ignored.  Two calls whose
+ *               kernels may overlap on the GPU must not share it.
+ * K and V of positions that a token does not attend, and of the blocks' rows
+ * behind the context, may hold anything.  Values that are not finite make
+ * not finite the outputs of the tokens that attend them, and of no others.
+ * Weights are rounded to the cache's type for their product with V and
+ * divided by the sum of the rounded ones; everything else is in 32 bits.
+ * The result does not depend on physical block ids, and is the same from run
+ * to run.
+ * Bad metadata never faults: query_starts out of order or range
+ * (PKV_DEVERR_QUERY) leave the sequence's rows alone; more than 64 query
+ * tokens (PKV_DEVERR_QUERY), a context length out of range or below n
+ * (PKV_DEVERR_CONTEXT_LEN) and a block id outside the pool
+ * (PKV_DEVERR_BLOCK_ID; the query heads of the KV heads that read it) get
+ * zeros.
+ * Supported: head_dim 128; block_size 16 or 32; bf16 or fp16;
+ * num_q_heads a multiple of num_kv_heads; num_seqs <= 65535; tables of up to
+ * 2^31 - 1024 positions.
+ */
+pkv_status paged_attention_tree(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_starts,
+                                const int64_t* tree_masks, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                                float scale, void* out, const pkv_cache_desc* cache, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of paged_attention_tree on the current device (0: no device). */
+size_t paged_attention_tree_workspace_bytes(void);
+
+/*
+ * Write into a paged latent cache: one row a token, a latent that every
+ * head's keys and values are expanded from and a key part with the position
+ * that all heads share.  For every token t with slot_mapping[t] >= 0, with c =
+ * the first latent_dim values of its row of kv and r = the rope_dim behind
+ * them:
+ *     c' = c / sqrt(mean(c^2) + norm_eps) * kv_norm   (c' = c where that is NULL)
+ *     r' = r turned by the position, as paged_kv_append_rope turns a head with rot_dim = rope_dim
+ * and (c', r') goes to the token's slot of the cache, and to its row of
+ * kv_out where that is given (the prompt's latents, to be expanded); every
+ * head's rope_dim query values are turned by the same angles into q_out.
+ * Everything between the loads and the one rounding is in 32 bits.
+ *
+ * q, q_out:     token t's head h at base + t * stride + h * head_stride
+ *               elements, rope_dim contiguous values: slices of the query
+ *               projection and of the absorbed queries are passed as they
+ *               are.  q_out may be q with the same strides, and must not
+ *               overlap it otherwise.  May be NULL when num_heads is 0.
+ * kv:           row t at base + t * kv_stride.
+ * kv_out:       [num_tokens][latent_dim + rope_dim] or NULL; may be kv when
+ *               kv_stride is latent_dim + rope_dim, and must not overlap it
+ *               otherwise.
+ * positions:    [num_tokens] int64; not read, NULL allowed, when cos_sin is NULL.
+ * cos_sin:      [max_position][rope_dim] fp32, or NULL: no rotation.
+ * kv_norm:      [latent_dim] or NULL.
+ * slot_mapping: [num_tokens] int64; negative: padding, whose rows of q_out and
+ *               kv_out keep their contents.
+ * All device memory, 16-byte aligned but for positions and slot_mapping (8).
+ * A slot past the pool is recorded as PKV_DEVERR_SLOT and a position outside
+ * [0, max_position) as PKV_DEVERR_POSITION; such a token's row is not written
+ * and its rows of q_out and kv_out are zeros.  Two tokens with the same slot
+ * race.  num_tokens == 0 is a no-op.  Supported: latent_dim 512, rope_dim 64,
+ * bf16 or fp16, any block size.
+ */
+pkv_status paged_latent_append_rope(const void* q, const void* kv, const int64_t* positions, const float* cos_sin,
+                                    const void* kv_norm, const int64_t* slot_mapping, int64_t num_tokens, void* q_out,
+                                    void* kv_out, void* latent_cache, const pkv_latent_desc* cache,
+                                    const pkv_latent_rope_desc* rope, void* stream);
+
+/*
+ * Attention over a paged latent cache in its absorbed form: each head's query
+ * has been taken through the key expansion, so that its score against a token
+ * is a product over the whole cached row, whose first latent_dim values are
+ * the value too (the caller takes the output through the value expansion):
+ *     out[i][h][:] = sum_t softmax_t(scale * q[i][h] . row[t]) row[t][:latent_dim]
+ * over the positions that query token i attends, which query_starts,
+ * tree_masks and context_lens say as for paged_attention_tree; so do the
+ * errors, the workspace (paged_latent_decode_workspace_bytes()), the
+ * roundings and what may lie in places that are not attended.
+ * q:            [num_tokens][num_heads][latent_dim + rope_dim], cache dtype, 16-byte aligned.
+ * latent_cache: the pool, 16-byte aligned.
+ * out:          [num_tokens][num_heads][latent_dim], cache dtype, 16-byte aligned.
+ * Supported: latent_dim 512, rope_dim 64; block_size 16 or 32; bf16 or fp16;
+ * num_seqs <= 65535; num_tokens * num_heads and num_blocks * block_size below
+ * 2^31; tables of up to 2^31 - 1024 positions.
+ */
+pkv_status paged_latent_decode(const void* q, const void* latent_cache, const int32_t* block_tables,
+                               int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_starts,
+                               const int64_t* tree_masks, int32_t num_seqs, int32_t num_tokens, int32_t num_heads,
+                               float scale, void* out, const pkv_latent_desc* cache, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of paged_latent_decode on the current device (0: no device). */
+size_t paged_latent_decode_workspace_bytes(void);
+
+/*
+ * Causal attention of whole prompts in the expanded form of latent attention:
+ * each head has a key of nope_dim values and a value of value_dim values a
+ * token, expanded from the token's latent and side by side in kv, and the
+ * rope_dim turned key values of k_rope are shared by the heads.  Sequence s's
+ * queries are tokens query_starts[s] .. query_starts[s+1]-1 of q, n of them,
+ * its keys tokens key_starts[s] .. key_starts[s+1]-1 of kv and k_rope, m of
+ * them; the queries are the last n positions of the m: query i attends keys j
+ * <= i + m - n.
+ *     s_ij = scale * (q[i][h][:nope] . kv[j][h][:nope] + q[i][h][nope:] . k_rope[j])
+ *     out[i][h][:] = sum_j softmax_j(s_ij) kv[j][h][nope:]
+ * A query that attends nothing (m < n) gets zeros.
+ * q:        token t's head h at base + t * q_stride + h * q_head_stride, nope_dim + rope_dim values.
+ * kv:       token t's head h at base + t * kv_stride + h * kv_head_stride, nope_dim + value_dim values.
+ * k_rope:   token t at base + t * k_rope_stride: kv_out of paged_latent_append_rope behind its first latent_dim values.
+ * query_starts, key_starts: [num_seqs + 1] int32 device memory, in order.
+ *           Rows of q and out outside the sequences are left alone.
+ * max_query_len: host-side upper bound of the sequences' n.
+ * out:      [num_query_tokens][num_heads][value_dim], 16-byte aligned.
+ * q, kv and k_rope are 16-byte aligned.  What is not finite stays with the
+ * queries that attend it, and weights are rounded as for paged_attention_tree.
+ * Bad metadata never faults: query_starts out of order or range leave the
+ * sequence's rows alone, key_starts out of order or range and n >
+ * max_query_len get zeros (PKV_DEVERR_QUERY).
+ * Supported: nope_dim 128, rope_dim 64, value_dim 128; bf16 or fp16; num_heads and num_seqs <= 65535.
+ */
+pkv_status latent_attention_prefill(const void* q, const void* kv, const void* k_rope, const int32_t* query_starts,
+                                    const int32_t* key_starts, int32_t num_seqs, int32_t num_query_tokens,
+                                    int32_t num_key_tokens, int32_t max_query_len, float scale, void* out,
+                                    const pkv_prompt_desc* prompt, void* stream);
 
 /*
  * A decode step in one launch: the block write of one new token per

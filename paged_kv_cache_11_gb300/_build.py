@@ -27,7 +27,7 @@ PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 LIBDIR = PKG / "_lib"
 CUDA_SOURCES = ["api.cu", "decode.cu", "group_prefix.cu", "append_copy.cu", "rope_append.cu", "decode_fp8.cu",
-                "noalloc.cu"]
+                "noalloc.cu", "tree.cu", "latent.cu", "latent_append.cu", "latent_prompt.cu", "drafted.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -58,8 +58,7 @@ def _stale(target: Path, deps: list[Path]) -> bool:
 def build_library(force: bool = False, verbose: bool = False) -> Path:
     LIBDIR.mkdir(exist_ok=True)
     out = LIBDIR / "libpagedkv.so"
-    deps = [CSRC / s for s in CUDA_SOURCES] + [CSRC / "pkv_internal.cuh", CSRC / "decode_common.cuh",
-                                                PKG.parent / "include" / "pagedkv.h"]
+    deps = [CSRC / s for s in CUDA_SOURCES] + sorted(CSRC.glob("*.cuh")) + [PKG.parent / "include" / "pagedkv.h"]
     if not force and not _stale(out, deps):
         return out
     nvcc = _nvcc()

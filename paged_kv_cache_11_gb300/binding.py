@@ -22,7 +22,7 @@ LIB_PATH = Path(__file__).resolve().parent / "_lib" / "libpagedkv.so"
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_WORKSPACE, PKV_ERR_CUDA, PKV_ERR_DEVICE_METADATA = range(6)
 PKV_BF16, PKV_FP16, PKV_FP32, PKV_E4M3 = 0, 1, 2, 3
 DEVERR_NAMES = {0: "none", 1: "slot", 2: "copy_id", 3: "context_len", 4: "block_id", 5: "timeout",
-                6: "prefix_len", 7: "group", 8: "position", 9: "scale"}
+                6: "prefix_len", 7: "group", 8: "position", 9: "scale", 10: "query"}
 
 _DTYPE_CODE = {torch.bfloat16: PKV_BF16, torch.float16: PKV_FP16, torch.float32: PKV_FP32,
                torch.float8_e4m3fn: PKV_E4M3}
@@ -49,6 +49,45 @@ class RopeDesc(ctypes.Structure):
         ("rot_dim", ctypes.c_int32),
         ("interleaved", ctypes.c_int32),
         ("norm_eps", ctypes.c_float),
+    ]
+
+
+class LatentDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_blocks", ctypes.c_int64),
+        ("block_size", ctypes.c_int32),
+        ("latent_dim", ctypes.c_int32),
+        ("rope_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class LatentRopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_heads", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64),
+        ("q_out_head_stride", ctypes.c_int64),
+        ("kv_stride", ctypes.c_int64),
+        ("max_position", ctypes.c_int64),
+        ("norm_eps", ctypes.c_float),
+    ]
+
+
+class PromptDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_heads", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("nope_dim", ctypes.c_int32),
+        ("rope_dim", ctypes.c_int32),
+        ("value_dim", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("kv_stride", ctypes.c_int64),
+        ("kv_head_stride", ctypes.c_int64),
+        ("k_rope_stride", ctypes.c_int64),
     ]
 
 
@@ -91,6 +130,20 @@ def _lib() -> ctypes.CDLL:
     lib.paged_attention_decode_fp8.restype = ctypes.c_int
     lib.copy_blocks_fp8.argtypes = [vp, vp, vp, vp, i32, vp, i32, desc_p, vp]
     lib.copy_blocks_fp8.restype = ctypes.c_int
+    latent_p = ctypes.POINTER(LatentDesc)
+    lib.paged_attention_tree.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, ctypes.c_float, vp, desc_p, vp, sz,
+                                         vp]
+    lib.paged_attention_tree.restype = ctypes.c_int
+    lib.paged_latent_decode.argtypes = [vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, ctypes.c_float, vp, latent_p, vp, sz, vp]
+    lib.paged_latent_decode.restype = ctypes.c_int
+    lib.paged_latent_append_rope.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, latent_p,
+                                             ctypes.POINTER(LatentRopeDesc), vp]
+    lib.paged_latent_append_rope.restype = ctypes.c_int
+    lib.latent_attention_prefill.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp,
+                                             ctypes.POINTER(PromptDesc), vp]
+    lib.latent_attention_prefill.restype = ctypes.c_int
+    for f in (lib.paged_attention_tree_workspace_bytes, lib.paged_latent_decode_workspace_bytes):
+        f.argtypes, f.restype = [], sz
     lib.paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     lib.paged_attention_workspace_bytes.restype = sz
     lib.paged_attention_plan.argtypes = [i32, i32, i32, i32, i32, i32]
@@ -333,6 +386,86 @@ def paged_attention_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                                               out, max_context_len, partition_size, workspace, out_dtype)
     return (_MARSHAL or _marshal()).decode_fp8(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale,
                                                out, max_context_len, partition_size, workspace, out_dtype)
+
+
+def paged_attention_tree_workspace_bytes() -> int:
+    return int(_lib().paged_attention_tree_workspace_bytes())
+
+
+def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                         context_lens: torch.Tensor, query_starts: torch.Tensor | None, tree_masks: torch.Tensor | None,
+                         scale: float, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Attention of each sequence's drafted tokens, the last ones of its context, over the paged cache; returns ``out``
+    [num_tokens, num_q_heads, 128], of q's dtype.
+
+    Tokens query_starts[s] .. query_starts[s + 1] - 1 of q (at most 64) are sequence s's; bit j of a token's tree_masks says
+    whether it attends the j-th of them (None: a chain, each attends those up to itself).  ``context_lens`` counts them: their
+    K and V are in the cache.  Without query_starts every sequence has one token.
+    """
+    if stream is not None:
+        with _on(stream, q):
+            return paged_attention_tree(q, k_cache, v_cache, block_tables, context_lens, query_starts, tree_masks, scale, out,
+                                        workspace)
+    return (_MARSHAL or _marshal()).tree(q, k_cache, v_cache, block_tables, context_lens, query_starts, tree_masks, scale,
+                                         out, workspace)
+
+
+def paged_latent_append_rope(q: torch.Tensor | None, kv: torch.Tensor, positions: torch.Tensor | None,
+                             cos_sin: torch.Tensor | None, slot_mapping: torch.Tensor, cache: torch.Tensor,
+                             kv_norm: torch.Tensor | None = None, norm_eps: float = 1e-6, interleaved: bool = False,
+                             q_out: torch.Tensor | None = None, kv_out: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor | None:
+    """Write of new tokens into a latent cache [num_blocks, block_size, 576]: kv [num_tokens, 576] is a token's latent (512,
+    normed where ``kv_norm`` [512] is given) and its key part (64, rotated by position); returns ``q_out``, the rotated
+    64 values of every query head.
+
+    q and q_out [num_tokens, num_heads, 64] may be slices of wider rows (of the query projection, of the absorbed queries),
+    and q_out q itself.  ``kv_out`` [num_tokens, 576] takes the written rows too.  Rows of padding tokens (negative slots) are
+    left as they were.
+    """
+    if stream is not None:
+        with _on(stream, cache):
+            return paged_latent_append_rope(q, kv, positions, cos_sin, slot_mapping, cache, kv_norm, norm_eps, interleaved,
+                                            q_out, kv_out)
+    return (_MARSHAL or _marshal()).latent_append(q, kv, positions, cos_sin, slot_mapping, cache, kv_norm, norm_eps,
+                                                  interleaved, q_out, kv_out)
+
+
+def paged_latent_decode_workspace_bytes() -> int:
+    return int(_lib().paged_latent_decode_workspace_bytes())
+
+
+def paged_latent_decode(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                        scale: float, query_starts: torch.Tensor | None = None, tree_masks: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Attention over a latent cache [num_blocks, block_size, 576] in its absorbed form: q [num_tokens, num_heads, 576] holds
+    each head's query taken through the key expansion (512) and its rotated part (64); returns ``out`` [num_tokens,
+    num_heads, 512], to be taken through the value expansion.  One token a sequence, or several drafted ones with
+    query_starts and tree_masks as for paged_attention_tree."""
+    if stream is not None:
+        with _on(stream, q):
+            return paged_latent_decode(q, cache, block_tables, context_lens, scale, query_starts, tree_masks, out, workspace)
+    return (_MARSHAL or _marshal()).latent_decode(q, cache, block_tables, context_lens, scale, query_starts, tree_masks, out,
+                                                  workspace)
+
+
+def latent_attention_prefill(q: torch.Tensor, kv: torch.Tensor, k_rope: torch.Tensor, query_starts: torch.Tensor,
+                             key_starts: torch.Tensor, scale: float, max_query_len: int | None = None,
+                             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of whole prompts in the expanded form: q [num_query_tokens, num_heads, 192] (128 values, then 64
+    rotated ones), kv [num_key_tokens, num_heads, 256] (each head's key and value, 128 each), k_rope [num_key_tokens, 64], the
+    rotated key values that the heads share; returns ``out`` [num_query_tokens, num_heads, 128].
+
+    Sequence s's queries are the last of its keys' positions (more keys than queries: a prefix that is cached).  Tokens and
+    heads of q and kv, and rows of k_rope, may be any multiple of 8 elements apart.  ``max_query_len`` bounds the prompts'
+    lengths (default: all of q).
+    """
+    if stream is not None:
+        with _on(stream, q):
+            return latent_attention_prefill(q, kv, k_rope, query_starts, key_starts, scale, max_query_len, out)
+    return (_MARSHAL or _marshal()).prefill(q, kv, k_rope, query_starts, key_starts, scale, max_query_len, out)
 
 
 def paged_attention_append_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,

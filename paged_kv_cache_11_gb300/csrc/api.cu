@@ -8,6 +8,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "drafted.cuh"
 #include "pkv_internal.cuh"
 
 namespace pkv {
@@ -762,6 +763,313 @@ pkv_status copy_blocks_fp8(void* const* k_caches, void* const* v_caches, float* 
         p.num_pairs = num_pairs;
         e = launch_copy_blocks_fp8(p, static_cast<cudaStream_t>(stream), &launches);
     }
+    g_launches += launches;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// Partials of the calls on drafted tokens: one CTA per SM, two slots each.
+struct DraftLayout {
+    int64_t ml_off, desc_off, total;
+};
+static DraftLayout draft_layout(int64_t ctas, int64_t unit_rows, int64_t value_dims) {
+    DraftLayout w;
+    w.ml_off = round256(ctas * 2 * unit_rows * value_dims * 4);
+    w.desc_off = w.ml_off + round256(ctas * 2 * unit_rows * 8);
+    w.total = w.desc_off + round256(ctas * 4 * 16);
+    return w;
+}
+
+// A tensor of 16-bit elements in `rank` dimensions, innermost first, 128-byte
+// swizzle: strides in bytes from the second dimension on.
+static pkv_status encode_map(CUtensorMap* m, const void* base, int dtype, int rank, const cuuint64_t* dims,
+                             const cuuint64_t* strides, const cuuint32_t* box) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return PKV_ERR_CUDA;
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    const CUresult r = fn(m, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                          const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_INVALID_ARG;
+}
+
+// Checks and parameters that paged_attention_tree and paged_latent_decode share.
+static pkv_status draft_params(DraftParams& p, const void* q, const void* pool, const int32_t* block_tables,
+                               int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_starts,
+                               const int64_t* tree_masks, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                               float scale, void* out, int64_t num_blocks, int32_t num_kv_heads, int32_t block_size,
+                               void* workspace, size_t workspace_bytes, int unit_rows, int value_dims) {
+    if (num_seqs < 0 || num_seqs > 65535 || num_tokens < 0 || num_q_heads < 1 || num_q_heads % num_kv_heads != 0)
+        return PKV_ERR_INVALID_ARG;
+    if (!query_starts && num_tokens != num_seqs) return PKV_ERR_INVALID_ARG;
+    if (max_blocks_per_seq < 1 || !std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
+    if ((int64_t)max_blocks_per_seq * block_size > INT_MAX - 1024) return PKV_ERR_UNSUPPORTED;
+    // rows of a sequence and of the batch are counted in 32 bits
+    if (num_q_heads > 65535 || (int64_t)num_tokens * num_q_heads > INT_MAX) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+    if (!q || !pool || !block_tables || !context_lens || !out) return PKV_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(block_tables, 4) ||
+        !aligned(context_lens, 4) || !aligned(query_starts, 4) || !aligned(tree_masks, 8))
+        return PKV_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms < 1) return PKV_ERR_CUDA;
+    const DraftLayout w = draft_layout(sms, unit_rows, value_dims);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)w.total) return PKV_ERR_WORKSPACE;
+    p.err = error_word();
+    if (!p.err) return PKV_ERR_CUDA;
+    p.q = q;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_starts = query_starts;
+    p.tree_masks = tree_masks;
+    p.out = out;
+    char* base = static_cast<char*>(workspace);
+    p.part_o = reinterpret_cast<float*>(base);
+    p.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
+    p.part_desc = reinterpret_cast<int4*>(base + w.desc_off);
+    p.num_blocks = num_blocks;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.len_limit = max_blocks_per_seq * block_size;
+    p.ctas = sms;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    return PKV_OK;
+}
+
+static pkv_status check_latent(const pkv_latent_desc* c) {
+    if (!c || c->num_blocks < 1 || c->block_size < 1 || c->latent_dim < 1 || c->rope_dim < 0) return PKV_ERR_INVALID_ARG;
+    if (c->dtype != PKV_BF16 && c->dtype != PKV_FP16) return PKV_ERR_UNSUPPORTED;
+    if (c->latent_dim != kLatentDim || c->rope_dim != kLatentRope) return PKV_ERR_UNSUPPORTED;
+    if (c->num_blocks > INT_MAX / c->block_size) return PKV_ERR_UNSUPPORTED;  // slots are held in 32 bits
+    return PKV_OK;
+}
+
+// Bytes from the first element of a strided tensor [n][heads][width] to behind its last.
+static __int128 span_bytes(int64_t n, int64_t stride, int64_t heads, int64_t head_stride, int64_t width) {
+    return 2 * ((__int128)(n - 1) * stride + (__int128)(heads - 1) * head_stride + width);
+}
+static bool overlap(const void* a, __int128 a_bytes, const void* b, __int128 b_bytes) {
+    const __int128 x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + b_bytes && y < x + a_bytes;
+}
+static bool good_stride(int64_t s) { return s >= 0 && s % 8 == 0 && s < ((int64_t)1 << 38); }
+
+extern "C" {
+
+size_t paged_attention_tree_workspace_bytes(void) {
+    const int sms = sm_count();
+    return sms < 1 ? 0 : (size_t)draft_layout(sms, kTreeRows, kHeadDim).total;
+}
+
+size_t paged_latent_decode_workspace_bytes(void) {
+    const int sms = sm_count();
+    return sms < 1 ? 0 : (size_t)draft_layout(sms, kLatentRows, kLatentDim).total;
+}
+
+pkv_status paged_attention_tree(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_starts,
+                                const int64_t* tree_masks, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                                float scale, void* out, const pkv_cache_desc* cache, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (cache->head_dim != kHeadDim || (cache->block_size != 16 && cache->block_size != 32)) return PKV_ERR_UNSUPPORTED;
+    // tile rows must be addressable by a 32-bit TMA coordinate
+    if ((__int128)cache->num_blocks * cache->num_kv_heads * cache->block_size > INT_MAX) return PKV_ERR_UNSUPPORTED;
+    DraftParams p;
+    std::memset(&p, 0, sizeof(p));
+    st = draft_params(p, q, k_cache, block_tables, max_blocks_per_seq, context_lens, query_starts, tree_masks, num_seqs,
+                      num_tokens, num_q_heads, scale, out, cache->num_blocks, cache->num_kv_heads, cache->block_size,
+                      workspace, workspace_bytes, kTreeRows, kHeadDim);
+    if (st != PKV_OK || num_seqs == 0 || num_tokens == 0) return st;
+    if (!v_cache || !aligned(v_cache, 16)) return PKV_ERR_INVALID_ARG;
+    const __int128 bytes = (__int128)num_tokens * num_q_heads * kHeadDim * 2;
+    if (overlap(q, bytes, out, bytes)) return PKV_ERR_INVALID_ARG;
+    p.values = v_cache;
+    CUtensorMap tmk, tmv;
+    st = encode_cache_map(&tmk, k_cache, *cache, 4);
+    if (st == PKV_OK) st = encode_cache_map(&tmv, v_cache, *cache, 4);
+    if (st != PKV_OK) return st;
+    int launches = 0;
+    const cudaError_t e =
+        launch_tree(p, cache->dtype, cache->block_size, tmk, tmv, static_cast<cudaStream_t>(stream), &launches);
+    g_launches += launches;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status paged_latent_decode(const void* q, const void* latent_cache, const int32_t* block_tables,
+                               int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_starts,
+                               const int64_t* tree_masks, int32_t num_seqs, int32_t num_tokens, int32_t num_heads,
+                               float scale, void* out, const pkv_latent_desc* cache, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    pkv_status st = check_latent(cache);
+    if (st != PKV_OK) return st;
+    if (cache->block_size != 16 && cache->block_size != 32) return PKV_ERR_UNSUPPORTED;
+    DraftParams p;
+    std::memset(&p, 0, sizeof(p));
+    st = draft_params(p, q, latent_cache, block_tables, max_blocks_per_seq, context_lens, query_starts, tree_masks, num_seqs,
+                      num_tokens, num_heads, scale, out, cache->num_blocks, 1, cache->block_size, workspace,
+                      workspace_bytes, kLatentRows, kLatentDim);
+    if (st != PKV_OK || num_seqs == 0 || num_tokens == 0) return st;
+    const __int128 rows = (__int128)num_tokens * num_heads;
+    if (overlap(q, rows * kLatentRow * 2, out, rows * kLatentDim * 2)) return PKV_ERR_INVALID_ARG;
+    p.values = latent_cache;
+    CUtensorMap tmq, tmc;
+    {
+        const cuuint64_t dims[2] = {kLatentRow, (cuuint64_t)rows}, strides[1] = {kLatentRow * 2};
+        const cuuint32_t box[2] = {64, kLatentRows};
+        st = encode_map(&tmq, q, cache->dtype, 2, dims, strides, box);
+        if (st != PKV_OK) return st;
+    }
+    {
+        // [8-token groups][nine 64-value parts][8 tokens][64]: one copy brings 16 tokens
+        const cuuint64_t dims[4] = {64, 8, kLatentRow / 64, (cuuint64_t)cache->num_blocks * cache->block_size / 8};
+        const cuuint64_t strides[3] = {kLatentRow * 2, 128, kLatentRow * 2 * 8};
+        const cuuint32_t box[4] = {64, 8, kLatentRow / 64, 2};
+        st = encode_map(&tmc, latent_cache, cache->dtype, 4, dims, strides, box);
+        if (st != PKV_OK) return st;
+    }
+    int launches = 0;
+    const cudaError_t e =
+        launch_latent_decode(p, cache->dtype, cache->block_size, tmq, tmc, static_cast<cudaStream_t>(stream), &launches);
+    g_launches += launches;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status paged_latent_append_rope(const void* q, const void* kv, const int64_t* positions, const float* cos_sin,
+                                    const void* kv_norm, const int64_t* slot_mapping, int64_t num_tokens, void* q_out,
+                                    void* kv_out, void* latent_cache, const pkv_latent_desc* cache,
+                                    const pkv_latent_rope_desc* rope, void* stream) {
+    const pkv_status st = check_latent(cache);
+    if (st != PKV_OK) return st;
+    if (!rope || num_tokens < 0 || rope->num_heads < 0 || !(rope->norm_eps >= 0.f) || rope->norm_eps == INFINITY)
+        return PKV_ERR_INVALID_ARG;
+    for (const int64_t s : {rope->q_stride, rope->q_head_stride, rope->q_out_stride, rope->q_out_head_stride, rope->kv_stride})
+        if (!good_stride(s)) return PKV_ERR_INVALID_ARG;
+    if (rope->num_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PKV_OK;
+    if (num_tokens > INT_MAX / (rope->num_heads + 1)) return PKV_ERR_INVALID_ARG;  // rows are counted in 32 bits
+    if (!kv || !slot_mapping || !latent_cache || !aligned(kv, 16) || !aligned(latent_cache, 16) ||
+        !aligned(slot_mapping, 8) || !aligned(kv_out, 16) || !aligned(kv_norm, 16))
+        return PKV_ERR_INVALID_ARG;
+    if (rope->num_heads > 0 && (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16))) return PKV_ERR_INVALID_ARG;
+    if (cos_sin && (!positions || !aligned(positions, 8) || !aligned(cos_sin, 16) || rope->max_position < 1))
+        return PKV_ERR_INVALID_ARG;
+    if (rope->num_heads > 0) {
+        const bool in_place = q == q_out && rope->q_stride == rope->q_out_stride &&
+                              (rope->q_head_stride == rope->q_out_head_stride || rope->num_heads == 1);
+        const __int128 to = span_bytes(num_tokens, rope->q_out_stride, rope->num_heads, rope->q_out_head_stride, kLatentRope);
+        if (!in_place && (overlap(q, span_bytes(num_tokens, rope->q_stride, rope->num_heads, rope->q_head_stride, kLatentRope),
+                                  q_out, to) ||
+                          overlap(kv, span_bytes(num_tokens, rope->kv_stride, 1, 0, kLatentRow), q_out, to)))
+            return PKV_ERR_INVALID_ARG;
+        // a token's heads, and tokens, do not lie over one another where they are written
+        if ((rope->num_heads > 1 && rope->q_out_head_stride < kLatentRope) ||
+            (num_tokens > 1 && rope->q_out_stride < kLatentRope))
+            return PKV_ERR_INVALID_ARG;
+    }
+    if (kv_out && !(kv == kv_out && rope->kv_stride == kLatentRow) &&
+        overlap(kv, span_bytes(num_tokens, rope->kv_stride, 1, 0, kLatentRow), kv_out, span_bytes(num_tokens, kLatentRow, 1, 0, kLatentRow)))
+        return PKV_ERR_INVALID_ARG;
+    int* err = error_word();
+    if (!err) return PKV_ERR_CUDA;
+    LatentAppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.err = err;
+    p.q = static_cast<const uint16_t*>(q);
+    p.kv = static_cast<const uint16_t*>(kv);
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.kv_norm = static_cast<const uint16_t*>(kv_norm);
+    p.slot_mapping = slot_mapping;
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.kv_out = static_cast<uint16_t*>(kv_out);
+    p.cache = static_cast<uint16_t*>(latent_cache);
+    p.num_tokens = num_tokens;
+    p.num_slots = cache->num_blocks * cache->block_size;
+    p.max_position = rope->max_position;
+    p.q_stride = rope->q_stride;
+    p.q_head_stride = rope->q_head_stride;
+    p.q_out_stride = rope->q_out_stride;
+    p.q_out_head_stride = rope->q_out_head_stride;
+    p.kv_stride = rope->kv_stride;
+    p.num_heads = rope->num_heads;
+    p.interleaved = rope->interleaved != 0;
+    p.norm_eps = rope->norm_eps;
+    int launches = 0;
+    const cudaError_t e = launch_latent_append(p, cache->dtype, static_cast<cudaStream_t>(stream), &launches);
+    g_launches += launches;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status latent_attention_prefill(const void* q, const void* kv, const void* k_rope, const int32_t* query_starts,
+                                    const int32_t* key_starts, int32_t num_seqs, int32_t num_query_tokens,
+                                    int32_t num_key_tokens, int32_t max_query_len, float scale, void* out,
+                                    const pkv_prompt_desc* d, void* stream) {
+    if (!d || d->num_heads < 1) return PKV_ERR_INVALID_ARG;
+    if (d->dtype != PKV_BF16 && d->dtype != PKV_FP16) return PKV_ERR_UNSUPPORTED;
+    if (d->nope_dim != kHeadDim || d->rope_dim != kLatentRope || d->value_dim != kHeadDim || d->num_heads > 65535)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || num_seqs > 65535 || num_query_tokens < 0 || num_key_tokens < 0 || max_query_len < 0 ||
+        max_query_len > num_query_tokens || !std::isfinite(scale))
+        return PKV_ERR_INVALID_ARG;
+    for (const int64_t s : {d->q_stride, d->q_head_stride, d->kv_stride, d->kv_head_stride, d->k_rope_stride})
+        if (!good_stride(s)) return PKV_ERR_INVALID_ARG;
+    if (num_query_tokens > INT_MAX - 1024 || num_key_tokens > INT_MAX - 1024) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return PKV_OK;
+    if (!q || !query_starts || !key_starts || !out || !aligned(q, 16) || !aligned(kv, 16) || !aligned(k_rope, 16) ||
+        !aligned(out, 16) || !aligned(query_starts, 4) || !aligned(key_starts, 4))
+        return PKV_ERR_INVALID_ARG;
+    if (num_key_tokens > 0 && (!kv || !k_rope)) return PKV_ERR_INVALID_ARG;
+    const __int128 to = (__int128)num_query_tokens * d->num_heads * kHeadDim * 2;
+    if (overlap(q, span_bytes(num_query_tokens, d->q_stride, d->num_heads, d->q_head_stride, kHeadDim + kLatentRope), out, to))
+        return PKV_ERR_INVALID_ARG;
+    LatentPromptParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.err = error_word();
+    if (!p.err) return PKV_ERR_CUDA;
+    p.query_starts = query_starts;
+    p.key_starts = key_starts;
+    p.values = kv;
+    p.out = out;
+    p.kv_stride = d->kv_stride;
+    p.kv_head_stride = d->kv_head_stride;
+    p.num_seqs = num_seqs;
+    p.num_heads = d->num_heads;
+    p.num_queries = num_query_tokens;
+    p.num_keys = num_key_tokens;
+    p.max_query_len = max_query_len;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    // [tokens][heads][values]: one copy brings 64 values of one head of 128 tokens (a tensor without tokens is never
+    // copied from; its map only has to exist)
+    const auto heads_map = [&](CUtensorMap* m, const void* base, int64_t tokens, int64_t stride, int64_t head_stride, int width) {
+        const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)d->num_heads, (cuuint64_t)tokens};
+        // a dimension of one entry may have any stride: one that the encoding takes
+        const cuuint64_t strides[2] = {(cuuint64_t)(d->num_heads > 1 ? head_stride : width) * 2,
+                                       (cuuint64_t)(tokens > 1 ? stride : (int64_t)width * d->num_heads) * 2};
+        const cuuint32_t box[3] = {64, 1, 128};
+        return encode_map(m, base, d->dtype, 3, dims, strides, box);
+    };
+    CUtensorMap tmq, tmkv, tmr;
+    pkv_status st = heads_map(&tmq, q, num_query_tokens, d->q_stride, d->q_head_stride, kHeadDim + kLatentRope);
+    if (st != PKV_OK) return st;
+    st = num_key_tokens > 0 ? heads_map(&tmkv, kv, num_key_tokens, d->kv_stride, d->kv_head_stride, 2 * kHeadDim)
+                            : heads_map(&tmkv, q, 1, 0, 2 * kHeadDim, 2 * kHeadDim);
+    if (st != PKV_OK) return st;
+    {
+        const cuuint64_t dims[2] = {kLatentRope, (cuuint64_t)(num_key_tokens > 0 ? num_key_tokens : 1)};
+        const cuuint64_t strides[1] = {(cuuint64_t)(num_key_tokens > 1 ? d->k_rope_stride : kLatentRope) * 2};
+        const cuuint32_t box[2] = {64, 128};
+        st = encode_map(&tmr, num_key_tokens > 0 ? k_rope : q, d->dtype, 2, dims, strides, box);
+        if (st != PKV_OK) return st;
+    }
+    int launches = 0;
+    const cudaError_t e = launch_latent_prompt(p, d->dtype, tmq, tmkv, tmr, static_cast<cudaStream_t>(stream), &launches);
     g_launches += launches;
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

@@ -1,0 +1,330 @@
+// latent_prompt.cu -- latent_attention_prefill: causal attention of whole
+// prompts in the expanded form of latent attention.  Each head has keys of 128
+// values of its own beside the 64 that all heads share, and values of 128:
+//   S = scale (Q_n K_n^T + Q_r K_r^T),  O = softmax(S) V
+// 640 operations a (query, key, head): the tensor cores bound it.
+//
+// A CTA takes 256 queries of one head and walks the keys 128 at a time.  Two
+// streams of 128 queries each, with their own Q (shared memory), S, P and O
+// (tensor memory) and four softmax warps, take turns: while one's products run,
+// the other is in its softmax (softmax_tile.cuh has its arithmetic).  Both
+// streams use each tile of keys and values before it is given back.
+//
+// Shared memory is Q (2 x 48 KiB) and a ring of eight 16 KiB units of 128
+// tokens x 64 values: a tile of keys is three units, a tile of values two.  A
+// unit's copy waits for that unit alone, so the ring holds a tile of values and
+// two of keys in any order.
+//
+// CTAs of one head follow one another, the longest rows first.
+#include "softmax_tile.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kStreamWarps = 4;
+constexpr int kCopyWarp = 2 * kStreamWarps, kProductWarp = kCopyWarp + 1;
+constexpr int kThreads = (kProductWarp + 1) * 32;
+constexpr int kRows = 256;               // queries of a CTA
+constexpr int kTile = 128;               // keys
+constexpr int kUnit = kTile * 128;       // bytes of a ring unit
+constexpr int kKeyUnits = 3, kTileUnits = 5;
+constexpr int kRing = 8;
+constexpr int kLostTiles = 3;            // tiles that some of a CTA's queries mask: 255 keys and a part of one more
+constexpr uint32_t kTmemCols = 512;      // S and P of the streams: [0, 128), [128, 256); O: [256, 384), [384, 512)
+
+struct PromptSmem {
+    static constexpr int kQ = 0;  // [2 streams][3 parts][128 rows][128 B]
+    static constexpr int kKV = kQ + 2 * kKeyUnits * kUnit;
+    static constexpr int kBar = kKV + kRing * kUnit;
+    // full[kRing], empty[kRing], qfull[2], sfull[2], pfull[2], odone[2]
+    static constexpr int kNumBars = 2 * kRing + 8;
+    static constexpr int kAddr = kBar + kNumBars * 8;  // tensor memory address
+    static constexpr int kLost = kAddr + 8;            // [12] keys whose values were taken out, from the first masked tile on
+    static constexpr int kTotal = kLost + kLostTiles * 4 * 4;
+    static_assert(kTotal <= 227 * 1024, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ void both_streams() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// 32 keys from c on as bits: those before `seen`.
+__device__ __forceinline__ uint32_t before(int c, int seen) {
+    return seen - c >= 32 ? ~0u : seen > c ? (1u << (seen - c)) - 1 : 0u;
+}
+
+template <bool kBF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmkv,
+                         const __grid_constant__ CUtensorMap tmr, const LatentPromptParams p) {
+    using S = PromptSmem;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sbase = smem_addr(smem);
+    const uint32_t full0 = sbase + S::kBar, empty0 = full0 + 8 * kRing, qfull0 = empty0 + 8 * kRing, sfull0 = qfull0 + 16,
+                   pfull0 = sfull0 + 16, odone0 = pfull0 + 16;
+    uint32_t* lost = reinterpret_cast<uint32_t*>(smem + S::kLost);
+    const int head = blockIdx.y, seq = blockIdx.z;
+    const int q0 = (int)(gridDim.x - 1 - blockIdx.x) * kRows;  // first query of the CTA in its prompt
+
+    pdl_wait();
+    pdl_launch_dependents();
+    const int a0 = p.query_starts[seq], a1 = p.query_starts[seq + 1], b0 = p.key_starts[seq], b1 = p.key_starts[seq + 1];
+    const bool no_rows = a0 < 0 || a1 < a0 || a1 > p.num_queries;
+    const bool bad = !no_rows && (b0 < 0 || b1 < b0 || b1 > p.num_keys || a1 - a0 > p.max_query_len);
+    if ((no_rows || bad) && tid == 0 && head == 0 && q0 == 0) record_error(p.err, PKV_DEVERR_QUERY);
+    if (no_rows) return;
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    const int nq = a1 - a0;
+    if (bad) {  // its rows become zeros, whatever their number
+        for (int64_t i = (int64_t)q0 * 16 + tid; i < (int64_t)nq * 16; i += kThreads) {
+            if (blockIdx.x != gridDim.x - 1 && i >= (int64_t)(q0 + kRows) * 16) break;
+            *reinterpret_cast<uint4*>(out + ((a0 + i / 16) * p.num_heads + head) * 128 + i % 16 * 8) = make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
+    if (q0 >= nq) return;
+    const int nk = b1 - b0;
+    const int rows = min(kRows, nq - q0);
+    // Query i attends the first i + 1 + nk - nq keys.  Of the CTA: its first row's, and the tiles of each stream.
+    const int seen0 = q0 + 1 + nk - nq;
+    const int tiles_a = max(0, seen0 + min(rows, 128) - 1 + kTile - 1) / kTile;
+    const int tiles_b = rows > 128 ? max(0, seen0 + rows - 1 + kTile - 1) / kTile : 0;
+    const int tiles = max(tiles_a, tiles_b);
+    const int masked = max(0, seen0) / kTile;  // tiles before it hold no key that any row masks
+
+    if (tid == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(qfull0 + 8 * i, 1);
+            mbar_init(sfull0 + 8 * i, 1);
+            mbar_init(pfull0 + 8 * i, kStreamWarps);
+            mbar_init(odone0 + 8 * i, 1);
+        }
+        for (int i = 0; i < kLostTiles * 4; ++i) lost[i] = 0;
+        fence_barrier_init();
+    }
+    if (warp == kProductWarp) tmem_alloc(sbase + S::kAddr, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S::kAddr);
+    bool ok = true;  // no wait has run out
+
+    if (warp == kCopyWarp) {
+        // -------------------------------------------------------------- copies
+        if (lane == 0 && tiles > 0) {
+            prefetch_tensormap(&tmq);
+            prefetch_tensormap(&tmkv);
+            prefetch_tensormap(&tmr);
+            const auto queries = [&](int x) {
+                mbar_arrive_expect_tx(qfull0 + 8 * x, kKeyUnits * kUnit);
+                for (int i = 0; i < kKeyUnits; ++i)
+                    tma_load_3d(sbase + S::kQ + (x * kKeyUnits + i) * kUnit, &tmq, qfull0 + 8 * x, 64 * i, head,
+                                a0 + q0 + 128 * x);
+            };
+            queries(0);
+            int u = 0;  // units so far
+            for (int t = 0; t < tiles && ok; ++t) {
+                for (int i = 0; i < kTileUnits && ok; ++i, ++u) {
+                    const int b = u % kRing;
+                    if (u >= kRing) ok = mbar_wait(empty0 + 8 * b, (u / kRing - 1) & 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(full0 + 8 * b, kUnit);
+                    const uint32_t dst = sbase + S::kKV + b * kUnit;
+                    if (i == 2)
+                        tma_load_2d(dst, &tmr, full0 + 8 * b, 0, b0 + t * kTile);
+                    else
+                        tma_load_3d(dst, &tmkv, full0 + 8 * b, 64 * (i < 2 ? i : i - 1), head, b0 + t * kTile);
+                    if (u == 2 && tiles_b > 0) queries(1);
+                }
+            }
+            if (!ok) record_error(p.err, PKV_DEVERR_TIMEOUT);
+            // every copy has landed before the CTA ends
+            mbar_wait(qfull0, 0);
+            if (tiles_b > 0 && u > 2) mbar_wait(qfull0 + 8, 0);
+            for (int i = max(0, u - kRing); i < u; ++i) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
+        }
+    } else if (warp == kProductWarp) {
+        // ------------------------------------------------------------ products
+        if (lane == 0) {
+            const uint32_t id_s = umma_idesc(kBF16, 128, kTile, false, false);
+            const uint32_t id_o = umma_idesc(kBF16, 128, 128, false, true), id_h = umma_idesc(kBF16, 128, 64, false, true);
+            int pend_x = -1, pend_t = 0;  // a tile whose second product is still to come
+            uint32_t last_bar = 0, last_par = 0;
+            const auto unit = [&](int u) { return sbase + S::kKV + (u % kRing) * kUnit; };
+            const auto landed = [&](int u) { return mbar_wait(full0 + 8 * (u % kRing), (u / kRing) & 1); };
+            const auto values = [&]() {
+                const int x = pend_x, t = pend_t, u = t * kTileUnits + kKeyUnits;
+                pend_x = -1;
+                ok = mbar_wait(pfull0 + 8 * x, t & 1) && landed(u) && landed(u + 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t o = tmem + 256 + 128 * x, pp = tmem + 128 * x, v0 = unit(u), v1 = unit(u + 1);
+                if (v1 > v0) {
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        umma_f16_ts(o, pp + 8 * ks, umma_desc_sw128(v0 + ks * 2048, kUnit, 1024), id_o, t > 0 || ks > 0);
+                } else {  // the two halves of the values do not stand together in the ring
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks) {
+                        umma_f16_ts(o, pp + 8 * ks, umma_desc_sw128(v0 + ks * 2048, 16, 1024), id_h, t > 0 || ks > 0);
+                        umma_f16_ts(o + 64, pp + 8 * ks, umma_desc_sw128(v1 + ks * 2048, 16, 1024), id_h, t > 0 || ks > 0);
+                    }
+                }
+                if (x == 1 || t >= tiles_b) {  // the last to read it
+                    umma_commit(empty0 + 8 * (u % kRing));
+                    umma_commit(empty0 + 8 * ((u + 1) % kRing));
+                }
+                umma_commit(odone0 + 8 * x);
+                last_bar = odone0 + 8 * x;
+                last_par = t & 1;
+            };
+            for (int t = 0; t < tiles && ok; ++t) {
+                for (int x = t < tiles_a ? 0 : 1; x < (t < tiles_b ? 2 : 1) && ok; ++x) {
+                    if (pend_x == x) values();  // P of this stream lies where S goes
+                    if (ok && t == 0) ok = mbar_wait(qfull0 + 8 * x, 0);
+                    const int u = t * kTileUnits;
+                    for (int i = 0; i < kKeyUnits && ok; ++i) {
+                        ok = landed(u + i);
+                        if (!ok) break;
+                        if (i == 0) tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_f16_ss(tmem + 128 * x,
+                                        umma_desc_sw128(sbase + S::kQ + (x * kKeyUnits + i) * kUnit + ks * 32, 16, 1024),
+                                        umma_desc_sw128(unit(u + i) + ks * 32, 16, 1024), id_s, i > 0 || ks > 0);
+                        if (x == 1 || t >= tiles_b) umma_commit(empty0 + 8 * ((u + i) % kRing));
+                    }
+                    if (!ok) break;
+                    umma_commit(sfull0 + 8 * x);
+                    last_bar = sfull0 + 8 * x;
+                    last_par = t & 1;
+                    if (pend_x >= 0) values();
+                    pend_x = x;
+                    pend_t = t;
+                }
+            }
+            if (ok && pend_x >= 0) values();
+            if (!ok) record_error(p.err, PKV_DEVERR_TIMEOUT);
+            // every product that was issued has ended before tensor memory is given back
+            if (last_bar) mbar_wait(last_bar, last_par);
+        }
+    } else {
+        // ------------------------------------------------------------- softmax
+        const int X = warp >> 2, r = tid & 127, row = 128 * X + r;
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t s_addr = lane_addr + 128 * X, o_addr = lane_addr + 256 + 128 * X;
+        const int mine = X ? tiles_b : tiles_a;
+        const int seen = min(nk, seen0 + row);  // keys that this row attends (rows past the prompt's end: whatever)
+        const bool live = 128 * X + 32 * (warp & 3) < rows;
+        float m_run = -INFINITY, l = 0.f;
+        for (int t = 0; t < mine; ++t) {
+            const bool shared = t < tiles_a && t < tiles_b;
+            const bool guard = t >= masked;
+            ok = ok && mbar_wait(sfull0 + 8 * X, t & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (guard) {
+                const int u = t * kTileUnits + kKeyUnits;
+                ok = ok && mbar_wait(full0 + 8 * (u % kRing), (u / kRing) & 1) &&
+                     mbar_wait(full0 + 8 * ((u + 1) % kRing), ((u + 1) / kRing) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    // this thread's key: its values past the prompt become zeros, and those not finite are taken out;
+                    // where both streams use the tile each sees to half of it
+                    const int key = shared ? 64 * X + (r >> 1) : r, pos = t * kTile + key;
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (shared && h != (r & 1)) continue;
+                        uint4* v = reinterpret_cast<uint4*>(smem + S::kKV + ((u + h) % kRing) * kUnit + key * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            uint4 w = make_uint4(0, 0, 0, 0);
+                            if (pos < nk) {
+                                w = v[i];
+                                const uint32_t gone = not_finite2<kBF16>(w.x) | not_finite2<kBF16>(w.y) |
+                                                      not_finite2<kBF16>(w.z) | not_finite2<kBF16>(w.w);
+                                any |= gone;
+                                if (!gone) continue;
+                                w.x = finite_or_zero2<kBF16>(w.x), w.y = finite_or_zero2<kBF16>(w.y);
+                                w.z = finite_or_zero2<kBF16>(w.z), w.w = finite_or_zero2<kBF16>(w.w);
+                            }
+                            v[i] = w;
+                        }
+                    }
+                    if (any) atomicOr(lost + (pos - masked * kTile) / 32, 1u << (pos & 31));
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (shared) both_streams();
+            }
+            if (!ok) continue;
+            if (live) {
+                tc_fence_after();
+                softmax_tile<kBF16>(s_addr, o_addr, guard || !(p.scale_log2 > 0.f), p.scale_log2, t > 0, m_run, l,
+                                    [&](int c) { return before(t * kTile + c, seen); });
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pfull0 + 8 * X);
+        }
+        both_streams();  // (what was taken out is known)
+        if (mine > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(odone0 + 8 * X, (mine - 1) & 1));
+        tc_fence_after();
+        uint32_t any = 0;
+        for (int i = 0; i < kLostTiles * 4; ++i) any |= lost[i];
+        const float inv = ok && l != 0.f ? 1.f / l : 0.f;
+        uint16_t* dst = out + ((int64_t)(a0 + q0 + row) * p.num_heads + head) * 128;
+        for (int c = 0; c < 4; ++c) {
+            float o[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            if (live && ok && mine > 0) {
+                tmem_ld32_start(o_addr + 32 * c, o);
+                tmem_ld_wait32(o);
+            }
+            if (row >= rows) continue;
+            if (any) {
+                for (int w = 0; w < kLostTiles * 4; ++w)
+                    for (uint32_t at = lost[w]; at; at &= at - 1) {
+                        const int pos = masked * kTile + 32 * w + __ffs(at) - 1;
+                        if (pos >= seen) continue;
+                        const uint16_t* v = static_cast<const uint16_t*>(p.values) + (b0 + pos) * p.kv_stride +
+                                            head * p.kv_head_stride + 128 + 32 * c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (not_finite2<kBF16>(v[i])) o[i] += widen16<kBF16>(v[i]);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = inv != 0.f ? pack2<kBF16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv) : 0u;
+                *reinterpret_cast<uint4*>(dst + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kProductWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_prompt(const LatentPromptParams& p, int dtype, const CUtensorMap& tmq, const CUtensorMap& tmkv,
+                                 const CUtensorMap& tmr, cudaStream_t stream, int* launches) {
+    auto kern = dtype == PKV_BF16 ? latent_prompt_kernel<true> : latent_prompt_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem::kTotal);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((p.max_query_len + kRows - 1) / kRows, p.num_heads, p.num_seqs);
+    e = launch_pdl(kern, grid, dim3(kThreads), PromptSmem::kTotal, stream, tmq, tmkv, tmr, p);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+}  // namespace pkv

@@ -1,0 +1,465 @@
+// tree.cu -- paged_attention_tree: attention of the drafted tokens of each
+// sequence (a tree or a chain, the last n positions of its context) over a
+// paged K/V cache.
+//
+// The n x G query rows of a sequence and KV head (G query heads share it; row
+// r is token r / G, head r % G) all read the same keys and values, so they are
+// the M dimension of dense products on the 5th-generation tensor cores, 128
+// keys at a time:
+//   S = Q K^T   A = Q [128 rows x 128 dims] and B = K [128 keys x 128 dims],
+//               both in shared memory, K-major, 128-byte swizzle
+//   O += P V    A = P (16 bits, in tensor memory over the S that it was made
+//               from), B = V, dims-major
+// A unit takes up to 256 rows (256 rows of 2 x 2 x 128 operations a key and dim
+// against 512 bytes of K and V a key: 256 operations a byte, near the 288 that
+// the card has), so K and V leave HBM once for every 256 rows.
+//
+// Two streams, each with a buffer of Q, S and O and four softmax warps, keep
+// the tensor core and the softmax at work at once.  A unit of more than 128
+// rows gives each stream 128 of them, and both walk every tile of keys; one of
+// fewer gives both streams all of its rows, and they walk the odd and the even
+// tiles and join their sums at the end.
+//
+// Each thread of the softmax holds one row of S: the running maximum and sum
+// need no exchange.  The maximum is raised, and O rescaled, only when a score
+// passes it by 2^8 (weights up to 2^8 against the old one are as good).  A
+// weight is rounded to the cache's 16-bit type, for the product; the row's sum
+// is that of the rounded weights, so they add up to one: half a step, 2^-9
+// (bf16), of each weight, some up and some down, where the output is rounded by as much.
+//
+// Warps: 0-3 and 4-7 the streams' softmax, 8 the copies (one TMA copy for each
+// block of K or V, as 8-token groups of 2 KiB, into a ring of five 32 KiB
+// buffers that runs on across units), 9 the products.
+//
+// Keys past the context, drafted tokens that a row does not descend from, and
+// whatever the ring held before count nothing: their scores are replaced, not
+// added to.  Their values meet weights of zero, which an infinity or NaN would
+// turn into NaN; so in the tiles that any row masks, values past the context
+// are zeroed and drafted values that are not finite are taken out, and added to
+// the rows that do attend them when those are written.
+#include "drafted.cuh"
+#include "softmax_tile.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kStreamWarps = 4;
+constexpr int kCopyWarp = 2 * kStreamWarps;
+constexpr int kProductWarp = kCopyWarp + 1;
+constexpr int kThreads = (kProductWarp + 1) * 32;
+constexpr int kTile = 128;                 // keys
+constexpr int kRing = 5;                   // 32 KiB buffers of K or V, in turn
+constexpr int kBuf = kTile * kHeadDim * 2;
+constexpr int kLeast = 4;                  // tiles of a piece
+constexpr uint32_t kTmemCols = 512;        // S and P of the streams: [0, 128), [128, 256); O: [256, 384), [384, 512)
+
+struct TreeSmem {
+    static constexpr int kQ = 0;  // [2 streams][2 dims halves][128 rows][128 B]
+    static constexpr int kKV = kQ + 2 * kBuf;
+    static constexpr int kXch = kKV + kRing * kBuf;  // [256] maximum and sum of each softmax thread
+    static constexpr int kBar = kXch + 256 * 8;
+    // full[kRing], empty[kRing], qfull[2], sfull[2], pfull[2], odone[2]
+    static constexpr int kNumBars = 2 * kRing + 8;
+    static constexpr int kLost = kBar + kNumBars * 8;   // [3] drafted tokens whose values were taken out
+    static constexpr int kSlot = kLost + 3 * 8;         // tensor memory address
+    static constexpr int kBad = kSlot + 8;              // [kRing] a block id outside the pool
+    static constexpr int kTotal = kBad + kRing * 4 + 4;
+    static_assert(kTotal <= 227 * 1024 && kBar % 8 == 0, "shared memory of one CTA");
+    static_assert((kThreads / 32) * 8 + 32 <= kBuf, "the schedule's scratch lies where Q will");
+};
+
+__device__ __forceinline__ void both_streams() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <bool kBF16, int BS>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const DraftParams p) {
+    using S = TreeSmem;
+    using Cursor = DraftCursor<kTreeRows, kTile>;
+    constexpr int D = kHeadDim, kBlocks = kTile / BS;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sbase = smem_addr(smem);
+    const uint32_t full0 = sbase + S::kBar, empty0 = full0 + 8 * kRing, qfull0 = empty0 + 8 * kRing, sfull0 = qfull0 + 16,
+                   pfull0 = sfull0 + 16, odone0 = pfull0 + 16;
+    unsigned long long* lost = reinterpret_cast<unsigned long long*>(smem + S::kLost);
+    volatile int* bad = reinterpret_cast<volatile int*>(smem + S::kBad);
+
+    if (tid == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 1);
+            bad[i] = 0;
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(qfull0 + 8 * i, kStreamWarps);
+            mbar_init(sfull0 + 8 * i, 1);
+            mbar_init(pfull0 + 8 * i, kStreamWarps);
+            mbar_init(odone0 + 8 * i, 1);
+        }
+        for (int i = 0; i < 3; ++i) lost[i] = 0;
+        fence_barrier_init();
+    }
+    if (warp == kCopyWarp && lane == 0) {
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+    }
+    if (warp == kProductWarp) tmem_alloc(sbase + S::kSlot, kTmemCols);
+    pdl_wait();
+    pdl_launch_dependents();  // (the merge kernel waits for this one's end)
+    if (tid == 0) {           // no partials yet
+        p.part_desc[blockIdx.x * 4] = make_int4(0, 0, 0, 0);
+        p.part_desc[blockIdx.x * 4 + 2] = make_int4(0, 0, 0, 0);
+    }
+    Cursor cur;
+    draft_schedule<kTreeRows, kTile, kThreads, kLeast>(p, D, smem + S::kQ, cur);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S::kSlot);
+    DraftItem it;
+    bool ok = true;  // no wait has run out
+
+    if (warp == kCopyWarp) {
+        // -------------------------------------------------------------- copies
+        const uint64_t policy = l2_policy_evict_first();
+        int k = 0;  // buffers filled: K and V of each tile in turn
+        while (ok && cur.next(p, it)) {
+            const int32_t* table = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
+            const int nblk = (it.q.L + BS - 1) / BS;  // <= max_blocks_per_seq
+            int ids = 0;                              // 32 block ids, of 32 / kBlocks tiles
+            for (int t = it.t0; t < it.t1 && ok; ++t) {
+                const int at = (t - it.t0) % (32 / kBlocks) * kBlocks;
+                if (at == 0) {
+                    const int j = t * kBlocks + lane;
+                    ids = j < nblk ? __ldg(table + j) : 0;
+                }
+                int id = __shfl_sync(0xffffffffu, ids, at + lane % kBlocks);
+                const int nb = min(kBlocks, nblk - t * kBlocks);
+                const bool wrong = lane < nb && (id < 0 || id >= p.num_blocks);
+                if (wrong) id = 0;  // keep the shape; the unit's rows become zeros
+                const bool any = __any_sync(0xffffffffu, wrong);
+                if (any && lane == 0) record_error(p.err, PKV_DEVERR_BLOCK_ID);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++k) {
+                    const int b = k % kRing;
+                    if (lane == 0 && k >= kRing) ok = mbar_wait(empty0 + 8 * b, (k / kRing - 1) & 1);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        bad[b] = any;
+                        mbar_arrive_expect_tx(full0 + 8 * b, (uint32_t)nb * BS * D * 2);
+                    }
+                    __syncwarp();
+                    if (lane < nb)
+                        tma_load_4d(sbase + S::kKV + b * kBuf + lane * BS * D * 2, kv ? &tmv : &tmk, full0 + 8 * b, 0, 0, 0,
+                                    (id * p.num_kv_heads + it.kvh) * (BS / 8), policy);
+                }
+            }
+        }
+        if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
+        // every copy has landed before the CTA ends
+        if (lane == 0)
+            for (int i = max(0, k - kRing); i < k; ++i) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
+    } else if (warp == kProductWarp) {
+        // ------------------------------------------------------------ products
+        if (lane == 0) {
+            const uint32_t id_s = umma_idesc(kBF16, 128, kTile, false, false);
+            const uint32_t id_o = umma_idesc(kBF16, 128, D, false, true);
+            int nq[2] = {0, 0}, nsc[2] = {0, 0}, np[2] = {0, 0};  // of each stream: units, products Q K, products P V
+            // the tile whose P V is still to come: QK of the next tile goes first, so that the tensor core has
+            // work while the softmax has its turn
+            int pend_x = -1, pend_b = 0, pend_k = 0, pend_first = 0, pend_frees = 0;
+            uint32_t last_bar = 0, last_par = 0;
+            int j = 0;  // tiles so far
+            const auto values = [&]() {
+                const int x = pend_x;
+                pend_x = -1;
+                ok = mbar_wait(pfull0 + 8 * x, np[x] & 1) && mbar_wait(full0 + 8 * pend_b, (pend_k / kRing) & 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t vb = sbase + S::kKV + pend_b * kBuf;
+#pragma unroll
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                    umma_f16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * ks, umma_desc_sw128(vb + ks * 4096, 1024, 2048),
+                                id_o, !pend_first || ks > 0);
+                if (pend_frees) umma_commit(empty0 + 8 * pend_b);
+                umma_commit(odone0 + 8 * x);
+                last_bar = odone0 + 8 * x;
+                last_par = np[x] & 1;
+                ++np[x];
+            };
+            while (ok && cur.next(p, it)) {
+                const bool two = it.rows > 128;
+                bool begun[2] = {false, false};
+                for (int t = it.t0; t < it.t1 && ok; ++t, ++j) {
+                    const int kk = 2 * j, kb = kk % kRing;
+                    for (int x = two ? 0 : j & 1; x < 2 && ok; ++x) {
+                        if (pend_x == x) values();  // P of this stream lies where S goes
+                        if (!ok) break;
+                        if (!begun[x]) {
+                            ok = mbar_wait(qfull0 + 8 * x, nq[x] & 1);
+                            ++nq[x];
+                        }
+                        ok = ok && mbar_wait(full0 + 8 * kb, (kk / kRing) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t qb = sbase + S::kQ + x * kBuf, kbuf = sbase + S::kKV + kb * kBuf;
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            umma_f16_ss(tmem + 128 * x, umma_desc_sw128(qb + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                                        umma_desc_sw128(kbuf + (ks >> 2) * 1024 + (ks & 3) * 32, 16, 2048), id_s, ks > 0);
+                        if (!two || x == 1) umma_commit(empty0 + 8 * kb);
+                        umma_commit(sfull0 + 8 * x);
+                        last_bar = sfull0 + 8 * x;
+                        last_par = nsc[x]++ & 1;
+                        if (pend_x >= 0) values();
+                        pend_x = x;
+                        pend_k = kk + 1;
+                        pend_b = pend_k % kRing;
+                        pend_first = !begun[x];
+                        pend_frees = !two || x == 1;
+                        begun[x] = true;
+                        if (!two) break;
+                    }
+                }
+            }
+            if (ok && pend_x >= 0) values();
+            if (!ok) record_error(p.err, PKV_DEVERR_TIMEOUT);
+            // every product that was issued has ended before tensor memory is given back
+            if (last_bar) mbar_wait(last_bar, last_par);
+        }
+    } else {
+        // ------------------------------------------------------------- softmax
+        const int X = warp >> 2, r = tid & 127;  // stream, row of its tile (tensor memory lane)
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t s_addr = lane_addr + 128 * X, o_addr = lane_addr + 256;
+        float2* xch = reinterpret_cast<float2*>(smem + S::kXch);
+        int ns = 0, no[2] = {0, 0};  // tiles of this stream; products of both
+        int j = 0, k = 0;            // tiles, items
+        bool more = cur.next(p, it);
+        // Q of an item into this stream's buffer (which its earlier products have read)
+        const auto load_q = [&](const DraftItem& n, int j0) {
+            const bool two = n.rows > 128;
+            if (!two && n.t1 - n.t0 == 1 && (j0 & 1) != X) return;  // no tile of this unit is this stream's
+            const int row = (two ? 128 * X : 0) + r;
+            uint4 v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = make_uint4(0, 0, 0, 0);
+            if (row < n.rows) {
+                const int token = (n.row0 + row) / p.group, g = n.row0 + row - token * p.group;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(p.q) +
+                    ((int64_t)(n.q.tok0 + token) * p.num_q_heads + n.kvh * p.group + g) * D);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = __ldg(src + i);
+            }
+            if ((two ? 128 * X : 0) + 32 * (warp & 3) < n.rows) {
+                uint8_t* dst = smem + S::kQ + X * kBuf + r * 128;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4)) = v[i];
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull0 + 8 * X);
+        };
+        if (more) load_q(it, 0);
+        while (more) {
+            const bool two = it.rows > 128;
+            const int row = (two ? 128 * X : 0) + r;
+            const bool live = (two ? 128 * X : 0) + 32 * (warp & 3) < it.rows;  // some row of the warp is real
+            const int token = min((it.row0 + row) / p.group, it.q.n - 1);
+            const uint64_t mask = row < it.rows ? draft_mask(p, it.q, token) : 0;
+            const int base = it.q.L - it.q.n;
+            float m_run = -INFINITY, l = 0.f;
+            bool begun = false, wrong = false;
+            for (int t = it.t0; t < it.t1; ++t, ++j) {
+                const bool mine = two || (j & 1) == X;
+                ++no[0], ++no[1];
+                if (!two) --no[(j & 1) ^ 1];
+                const bool guard = (t + 1) * kTile > base;
+                const int vk = 2 * j + 1;
+                if (mine) {
+                    ok = ok && mbar_wait(sfull0 + 8 * X, ns & 1) &&
+                         (!guard || mbar_wait(full0 + 8 * (vk % kRing), (vk / kRing) & 1));
+                    ok = __all_sync(0xffffffffu, ok);
+                    ++ns;
+                }
+                if (guard && ok && (mine || two)) {
+                    // this thread's token of V: all of a tile that is the stream's own, half of one that both walk
+                    const int tk = two ? 64 * X + (r >> 1) : r;
+                    const int pos = t * kTile + tk;
+                    if (pos >= base) {
+                        uint4* v = reinterpret_cast<uint4*>(smem + S::kKV + (vk % kRing) * kBuf + (tk >> 3) * 2048 +
+                                                            (tk & 7) * 128 + (two ? (r & 1) * 1024 : 0));
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (two && h) break;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                uint4 w = make_uint4(0, 0, 0, 0);
+                                if (pos < it.q.L) {
+                                    w = v[h * 64 + i];
+                                    const uint32_t lost2 = not_finite2<kBF16>(w.x) | not_finite2<kBF16>(w.y) |
+                                                           not_finite2<kBF16>(w.z) | not_finite2<kBF16>(w.w);
+                                    any |= lost2;
+                                    if (!lost2) continue;
+                                    w.x = finite_or_zero2<kBF16>(w.x), w.y = finite_or_zero2<kBF16>(w.y);
+                                    w.z = finite_or_zero2<kBF16>(w.z), w.w = finite_or_zero2<kBF16>(w.w);
+                                }
+                                v[h * 64 + i] = w;
+                            }
+                        }
+                        if (any) atomicOr(lost + k % 3, 1ull << (pos - base));
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                if (guard && two) both_streams();
+                if (!mine || !ok) continue;
+                if (live) {
+                    tc_fence_after();
+                    softmax_tile<kBF16>(s_addr, o_addr + 128 * X, guard || !(p.scale_log2 > 0.f), p.scale_log2, begun, m_run,
+                                        l, [&](int c) { return draft_visible(t * kTile + c, base, mask); });
+                    tc_fence_before();
+                }
+                begun = true;
+                ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * (vk % kRing), (vk / kRing) & 1));  // (the product waits too)
+                if (!ok) continue;
+                wrong |= bad[vk % kRing] != 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull0 + 8 * X);
+            }
+            // ---- the unit's end: the next unit's queries are fetched first
+            const DraftItem done = it;
+            more = cur.next(p, it);
+            if (ok && more) load_q(it, j);
+            xch[tid] = make_float2(m_run, wrong || !ok ? -1.f : l);
+            if (tid == 0) lost[(k + 1) % 3] = 0;  // (read last before the barrier of the unit before)
+            both_streams();
+            const int x0 = two ? X : 0, x1 = two ? X + 1 : 2;
+            // products whose sums are read: this stream's, or those of both where they walked a tile of the unit
+            bool has[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                has[x] = x >= x0 && x < x1 && (two || done.t1 - done.t0 > 1 || ((j - 1) & 1) == x);
+                if (has[x]) ok = ok && mbar_wait(odone0 + 8 * x, (no[x] - 1) & 1);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            const unsigned long long gone = lost[k % 3];
+            float m = m_run, f0 = 1.f, f1 = 1.f, sum = l;
+            bool zero = !ok || wrong;
+            if (!two) {
+                const float2 a = xch[r], b = xch[128 + r];
+                m = fmaxf(a.x, b.x);
+                const float ms = m == -INFINITY ? 0.f : m;
+                f0 = exp2f(a.x - ms), f1 = exp2f(b.x - ms);
+                zero = !ok || a.y < 0.f || b.y < 0.f;
+                sum = (has[0] ? a.y * f0 : 0.f) + (has[1] ? b.y * f1 : 0.f);
+            }
+            const bool part = done.partial();
+            const float inv = part ? 1.f : (sum != 0.f ? 1.f / sum : 0.f);
+            const int64_t prow = (int64_t)(blockIdx.x * 2 + (done.begins() ? 1 : 0)) * kTreeRows + row;
+            // this thread's dims: all of its row, or with both streams on one row the stream's half
+            const int c0 = two ? 0 : 2 * X, c1 = two ? 4 : 2 * X + 2;
+            const int head = done.kvh * p.group + done.row0 + row - token * p.group;
+            for (int c = c0; c < c1; ++c) {
+                float o[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                if (live && ok) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (!has[x]) continue;
+                        float v[32];
+                        tmem_ld32_start(o_addr + 128 * x + 32 * c, v);
+                        tmem_ld_wait32(v);
+                        const float f = two ? 1.f : x ? f1 : f0;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = f != 0.f ? fmaf(v[i], f, o[i]) : o[i];
+                    }
+                }
+                if (row >= done.rows) continue;
+                if (sum == 0.f) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                }
+                if (unsigned long long at = gone & mask) {
+                    // values that are not finite and were left out of the products (tokens that this item walked)
+                    do {
+                        const int pos = base + __ffsll(at) - 1;
+                        at &= at - 1;
+                        if (pos / kTile < done.t0 || pos / kTile >= done.t1) continue;
+                        const int id = p.block_tables[(int64_t)done.s * p.max_blocks_per_seq + pos / BS];
+                        if (id < 0 || id >= p.num_blocks) continue;
+                        const uint16_t* v = static_cast<const uint16_t*>(p.values) +
+                                            (((int64_t)id * p.num_kv_heads + done.kvh) * BS + pos % BS) * D + 32 * c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (not_finite2<kBF16>(v[i])) o[i] += widen16<kBF16>(v[i]);
+                    } while (at);
+                }
+                if (part) {
+                    float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                                          ((int64_t)(done.q.tok0 + token) * p.num_q_heads + head) * D +
+                                                          32 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = zero ? 0u : pack2<kBF16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
+                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (part && row < done.rows && (two || X == 0)) {
+                p.part_ml[prow] = make_float2(m, zero ? -1.f : sum);
+            }
+            if (part && tid == 0) {
+                int4* d = p.part_desc + (blockIdx.x * 2 + (done.begins() ? 1 : 0)) * 2;
+                d[0] = make_int4(kPartValid | (done.begins() ? kPartBegins : 0) | (done.ends() ? kPartEnds : 0),
+                                 done.q.tok0, done.row0, done.rows);
+                d[1] = make_int4(done.kvh, 0, 0, 0);
+            }
+            tc_fence_before();
+            both_streams();  // both streams' sums have been read
+            tc_fence_after();
+            ++k;
+        }
+        if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kProductWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <bool kBF16, int BS>
+cudaError_t launch_t(const DraftParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream) {
+    auto kern = tree_kernel<kBF16, BS>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem::kTotal);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(p.ctas), dim3(kThreads), TreeSmem::kTotal, stream, tmk, tmv, p);
+}
+
+}  // namespace
+
+cudaError_t launch_tree(const DraftParams& p, int dtype, int block_size, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                        cudaStream_t stream, int* launches) {
+    const bool bf16 = dtype == PKV_BF16;
+    const cudaError_t e = block_size == 16 ? (bf16 ? launch_t<true, 16>(p, tmk, tmv, stream) : launch_t<false, 16>(p, tmk, tmv, stream))
+                                           : (bf16 ? launch_t<true, 32>(p, tmk, tmv, stream) : launch_t<false, 32>(p, tmk, tmv, stream));
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    // a unit of one tile is never divided
+    return p.len_limit > kTile ? launch_draft_merge(p, dtype, kHeadDim, kTreeRows, stream, launches) : cudaSuccess;
+}
+
+}  // namespace pkv
