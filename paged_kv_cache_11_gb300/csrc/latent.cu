@@ -29,8 +29,8 @@
 //
 // Warps: 0-3 the softmax (16 rows each) and the output, 4 the copies of rows, 5
 // the products, 6 the copies of queries.  The maximum is raised lazily, as in
-// tree.cu; a weight is rounded to the cache's 16-bit type and the row's sum is
-// that of the rounded weights.  Masked places are replaced, not added to, and
+// tree.cu; a weight is rounded to the cache's 16-bit type for its product, the
+// row's sum is that of the weights before.  Masked places are replaced, not added to, and
 // values that are not finite are kept out of the products of tiles with masks,
 // as there.
 #include "drafted.cuh"
@@ -362,11 +362,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t wa[8], wb[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float u, v;
-                    wa[i] = pack2<kBF16>(fast_exp2(fmaf(s[4 * i], f, -na)), fast_exp2(fmaf(s[4 * i + 1], f, -na)), u, v);
-                    la += u + v;
-                    wb[i] = pack2<kBF16>(fast_exp2(fmaf(s[4 * i + 2], f, -nb)), fast_exp2(fmaf(s[4 * i + 3], f, -nb)), u, v);
-                    lb += u + v;
+                    const float a0 = fast_exp2(fmaf(s[4 * i], f, -na)), a1 = fast_exp2(fmaf(s[4 * i + 1], f, -na));
+                    const float b0 = fast_exp2(fmaf(s[4 * i + 2], f, -nb)), b1 = fast_exp2(fmaf(s[4 * i + 3], f, -nb));
+                    wa[i] = pack2<kBF16>(a0, a1);
+                    wb[i] = pack2<kBF16>(b0, b1);
+                    la += a0 + a1;
+                    lb += b0 + b1;
                 }
                 // the product before has read P and is in O
                 if (c > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(odone, (c - 1) & 1));

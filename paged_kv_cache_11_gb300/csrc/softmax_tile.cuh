@@ -40,72 +40,128 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // weights up to 2^8 against the old one are as good.
 constexpr float kRaise = 8.f;
 
-// One tile of S (128 columns from s_addr on; this thread's lane is its query row) into the row's running maximum m_run
-// (log2 domain) and sum l, and into P, 16 bits, over the first 64 columns of S; the row's O (128 columns from o_addr on, if
-// `begun`) is rescaled where the maximum is raised.  The row's sum is that of the rounded weights, so that the weights that
-// the products see add up to one.  scaled: the tile has masks, seen(c) says which of keys c .. c + 31 the row attends, or
-// the scale is not above zero; else every key counts and the scale is applied on the way into the exponential.
-//
-// Twice over S, 32 columns at a time, the largest score and then the weights: a row kept in registers between the two does
-// not fit beside the rest (168 registers a thread; 640 bytes of spills a thread), and tensor memory hands 32 columns over in
-// some 32 cycles.
-template <bool kBF16, typename Seen>
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, bool scaled, float scale_log2, bool begun,
-                                             float& m_run, float& l, Seen seen) {
-    const float f = scaled ? 1.f : scale_log2;
-    const auto scores = [&](int c, float (&s)[32]) {
-        tmem_ld_wait32(s);
-        if (scaled) {
-            const uint32_t bits = seen(32 * c);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1 ? s[i] * scale_log2 : -INFINITY;
-        }
-    };
-    float s[2][32];
-    float mx = -INFINITY;
-    tmem_ld32_start(s_addr, s[0]);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        scores(c, s[c & 1]);
-        if (c < 3) tmem_ld32_start(s_addr + 32 * (c + 1), s[(c + 1) & 1]);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(s[c & 1][i], s[c & 1][i + 1]));
-    }
-    tmem_ld32_start(s_addr, s[0]);
-    mx *= f;
+// Two fp32 values in a register pair, and their arithmetic.
+typedef uint64_t f32x2;
+__device__ __forceinline__ f32x2 pack_f32x2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma_f32x2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add_f32x2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Raises the row's maximum to mx where that passes it, and rescales what the row has summed.
+__device__ __forceinline__ void raise_maximum(float mx, uint32_t o_addr, bool begun, float& m_run, float& l) {
     const bool raise = mx > m_run + kRaise;
+    if (!__any_sync(0xffffffffu, raise)) return;
     float alpha = 1.f;
     if (raise) {
         alpha = m_run == -INFINITY ? 0.f : exp2f(m_run - mx);
         m_run = mx;
         l *= alpha;
     }
-    if (begun && __any_sync(0xffffffffu, raise)) {
+    if (!begun) return;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tmem_ld32_start(o_addr + 32 * c, o);
+        tmem_ld_wait32(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= alpha;
+        tmem_st32(o_addr + 32 * c, o);
+    }
+}
+
+// 32 scores v to weights 2^(v f - ms): 16 pairs to `w`, their sum added to `sum`.
+template <bool kBF16>
+__device__ __forceinline__ void weights32(const float (&v)[32], f32x2 f, f32x2 neg_ms, uint32_t (&w)[16], f32x2& sum) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 x = unpack_f32x2(fma_f32x2(pack_f32x2(v[2 * i], v[2 * i + 1]), f, neg_ms));
+        const float a = fast_exp2(x.x), b = fast_exp2(x.y);
+        w[i] = pack2<kBF16>(a, b);
+        sum = add_f32x2(sum, pack_f32x2(a, b));
+    }
+}
+
+// One tile of S (128 columns from s_addr on; this thread's lane is its query row) into the row's running maximum m_run
+// (log2 domain) and sum l, and into P, 16 bits, over the first 64 columns of S; the row's O (128 columns from o_addr on, if
+// `begun`) is rescaled where the maximum is raised.  masked: the tile has masks, seen(c) says which of keys c .. c + 31 the row
+// attends, or the scale is not above zero; else every key counts and the scale is applied on the way into the exponential.
+//
+// Twice over S, 32 columns at a time, the largest score and then the weights: a row kept in registers between the two does
+// not fit beside the rest (168 registers a thread).  The two kinds of tile are apart, and the rare one is a loop: with both
+// in one unrolled body the warps waited for instructions more than for anything else but the products (2.8 of 13 cycles an
+// instruction).
+template <bool kBF16, typename Seen>
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, bool masked, float scale_log2, bool begun,
+                                             float& m_run, float& l, Seen seen) {
+    f32x2 sum = pack_f32x2(0.f, 0.f);
+    if (!masked) {
+        float s[2][32];
+        float mx = -INFINITY;
+        tmem_ld32_start(s_addr, s[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait32(s[c & 1]);
+            tmem_ld32_start(s_addr + 32 * ((c + 1) & 3), s[(c + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(s[c & 1][i], s[c & 1][i + 1]));
+        }
+        raise_maximum(mx * scale_log2, o_addr, begun, m_run, l);
+        const float ms = m_run == -INFINITY ? 0.f : m_run;
+        const f32x2 f = pack_f32x2(scale_log2, scale_log2), neg = pack_f32x2(-ms, -ms);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait32(s[c & 1]);
+            if (c < 3) tmem_ld32_start(s_addr + 32 * (c + 1), s[(c + 1) & 1]);
+            uint32_t w[16];
+            weights32<kBF16>(s[c & 1], f, neg, w, sum);
+            tmem_st16_start(s_addr + 16 * c, w);  // over columns that have been read
+        }
+    } else {
+        const auto scores = [&](int c, float (&s)[32]) {
+            tmem_ld32_start(s_addr + 32 * c, s);
+            tmem_ld_wait32(s);
+            const uint32_t bits = seen(32 * c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1 ? s[i] * scale_log2 : -INFINITY;
+        };
+        float mx = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-            float o[32];
-            tmem_ld32_start(o_addr + 32 * c, o);
-            tmem_ld_wait32(o);
+            float s[32];
+            scores(c, s);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st32(o_addr + 32 * c, o);
+            for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(s[i], s[i + 1]));
+        }
+        raise_maximum(mx, o_addr, begun, m_run, l);
+        const float ms = m_run == -INFINITY ? 0.f : m_run;
+        const f32x2 f = pack_f32x2(1.f, 1.f), neg = pack_f32x2(-ms, -ms);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            float s[32];
+            scores(c, s);
+            uint32_t w[16];
+            weights32<kBF16>(s, f, neg, w, sum);
+            tmem_st16_start(s_addr + 16 * c, w);
         }
     }
-    const float ms = m_run == -INFINITY ? 0.f : m_run;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float(&v)[32] = s[c & 1];
-        scores(c, v);
-        if (c < 3) tmem_ld32_start(s_addr + 32 * (c + 1), s[(c + 1) & 1]);
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float a, b;
-            w[i] = pack2<kBF16>(fast_exp2(fmaf(v[2 * i], f, -ms)), fast_exp2(fmaf(v[2 * i + 1], f, -ms)), a, b);
-            l += a + b;
-        }
-        tmem_st16_start(s_addr + 16 * c, w);  // over columns that have been read
-    }
+    const float2 both = unpack_f32x2(sum);
+    l += both.x + both.y;
     tmem_st_wait();
 }
 

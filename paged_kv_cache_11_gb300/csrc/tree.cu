@@ -23,9 +23,9 @@
 // Each thread of the softmax holds one row of S: the running maximum and sum
 // need no exchange.  The maximum is raised, and O rescaled, only when a score
 // passes it by 2^8 (weights up to 2^8 against the old one are as good).  A
-// weight is rounded to the cache's 16-bit type, for the product; the row's sum
-// is that of the rounded weights, so they add up to one: half a step, 2^-9
-// (bf16), of each weight, some up and some down, where the output is rounded by as much.
+// weight is rounded to the cache's 16-bit type for the product, half a step at
+// most, 2^-8 (bf16), of each weight, some up and some down, where the output is
+// rounded by as much; the row's sum is that of the weights before, in 32 bits.
 //
 // Warps: 0-3 and 4-7 the streams' softmax, 8 the copies (one TMA copy for each
 // block of K or V, as 8-token groups of 2 KiB, into a ring of five 32 KiB
