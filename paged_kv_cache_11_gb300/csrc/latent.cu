@@ -207,58 +207,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kProductWarp) {
         // ------------------------------------------------------------ products
-        if (lane == 0) {
-            const uint32_t id_s = umma_idesc(kBF16, kLatentRows, kTile, false, false);
-            uint32_t id_o = 0;  // of the tile whose second product is still to come
-            int pend = -1, pend_first = 0, np = 0, nq = 0, c = 0;
-            uint32_t last_bar = 0, last_par = 0;
-            const auto values = [&]() {
-                ok = mbar_wait(pfull, np & 1);
-                if (!ok) return;
+        // Whichever is ready goes first, P V (which frees slots) before Q K (of at most two tiles ahead): a fixed order
+        // would have the one wait for copies that the other makes room for.
+        const uint32_t el = issuing_lane(), tm = __shfl_sync(0xffffffffu, tmem, 0), sb = __shfl_sync(0xffffffffu, sbase, 0);
+        const uint32_t id_s = umma_idesc(kBF16, kLatentRows, kTile, false, false);
+        const uint64_t q_desc = umma_desc_sw128(sb + S::kQ, 16, 1024), k_desc = umma_desc_sw128(sb + S::kKV, 16, kGroup),
+                       v_desc = umma_desc_sw128(sb + S::kKV, 1024, kGroup),
+                       p_desc = umma_desc_sw128(sb + S::kP, 16, 1024);  // + (bytes / 16)
+        constexpr uint32_t kTileStep = kSlots * kSlot / 16;
+        uint32_t nk = 0, np = 0, nq = 0;        // tiles whose Q K, whose P V was issued; units begun
+        int left = 0;                           // tiles of the unit whose Q K is still to come
+        bool first = false, more = true;
+        uint32_t pend_first = 0, pend_id[2];    // of the tiles between the two products: begins a unit (bits), P V's shape
+        pend_id[0] = pend_id[1] = 0;
+        uint32_t id_o = 0;
+        uint32_t last_bar = 0, last_par = 0;
+        uint64_t since = 0;  // of a wait
+        while (ok) {
+            if (left == 0 && more) {
+                more = cur.next(p, it);
+                left = __shfl_sync(0xffffffffu, more ? it.t1 - it.t0 : 0, 0);
+                more = left > 0;
+                id_o = umma_idesc(kBF16, 128, (__shfl_sync(0xffffffffu, it.rows, 0) + 15) / 16 * 16, true, false);
+                first = true;
+            }
+            if (np < nk && mbar_test_warp(pfull, np & 1)) {
                 tc_fence_after();
-                const uint32_t vb = sbase + S::kKV + (pend & 1) * kSlots * kSlot;
+                const uint32_t b = np & 1, id = b ? pend_id[1] : pend_id[0], begins = pend_first >> b & 1;
+                const uint64_t vd = v_desc + b * kTileStep;
+#pragma unroll
                 for (int ks = 0; ks < kSlots; ++ks) {
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
-                        umma_f16_ss(tmem + 64 * mt, umma_desc_sw128(vb + ks * kSlot + mt * 2048, 1024, kGroup),
-                                    umma_desc_sw128(sbase + S::kP + ks * 32, 16, 1024), id_o, !pend_first || ks > 0);
-                    umma_commit(empty0 + 8 * ((pend & 1) * kSlots + ks));
+                        umma_f16_ss(el, tm + 64 * mt, vd + ks * (kSlot / 16) + mt * 128, p_desc + ks * 2, id, !begins || ks > 0);
+                    umma_commit(el, empty0 + 8 * (b * kSlots + ks));
                 }
-                umma_commit(odone);
+                umma_commit(el, odone);
                 last_bar = odone;
                 last_par = np & 1;
                 ++np;
-                pend = -1;
-            };
-            while (ok && cur.next(p, it)) {
-                ok = mbar_wait(qfull, nq & 1);
-                ++nq;
-                for (int t = it.t0; t < it.t1 && ok; ++t, ++c) {
-                    const int b = c & 1;
-                    for (int i = 0; i < kSlots && ok; ++i) ok = mbar_wait(full0 + 8 * (b * kSlots + i), (c / 2) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t kb = sbase + S::kKV + b * kSlots * kSlot;
-#pragma unroll
-                    for (int ks = 0; ks < kRow / 16; ++ks)
-                        umma_f16_ss(tmem + 256 + 64 * b,
-                                    umma_desc_sw128(sbase + S::kQ + (ks >> 2) * (kLatentRows * 128) + (ks & 3) * 32, 16, 1024),
-                                    umma_desc_sw128(kb + (ks >> 2) * 1024 + (ks & 3) * 32, 16, kGroup), id_s, ks > 0);
-                    if (t + 1 == it.t1) umma_commit(qempty);
-                    umma_commit(sfull0 + 8 * b);
-                    last_bar = sfull0 + 8 * b;
-                    last_par = (c / 2) & 1;
-                    if (pend >= 0) values();
-                    pend = c;
-                    pend_first = t == it.t0;
-                    id_o = umma_idesc(kBF16, 128, (it.rows + 15) / 16 * 16, true, false);
-                }
+                since = 0;
+                continue;
             }
-            if (ok && pend >= 0) values();
-            if (!ok) record_error(p.err, PKV_DEVERR_TIMEOUT);
-            // every product that was issued has ended before tensor memory is given back
-            if (last_bar) mbar_wait(last_bar, last_par);
+            if (left > 0 && nk - np < 2 && (!first || mbar_test_warp(qfull, nq & 1)) &&
+                mbar_test_warp(full0 + 8 * ((nk & 1) * kSlots + kSlots - 1), (nk / 2) & 1)) {
+                const uint32_t b = nk & 1;
+                // (the slots before the last one landed before it, or soon will)
+                for (int i = 0; i < kSlots - 1 && ok; ++i) ok = mbar_wait_warp(full0 + 8 * (b * kSlots + i), (nk / 2) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t kd = k_desc + b * kTileStep;
+#pragma unroll
+                for (int ks = 0; ks < kRow / 16; ++ks)
+                    umma_f16_ss(el, tm + 256 + 64 * b, q_desc + (ks >> 2) * (kLatentRows * 128 / 16) + (ks & 3) * 2,
+                                kd + (ks >> 2) * 64 + (ks & 3) * 2, id_s, ks > 0);
+                --left;
+                if (left == 0) umma_commit(el, qempty);
+                umma_commit(el, sfull0 + 8 * b);
+                last_bar = sfull0 + 8 * b;
+                last_par = (nk / 2) & 1;
+                pend_first = (pend_first & ~(1u << b)) | (uint32_t)first << b;
+                if (b)
+                    pend_id[1] = id_o;
+                else
+                    pend_id[0] = id_o;
+                nq += first;
+                first = false;
+                ++nk;
+                since = 0;
+                continue;
+            }
+            if (!more && left == 0 && np == nk) break;
+            const uint64_t now = global_timer_ns();
+            if (since == 0) since = now;
+            ok = __shfl_sync(0xffffffffu, now - since <= kWaitLimitNs, 0);
         }
+        if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
+        // every product that was issued has ended before tensor memory is given back
+        if (last_bar) mbar_wait(last_bar, last_par);
     } else {
         // ------------------------------------------------------------- softmax
         const int ra = 16 * warp + (lane >> 2), rb = ra + 8;  // this thread's rows

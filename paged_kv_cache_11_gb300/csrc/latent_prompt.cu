@@ -148,69 +148,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kProductWarp) {
         // ------------------------------------------------------------ products
-        if (lane == 0) {
-            const uint32_t id_s = umma_idesc(kBF16, 128, kTile, false, false);
-            const uint32_t id_o = umma_idesc(kBF16, 128, 128, false, true), id_h = umma_idesc(kBF16, 128, 64, false, true);
-            int pend_x = -1, pend_t = 0;  // a tile whose second product is still to come
-            uint32_t last_bar = 0, last_par = 0;
-            const auto unit = [&](int u) { return sbase + S::kKV + (u % kRing) * kUnit; };
-            const auto landed = [&](int u) { return mbar_wait(full0 + 8 * (u % kRing), (u / kRing) & 1); };
-            const auto values = [&]() {
-                const int x = pend_x, t = pend_t, u = t * kTileUnits + kKeyUnits;
-                pend_x = -1;
-                ok = mbar_wait(pfull0 + 8 * x, t & 1) && landed(u) && landed(u + 1);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t o = tmem + 256 + 128 * x, pp = tmem + 128 * x, v0 = unit(u), v1 = unit(u + 1);
-                if (v1 > v0) {
+        const uint32_t el = issuing_lane(), tm = __shfl_sync(0xffffffffu, tmem, 0), sb = __shfl_sync(0xffffffffu, sbase, 0);
+        const int ta = __shfl_sync(0xffffffffu, tiles_a, 0), tb = __shfl_sync(0xffffffffu, tiles_b, 0), tn = max(ta, tb);
+        const uint32_t id_s = umma_idesc(kBF16, 128, kTile, false, false);
+        const uint32_t id_o = umma_idesc(kBF16, 128, 128, false, true), id_h = umma_idesc(kBF16, 128, 64, false, true);
+        const uint64_t q_desc = umma_desc_sw128(sb + S::kQ, 16, 1024), k_desc = umma_desc_sw128(sb + S::kKV, 16, 1024),
+                       v_desc = umma_desc_sw128(sb + S::kKV, kUnit, 1024);  // + (bytes / 16)
+        int pend_x = -1, pend_t = 0;  // a tile whose second product is still to come
+        uint32_t last_bar = 0, last_par = 0;
+        const auto landed = [&](uint32_t u) { return mbar_wait_warp(full0 + 8 * (u % kRing), (u / kRing) & 1); };
+        const auto values = [&]() {
+            const uint32_t x = pend_x, t = pend_t, u = t * kTileUnits + kKeyUnits;
+            pend_x = -1;
+            ok = mbar_wait_warp(pfull0 + 8 * x, t & 1) && landed(u) && landed(u + 1);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t o = tm + 256 + 128 * x, pp = tm + 128 * x, at = u % kRing;
+            if (at + 1 < kRing) {
+                const uint64_t vd = v_desc + at * (kUnit / 16);
 #pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        umma_f16_ts(o, pp + 8 * ks, umma_desc_sw128(v0 + ks * 2048, kUnit, 1024), id_o, t > 0 || ks > 0);
-                } else {  // the two halves of the values do not stand together in the ring
-#pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks) {
-                        umma_f16_ts(o, pp + 8 * ks, umma_desc_sw128(v0 + ks * 2048, 16, 1024), id_h, t > 0 || ks > 0);
-                        umma_f16_ts(o + 64, pp + 8 * ks, umma_desc_sw128(v1 + ks * 2048, 16, 1024), id_h, t > 0 || ks > 0);
-                    }
-                }
-                if (x == 1 || t >= tiles_b) {  // the last to read it
-                    umma_commit(empty0 + 8 * (u % kRing));
-                    umma_commit(empty0 + 8 * ((u + 1) % kRing));
-                }
-                umma_commit(odone0 + 8 * x);
-                last_bar = odone0 + 8 * x;
-                last_par = t & 1;
-            };
-            for (int t = 0; t < tiles && ok; ++t) {
-                for (int x = t < tiles_a ? 0 : 1; x < (t < tiles_b ? 2 : 1) && ok; ++x) {
-                    if (pend_x == x) values();  // P of this stream lies where S goes
-                    if (ok && t == 0) ok = mbar_wait(qfull0 + 8 * x, 0);
-                    const int u = t * kTileUnits;
-                    for (int i = 0; i < kKeyUnits && ok; ++i) {
-                        ok = landed(u + i);
-                        if (!ok) break;
-                        if (i == 0) tc_fence_after();
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            umma_f16_ss(tmem + 128 * x,
-                                        umma_desc_sw128(sbase + S::kQ + (x * kKeyUnits + i) * kUnit + ks * 32, 16, 1024),
-                                        umma_desc_sw128(unit(u + i) + ks * 32, 16, 1024), id_s, i > 0 || ks > 0);
-                        if (x == 1 || t >= tiles_b) umma_commit(empty0 + 8 * ((u + i) % kRing));
-                    }
-                    if (!ok) break;
-                    umma_commit(sfull0 + 8 * x);
-                    last_bar = sfull0 + 8 * x;
-                    last_par = t & 1;
-                    if (pend_x >= 0) values();
-                    pend_x = x;
-                    pend_t = t;
+                for (int ks = 0; ks < kTile / 16; ++ks) umma_f16_ts(el, o, pp + 8 * ks, vd + ks * 128, id_o, t > 0 || ks > 0);
+            } else {  // the two halves of the values do not stand together in the ring
+                const uint64_t v0 = k_desc + at * (kUnit / 16), v1 = k_desc;
+#pragma unroll 1
+                for (int ks = 0; ks < kTile / 16; ++ks) {
+                    umma_f16_ts(el, o, pp + 8 * ks, v0 + ks * 128, id_h, t > 0 || ks > 0);
+                    umma_f16_ts(el, o + 64, pp + 8 * ks, v1 + ks * 128, id_h, t > 0 || ks > 0);
                 }
             }
-            if (ok && pend_x >= 0) values();
-            if (!ok) record_error(p.err, PKV_DEVERR_TIMEOUT);
-            // every product that was issued has ended before tensor memory is given back
-            if (last_bar) mbar_wait(last_bar, last_par);
+            if (x == 1 || t >= (uint32_t)tb) {  // the last to read it
+                umma_commit(el, empty0 + 8 * at);
+                umma_commit(el, empty0 + 8 * ((u + 1) % kRing));
+            }
+            umma_commit(el, odone0 + 8 * x);
+            last_bar = odone0 + 8 * x;
+            last_par = t & 1;
+        };
+        for (int t = 0; t < tn && ok; ++t) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (t >= (x ? tb : ta) || !ok) continue;
+                if (pend_x == x) values();  // P of this stream lies where S goes
+                if (ok && t == 0) ok = mbar_wait_warp(qfull0 + 8 * x, 0);
+                const uint32_t u = t * kTileUnits;
+#pragma unroll
+                for (int i = 0; i < kKeyUnits; ++i) {
+                    ok = ok && landed(u + i);
+                    if (!ok) break;
+                    if (i == 0) tc_fence_after();
+                    const uint32_t at = (u + i) % kRing;
+                    const uint64_t qd = q_desc + (x * kKeyUnits + i) * (kUnit / 16), kd = k_desc + at * (kUnit / 16);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        umma_f16_ss(el, tm + 128 * x, qd + 2 * ks, kd + 2 * ks, id_s, i > 0 || ks > 0);
+                    if (x == 1 || t >= tb) umma_commit(el, empty0 + 8 * at);
+                }
+                if (!ok) break;
+                umma_commit(el, sfull0 + 8 * x);
+                last_bar = sfull0 + 8 * x;
+                last_par = t & 1;
+                if (pend_x >= 0) values();
+                pend_x = x;
+                pend_t = t;
+            }
         }
+        if (ok && pend_x >= 0) values();
+        if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
+        // every product that was issued has ended before tensor memory is given back
+        if (last_bar) mbar_wait(last_bar, last_par);
     } else {
         // ------------------------------------------------------------- softmax
         const int X = warp >> 2, r = tid & 127, row = 128 * X + r;

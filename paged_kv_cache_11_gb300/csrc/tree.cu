@@ -162,72 +162,74 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = max(0, k - kRing); i < k; ++i) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
     } else if (warp == kProductWarp) {
         // ------------------------------------------------------------ products
-        if (lane == 0) {
-            const uint32_t id_s = umma_idesc(kBF16, 128, kTile, false, false);
-            const uint32_t id_o = umma_idesc(kBF16, 128, D, false, true);
-            int nq[2] = {0, 0}, nsc[2] = {0, 0}, np[2] = {0, 0};  // of each stream: units, products Q K, products P V
-            // the tile whose P V is still to come: QK of the next tile goes first, so that the tensor core has
-            // work while the softmax has its turn
-            int pend_x = -1, pend_b = 0, pend_k = 0, pend_first = 0, pend_frees = 0;
-            uint32_t last_bar = 0, last_par = 0;
-            int j = 0;  // tiles so far
-            const auto values = [&]() {
-                const int x = pend_x;
-                pend_x = -1;
-                ok = mbar_wait(pfull0 + 8 * x, np[x] & 1) && mbar_wait(full0 + 8 * pend_b, (pend_k / kRing) & 1);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t vb = sbase + S::kKV + pend_b * kBuf;
+        const uint32_t el = issuing_lane(), tm = __shfl_sync(0xffffffffu, tmem, 0), sb = __shfl_sync(0xffffffffu, sbase, 0);
+        const uint32_t id_s = umma_idesc(kBF16, 128, kTile, false, false), id_o = umma_idesc(kBF16, 128, D, false, true);
+        const uint64_t q_desc = umma_desc_sw128(sb + S::kQ, 16, 1024), k_desc = umma_desc_sw128(sb + S::kKV, 16, 2048),
+                       v_desc = umma_desc_sw128(sb + S::kKV, 1024, 2048);  // + (bytes / 16)
+        uint32_t nq[2] = {0, 0}, nsc[2] = {0, 0}, np[2] = {0, 0};  // of each stream: units, products Q K, products P V
+        // the tile whose P V is still to come: QK of the next tile goes first, so that the tensor core has
+        // work while the softmax has its turn
+        int pend_x = -1;
+        uint32_t pend_k = 0, pend_first = 0, pend_frees = 0;
+        uint32_t last_bar = 0, last_par = 0;
+        uint32_t kk = 0;  // buffers so far
+        const auto values = [&]() {
+            const uint32_t x = pend_x, pb = pend_k % kRing;
+            pend_x = -1;
+            ok = mbar_wait_warp(pfull0 + 8 * x, np[x] & 1) && mbar_wait_warp(full0 + 8 * pb, (pend_k / kRing) & 1);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t vd = v_desc + pb * (kBuf / 16);
 #pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks)
-                    umma_f16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * ks, umma_desc_sw128(vb + ks * 4096, 1024, 2048),
-                                id_o, !pend_first || ks > 0);
-                if (pend_frees) umma_commit(empty0 + 8 * pend_b);
-                umma_commit(odone0 + 8 * x);
-                last_bar = odone0 + 8 * x;
-                last_par = np[x] & 1;
-                ++np[x];
-            };
-            while (ok && cur.next(p, it)) {
-                const bool two = it.rows > 128;
-                bool begun[2] = {false, false};
-                for (int t = it.t0; t < it.t1 && ok; ++t, ++j) {
-                    const int kk = 2 * j, kb = kk % kRing;
-                    for (int x = two ? 0 : j & 1; x < 2 && ok; ++x) {
-                        if (pend_x == x) values();  // P of this stream lies where S goes
-                        if (!ok) break;
-                        if (!begun[x]) {
-                            ok = mbar_wait(qfull0 + 8 * x, nq[x] & 1);
-                            ++nq[x];
-                        }
-                        ok = ok && mbar_wait(full0 + 8 * kb, (kk / kRing) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t qb = sbase + S::kQ + x * kBuf, kbuf = sbase + S::kKV + kb * kBuf;
+            for (int ks = 0; ks < kTile / 16; ++ks)
+                umma_f16_ts(el, tm + 256 + 128 * x, tm + 128 * x + 8 * ks, vd + ks * 256, id_o, !pend_first || ks > 0);
+            if (pend_frees) umma_commit(el, empty0 + 8 * pb);
+            umma_commit(el, odone0 + 8 * x);
+            last_bar = odone0 + 8 * x;
+            last_par = np[x] & 1;
+            ++np[x];
+        };
+        for (;;) {
+            const bool more = cur.next(p, it);
+            const int n = __shfl_sync(0xffffffffu, more && ok ? it.t1 - it.t0 : 0, 0);
+            const bool two = __shfl_sync(0xffffffffu, it.rows, 0) > 128;
+            if (n == 0) break;
+            bool begun[2] = {false, false};
+            for (int t = 0; t < n && ok; ++t, kk += 2) {
+                const uint32_t kb = kk % kRing;
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            umma_f16_ss(tmem + 128 * x, umma_desc_sw128(qb + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                                        umma_desc_sw128(kbuf + (ks >> 2) * 1024 + (ks & 3) * 32, 16, 2048), id_s, ks > 0);
-                        if (!two || x == 1) umma_commit(empty0 + 8 * kb);
-                        umma_commit(sfull0 + 8 * x);
-                        last_bar = sfull0 + 8 * x;
-                        last_par = nsc[x]++ & 1;
-                        if (pend_x >= 0) values();
-                        pend_x = x;
-                        pend_k = kk + 1;
-                        pend_b = pend_k % kRing;
-                        pend_first = !begun[x];
-                        pend_frees = !two || x == 1;
-                        begun[x] = true;
-                        if (!two) break;
+                for (int x = 0; x < 2; ++x) {
+                    if (!two && x != (kk >> 1 & 1)) continue;
+                    if (pend_x == x && ok) values();  // P of this stream lies where S goes
+                    if (!begun[x] && ok) {
+                        ok = mbar_wait_warp(qfull0 + 8 * x, nq[x] & 1);
+                        ++nq[x];
                     }
+                    ok = ok && mbar_wait_warp(full0 + 8 * kb, (kk / kRing) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t qd = q_desc + x * (kBuf / 16), kd = k_desc + kb * (kBuf / 16);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        umma_f16_ss(el, tm + 128 * x, qd + (ks >> 2) * 1024 + (ks & 3) * 2, kd + (ks >> 2) * 64 + (ks & 3) * 2,
+                                    id_s, ks > 0);
+                    if (!two || x == 1) umma_commit(el, empty0 + 8 * kb);
+                    umma_commit(el, sfull0 + 8 * x);
+                    last_bar = sfull0 + 8 * x;
+                    last_par = nsc[x]++ & 1;
+                    if (pend_x >= 0) values();
+                    pend_x = x;
+                    pend_k = kk + 1;
+                    pend_first = !begun[x];
+                    pend_frees = !two || x == 1;
+                    begun[x] = true;
                 }
             }
-            if (ok && pend_x >= 0) values();
-            if (!ok) record_error(p.err, PKV_DEVERR_TIMEOUT);
-            // every product that was issued has ended before tensor memory is given back
-            if (last_bar) mbar_wait(last_bar, last_par);
         }
+        if (ok && pend_x >= 0) values();
+        if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
+        // every product that was issued has ended before tensor memory is given back
+        if (last_bar) mbar_wait(last_bar, last_par);
     } else {
         // ------------------------------------------------------------- softmax
         const int X = warp >> 2, r = tid & 127;  // stream, row of its tile (tensor memory lane)
