@@ -9,56 +9,113 @@
 
 namespace pkv {
 
-constexpr int kMergeThreads = 128;
-constexpr int kMergeSlices = 16;  // CTAs of one unit
+constexpr int kMergeThreads = 256;
+constexpr int kMergeSlices = 4;    // CTAs of one unit
+constexpr int kMergeItems = 8;     // float4 of a thread
+constexpr int kMergeParts = 128;   // pieces at a time
 
-template <bool kBF16, int D>
-__global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftParams p, int unit_rows) {
+// kRows: of a slice, at most.
+template <bool kBF16, int D, int kRows>
+__global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftParams p) {
+    static_assert(kRows * D / 4 == kMergeThreads * kMergeItems, "every thread has its items");
+    constexpr int kUnitRows = kRows * kMergeSlices;
+    __shared__ float weight[kRows][kMergeParts];
+    __shared__ float top[kRows], total[kRows];
+    __shared__ int last_s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+    if (tid == 0) last_s = p.ctas - 1;
     pdl_wait();
-    const int c = blockIdx.x;
     const int4 d = __ldcg(p.part_desc + (c * 2 + 1) * 2);
     const int state = d.x, tok0 = d.y, row0 = d.z, rows = d.w;
     if (!(state & kPartValid) || (state & kPartEnds)) return;  // no unit begins here and ends elsewhere
     const int kvh = __ldcg(p.part_desc + (c * 2 + 1) * 2 + 1).x;
-    int last = c + 1;  // the CTA that holds the unit's last tile
-    while (last < p.ctas - 1 && !(__ldcg(p.part_desc + last * 4).x & kPartEnds)) ++last;
-    const int per = (rows + kMergeSlices - 1) / kMergeSlices, r0 = blockIdx.y * per, r1 = min(rows, r0 + per);
-    for (int i = r0 * (D / 4) + threadIdx.x; i < r1 * (D / 4); i += kMergeThreads) {
-        const int r = i / (D / 4), d4 = i - r * (D / 4);
-        float M = -INFINITY;
+    const int r0 = blockIdx.y * kRows, n = min(kRows, rows - r0);
+    if (n <= 0) return;
+    __syncthreads();
+    // the CTA that holds the unit's last tile: the first behind this one that ends a unit which it did not begin
+    for (int k = c + 1 + tid; k < p.ctas; k += kMergeThreads)
+        if (__ldcg(p.part_desc + k * 4).x & kPartEnds) {
+            atomicMin(&last_s, k);
+            break;
+        }
+    __syncthreads();
+    const int parts = last_s - c + 1;
+    const auto at = [&](int k, int r) { return (int64_t)((c + k) * 2 + (k == 0)) * kUnitRows + r0 + r; };
+    // each row's largest maximum and its weight in all, a warp to a row
+    for (int r = warp; r < n; r += kMergeThreads / 32) {
+        float m = -INFINITY;
         bool bad = false;
-        for (int k = c; k <= last; ++k) {
-            const float2 ml = __ldcg(p.part_ml + (int64_t)(k * 2 + (k == c)) * unit_rows + r);
-            M = fmaxf(M, ml.x);
+        for (int k = lane; k < parts; k += 32) {
+            const float2 ml = __ldcg(p.part_ml + at(k, r));
+            m = fmaxf(m, ml.x);
             bad |= ml.y < 0.f;
         }
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         float l = 0.f;
-        if (!bad && M != -INFINITY) {
-            for (int k = c; k <= last; ++k) {
-                const int64_t at = (int64_t)(k * 2 + (k == c)) * unit_rows + r;
-                const float2 ml = __ldcg(p.part_ml + at);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + d4);
-                if (ml.x == -INFINITY) continue;  // nothing there for this row
-                const float w = exp2f(ml.x - M);
-                l += w * ml.y;
-                o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+        for (int k = lane; k < parts; k += 32) {
+            const float2 ml = __ldcg(p.part_ml + at(k, r));
+            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);  // (nothing there for this row)
+            if (w != 0.f) l += w * ml.y;
+            if (k < kMergeParts) weight[r][k] = w;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) {
+            top[r] = m;
+            total[r] = bad || l == 0.f ? 0.f : 1.f / l;  // (NaN stays)
+        }
+    }
+    float4 o[kMergeItems];
+#pragma unroll
+    for (int i = 0; i < kMergeItems; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < parts; k0 += kMergeParts) {
+        const int np = min(kMergeParts, parts - k0);
+        __syncthreads();
+        if (k0 > 0) {  // (more pieces than weights are held at once)
+            for (int i = tid; i < n * np; i += kMergeThreads) {
+                const int r = i / np, k = i - r * np;
+                const float m = __ldcg(p.part_ml + at(k0 + k, r)).x;
+                weight[r][k] = m == -INFINITY ? 0.f : exp2f(m - top[r]);
+            }
+            __syncthreads();
+        }
+        for (int k = 0; k < np; ++k) {
+            float4 v[kMergeItems];
+#pragma unroll
+            for (int i = 0; i < kMergeItems; ++i) {
+                const int e = tid + i * kMergeThreads, r = e / (D / 4);
+                if (r < n) v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(k0 + k, r) * D) + e % (D / 4));
+            }
+#pragma unroll
+            for (int i = 0; i < kMergeItems; ++i) {
+                const int r = (tid + i * kMergeThreads) / (D / 4);
+                if (r >= n) continue;
+                const float w = weight[r][k];
+                if (w != 0.f) o[i].x += w * v[i].x, o[i].y += w * v[i].y, o[i].z += w * v[i].z, o[i].w += w * v[i].w;
             }
         }
-        const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays)
-        const int token = (row0 + r) / p.group, h = kvh * p.group + (row0 + r) - token * p.group;
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeItems; ++i) {
+        const int e = tid + i * kMergeThreads, r = e / (D / 4), d4 = e % (D / 4);
+        if (r >= n) continue;
+        const float inv = total[r];
+        const int row = row0 + r0 + r, token = row / p.group, h = kvh * p.group + row - token * p.group;
         uint16_t* dst = static_cast<uint16_t*>(p.out) + ((int64_t)(tok0 + token) * p.num_q_heads + h) * D + 4 * d4;
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(pack2<kBF16>(o.x * inv, o.y * inv), pack2<kBF16>(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2*>(dst) = inv == 0.f ? make_uint2(0, 0)
+                                                    : make_uint2(pack2<kBF16>(o[i].x * inv, o[i].y * inv),
+                                                                 pack2<kBF16>(o[i].z * inv, o[i].w * inv));
     }
 }
 
-cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, int unit_rows, cudaStream_t stream,
-                               int* launches) {
+cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, cudaStream_t stream, int* launches) {
+    constexpr int kTree = kTreeRows / kMergeSlices, kLatent = kLatentRows / kMergeSlices;
     const bool bf16 = dtype == PKV_BF16;
-    auto kern = value_dims == 128 ? (bf16 ? draft_merge_kernel<true, 128> : draft_merge_kernel<false, 128>)
-                                  : (bf16 ? draft_merge_kernel<true, 512> : draft_merge_kernel<false, 512>);
-    const cudaError_t e = launch_pdl(kern, dim3(p.ctas, kMergeSlices), dim3(kMergeThreads), 0, stream, p, unit_rows);
+    auto kern = value_dims == 128 ? (bf16 ? draft_merge_kernel<true, 128, kTree> : draft_merge_kernel<false, 128, kTree>)
+                                  : (bf16 ? draft_merge_kernel<true, 512, kLatent> : draft_merge_kernel<false, 512, kLatent>);
+    const cudaError_t e = launch_pdl(kern, dim3(p.ctas, kMergeSlices), dim3(kMergeThreads), 0, stream, p);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

@@ -67,6 +67,7 @@ __device__ __forceinline__ DraftSeq draft_seq(const DraftParams& p, int s) {
     r.err = 0;
     r.idle = false;
     r.L = 0;
+    const int L = p.context_lens[s];  // (on its way beside the others)
     if (r.tok0 < 0 || tok1 < r.tok0 || tok1 > p.num_tokens) {  // no rows that could be written
         r.n = 0;
         r.err = PKV_DEVERR_QUERY;
@@ -74,7 +75,7 @@ __device__ __forceinline__ DraftSeq draft_seq(const DraftParams& p, int s) {
     }
     r.n = tok1 - r.tok0;
     if (r.n == 0) return r;
-    r.L = p.context_lens[s];
+    r.L = L;
     if (r.n > kMaxDrafted)
         r.err = PKV_DEVERR_QUERY;
     else if (r.L < 0 || r.L > p.len_limit || (r.L > 0 && r.L < r.n))
@@ -237,9 +238,8 @@ __device__ __forceinline__ void draft_schedule(const DraftParams& p, int value_d
     cur.start(p, w0 < w1 ? (int)found[0] : 0, w0 < w1 ? found[1] : 0, w1 - w0);
 }
 
-// The merge of divided units (drafted.cu): value_dims 128 or 512, kRows rows of a unit.
-cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, int unit_rows, cudaStream_t stream,
-                               int* launches);
+// The merge of divided units (drafted.cu): value_dims 128 (tree.cu) or 512 (latent.cu).
+cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, cudaStream_t stream, int* launches);
 // tree.cu
 cudaError_t launch_tree(const DraftParams& p, int dtype, int block_size, const CUtensorMap& tmk, const CUtensorMap& tmv,
                         cudaStream_t stream, int* launches);

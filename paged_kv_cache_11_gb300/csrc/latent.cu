@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCopyWarp) {
         // -------------------------------------------------------------- copies
         const uint64_t policy = l2_policy_evict_first();
+        const uint32_t el = issuing_lane();
         int c = 0;  // tiles
         while (ok && cur.next(p, it)) {
             const int32_t* table = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
@@ -163,24 +164,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (wrong) id = 0;  // keep the shape; the unit's rows become zeros
                 const bool any = __any_sync(0xffffffffu, wrong);
                 if (any && lane == 0) record_error(p.err, PKV_DEVERR_BLOCK_ID);
-                const int b = c & 1;
-                for (int i = 0; i < kSlots && ok; ++i) {
-                    const int slot = b * kSlots + i;
-                    if (lane == i) {
-                        if (c >= 2) ok = mbar_wait(empty0 + 8 * slot, (c / 2 - 1) & 1);
-                        if (ok) {
-                            if (i == 0) bad[b] = any;
-                            const uint32_t bar = full0 + 8 * slot;
-                            if (there) {
-                                mbar_arrive_expect_tx(bar, kSlot);
-                                const int group = id * (BS / 8) + (j * kSlotKeys % BS) / 8;
-                                tma_load_4d(sbase + S::kKV + slot * kSlot, &tmc, bar, 0, 0, 0, group, policy);
-                            } else {
-                                mbar_arrive(bar);  // behind the context: whatever lies there is masked
-                            }
+                const uint32_t b = c & 1;
+                if (c >= 2) ok = mbar_wait_warp(empty0 + 8 * b * kSlots, (c / 2 - 1) & 1);
+                if (el && ok) bad[b] = any;
+#pragma unroll
+                for (int i = 0; i < kSlots; ++i) {
+                    const uint32_t slot = b * kSlots + i, bar = full0 + 8 * slot;
+                    if (c >= 2 && i > 0) ok = ok && mbar_wait_warp(empty0 + 8 * slot, (c / 2 - 1) & 1);
+                    if (!ok) break;
+                    const int jj = t * kSlots + i;
+                    const int group = __shfl_sync(0xffffffffu, id, i) * (BS / 8) + (jj * kSlotKeys % BS) / 8;
+                    if (jj < units) {
+                        if (el) {
+                            mbar_arrive_expect_tx(bar, kSlot);
+                            tma_load_4d(sbase + S::kKV + slot * kSlot, &tmc, bar, 0, 0, 0, group, policy);
                         }
+                    } else if (el) {
+                        mbar_arrive(bar);  // behind the context: whatever lies there is masked
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, i);
                 }
             }
         }
@@ -257,10 +258,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t kd = k_desc + b * kTileStep;
+#pragma unroll 3
+                for (int i = 0; i < kParts; ++i)
 #pragma unroll
-                for (int ks = 0; ks < kRow / 16; ++ks)
-                    umma_f16_ss(el, tm + 256 + 64 * b, q_desc + (ks >> 2) * (kLatentRows * 128 / 16) + (ks & 3) * 2,
-                                kd + (ks >> 2) * 64 + (ks & 3) * 2, id_s, ks > 0);
+                    for (int ks = 0; ks < 4; ++ks)
+                        umma_f16_ss(el, tm + 256 + 64 * b, q_desc + i * (kLatentRows * 128 / 16) + ks * 2,
+                                    kd + i * 64 + ks * 2, id_s, i > 0 || ks > 0);
                 --left;
                 if (left == 0) umma_commit(el, qempty);
                 umma_commit(el, sfull0 + 8 * b);
@@ -337,21 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint4* v = reinterpret_cast<uint4*>(smem + S::kKV + b * kSlots * kSlot + (key >> 3) * kGroup +
                                                             (key & 7) * 128 + (tid & 1) * 4096);
                         uint32_t any = 0;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            uint4* at = v + (i >> 3) * 64 + (i & 7);
-                            uint4 w = make_uint4(0, 0, 0, 0);
-                            if (pos < it.q.L) {
-                                w = *at;
-                                const uint32_t gone = not_finite2<kBF16>(w.x) | not_finite2<kBF16>(w.y) |
-                                                      not_finite2<kBF16>(w.z) | not_finite2<kBF16>(w.w);
-                                any |= gone;
-                                if (!gone) continue;
-                                w.x = finite_or_zero2<kBF16>(w.x), w.y = finite_or_zero2<kBF16>(w.y);
-                                w.z = finite_or_zero2<kBF16>(w.z), w.w = finite_or_zero2<kBF16>(w.w);
-                            }
-                            *at = w;
-                        }
+#pragma unroll 2
+                        for (int i = 0; i < 32; ++i) any |= scrub8<kBF16>(v + (i >> 3) * 64 + (i & 7), pos < it.q.L);
                         if (any) atomicOr(lost + k % 3, 1ull << (pos - base));
                     }
                 }
@@ -401,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (rescale) {
                     tc_fence_after();
                     const float4* al = reinterpret_cast<const float4*>(alpha + b * kLatentRows);
+#pragma unroll 1
                     for (int q = 0; q < 8; ++q) {  // 32 query rows of 128 values
                         float o[32];
                         tmem_ld32(lane_addr + 32 * q, o);
@@ -457,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             softmax_sync();
             tc_fence_after();
             const unsigned long long gone = lost[k % 3];
+#pragma unroll 1
             for (int q = 0; q < 8; ++q) {  // 32 query rows of this lane's value d
                 const int r0 = 32 * (q & 1), d = 128 * (q >> 1) + 32 * warp + lane;
                 if (r0 >= it.rows) continue;
@@ -466,23 +458,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0.f;
-                }
-                if (gone) {
-                    // values that are not finite and were left out of the products, for the rows that attend them
-                    for (unsigned long long at = gone; at; at &= at - 1) {
-                        const int bit = __ffsll(at) - 1, pos = base + bit;
-                        const int id = p.block_tables[(int64_t)it.s * p.max_blocks_per_seq + pos / BS];
-                        if (id < 0 || id >= p.num_blocks) continue;
-                        const uint16_t v =
-                            static_cast<const uint16_t*>(p.values)[((int64_t)id * BS + pos % BS) * kRow + d];
-                        if (!not_finite2<kBF16>(v)) continue;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int r = r0 + i;
-                            if (r < it.rows && draft_mask(p, it.q, (it.row0 + r) / p.group) >> bit & 1)
-                                o[i] += widen16<kBF16>(v);
-                        }
-                    }
                 }
                 if (part) {
                     float* dst = p.part_o + ((int64_t)slot * kLatentRows + r0) * kValue + d;
@@ -502,6 +477,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t w = lane & 1 ? pack2<kBF16>(other, y) : pack2<kBF16>(x, other);
                     if (r0 + 2 * i + (lane & 1) < it.rows)
                         *reinterpret_cast<uint32_t*>(dst + (int64_t)2 * i * kValue) = w;
+                }
+            }
+            if (gone && !zero) {
+                // values that are not finite and were left out of the products, for the rows that attend them: a thread
+                // takes four values of every row
+                softmax_sync();
+#pragma unroll 1
+                for (unsigned long long at = gone; at; at &= at - 1) {
+                    const int bit = __ffsll(at) - 1, pos = base + bit;
+                    const int id = p.block_tables[(int64_t)it.s * p.max_blocks_per_seq + pos / BS];
+#pragma unroll 1
+                    for (int r = 0; r < it.rows; ++r)
+                        if (draft_mask(p, it.q, (it.row0 + r) / p.group) >> bit & 1)
+                            add_not_finite<kBF16>(
+                                part ? p.part_o + ((int64_t)slot * kLatentRows + r) * kValue + 4 * tid : nullptr,
+                                static_cast<uint16_t*>(p.out) +
+                                    ((int64_t)it.q.tok0 * p.num_q_heads + it.row0 + r) * kValue + 4 * tid,
+                                static_cast<const uint16_t*>(p.values) + ((int64_t)id * BS + pos % BS) * kRow + 4 * tid, 4);
                 }
             }
             tc_fence_before();
@@ -533,7 +526,7 @@ cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size
     if (e != cudaSuccess) return e;
     ++*launches;
     // a unit of one tile is never divided
-    return p.len_limit > kTile ? launch_draft_merge(p, dtype, kValue, kLatentRows, stream, launches) : cudaSuccess;
+    return p.len_limit > kTile ? launch_draft_merge(p, dtype, kValue, stream, launches) : cudaSuccess;
 }
 
 }  // namespace pkv

@@ -239,26 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // this thread's key: its values past the prompt become zeros, and those not finite are taken out;
                     // where both streams use the tile each sees to half of it
                     const int key = shared ? 64 * X + (r >> 1) : r, pos = t * kTile + key;
+                    const int h0 = shared ? r & 1 : 0;
                     uint32_t any = 0;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (shared && h != (r & 1)) continue;
-                        uint4* v = reinterpret_cast<uint4*>(smem + S::kKV + ((u + h) % kRing) * kUnit + key * 128);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            uint4 w = make_uint4(0, 0, 0, 0);
-                            if (pos < nk) {
-                                w = v[i];
-                                const uint32_t gone = not_finite2<kBF16>(w.x) | not_finite2<kBF16>(w.y) |
-                                                      not_finite2<kBF16>(w.z) | not_finite2<kBF16>(w.w);
-                                any |= gone;
-                                if (!gone) continue;
-                                w.x = finite_or_zero2<kBF16>(w.x), w.y = finite_or_zero2<kBF16>(w.y);
-                                w.z = finite_or_zero2<kBF16>(w.z), w.w = finite_or_zero2<kBF16>(w.w);
-                            }
-                            v[i] = w;
-                        }
-                    }
+#pragma unroll 2
+                    for (int i = 0; i < (shared ? 8 : 16); ++i)
+                        any |= scrub8<kBF16>(reinterpret_cast<uint4*>(smem + S::kKV + ((u + h0 + (i >> 3)) % kRing) * kUnit +
+                                                                     key * 128) + (i & 7),
+                                             pos < nk);
                     if (any) atomicOr(lost + (pos - masked * kTile) / 32, 1u << (pos & 31));
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -277,10 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         both_streams();  // (what was taken out is known)
         if (mine > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(odone0 + 8 * X, (mine - 1) & 1));
         tc_fence_after();
-        uint32_t any = 0;
-        for (int i = 0; i < kLostTiles * 4; ++i) any |= lost[i];
         const float inv = ok && l != 0.f ? 1.f / l : 0.f;
         uint16_t* dst = out + ((int64_t)(a0 + q0 + row) * p.num_heads + head) * 128;
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             float o[32];
 #pragma unroll
@@ -290,18 +276,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait32(o);
             }
             if (row >= rows) continue;
-            if (any) {
-                for (int w = 0; w < kLostTiles * 4; ++w)
-                    for (uint32_t at = lost[w]; at; at &= at - 1) {
-                        const int pos = masked * kTile + 32 * w + __ffs(at) - 1;
-                        if (pos >= seen) continue;
-                        const uint16_t* v = static_cast<const uint16_t*>(p.values) + (b0 + pos) * p.kv_stride +
-                                            head * p.kv_head_stride + 128 + 32 * c;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (not_finite2<kBF16>(v[i])) o[i] += widen16<kBF16>(v[i]);
-                    }
-            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t w[4];
@@ -310,6 +284,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w[e] = inv != 0.f ? pack2<kBF16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv) : 0u;
                 *reinterpret_cast<uint4*>(dst + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
             }
+        }
+        if (row < rows && ok) {
+            // values that are not finite and were left out of the products
+#pragma unroll 1
+            for (int w = 0; w < kLostTiles * 4; ++w)
+                for (uint32_t at = lost[w]; at; at &= at - 1) {
+                    const int pos = masked * kTile + 32 * w + __ffs(at) - 1;
+                    if (pos < seen)
+                        add_not_finite<kBF16>(nullptr, dst,
+                                              static_cast<const uint16_t*>(p.values) + (b0 + pos) * p.kv_stride +
+                                                  head * p.kv_head_stride + 128,
+                                              128);
+                }
         }
         if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
     }

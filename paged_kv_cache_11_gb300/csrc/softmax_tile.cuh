@@ -21,12 +21,45 @@ __device__ __forceinline__ uint32_t finite_or_zero2(uint32_t w) {
     return w & ~((bad & 1u ? 0xffffu : 0u) | (bad & 2u ? 0xffff0000u : 0u));
 }
 
+// Eight 16-bit values of a token in shared memory: zeros for a token that is not there, else with those that are not finite
+// put to zero; whether there were any.
+template <bool kBF16>
+__device__ __forceinline__ uint32_t scrub8(uint4* v, bool there) {
+    if (!there) {
+        *v = make_uint4(0, 0, 0, 0);
+        return 0;
+    }
+    uint4 w = *v;
+    const uint32_t bad =
+        not_finite2<kBF16>(w.x) | not_finite2<kBF16>(w.y) | not_finite2<kBF16>(w.z) | not_finite2<kBF16>(w.w);
+    if (bad) {
+        w.x = finite_or_zero2<kBF16>(w.x), w.y = finite_or_zero2<kBF16>(w.y);
+        w.z = finite_or_zero2<kBF16>(w.z), w.w = finite_or_zero2<kBF16>(w.w);
+        *v = w;
+    }
+    return bad;
+}
+
 template <bool kBF16>
 __device__ __forceinline__ float widen16(uint16_t h) {
     if constexpr (kBF16)
         return __uint_as_float((uint32_t)h << 16);
     else
         return __half2float(__ushort_as_half(h));
+}
+
+// Adds to `n` sums (fp32 partials, or outputs of the 16-bit type) the values at v that are not finite.
+template <bool kBF16>
+__device__ __noinline__ void add_not_finite(float* part, uint16_t* out, const uint16_t* v, int n) {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        if (!not_finite2<kBF16>(v[i])) continue;
+        const float x = widen16<kBF16>(v[i]);
+        if (part)
+            part[i] += x;
+        else
+            out[i] = (uint16_t)pack2<kBF16>(widen16<kBF16>(out[i]) + x, 0.f);
+    }
 }
 
 // 2^x (results below fp32's normal range become zero).

@@ -295,24 +295,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint4* v = reinterpret_cast<uint4*>(smem + S::kKV + (vk % kRing) * kBuf + (tk >> 3) * 2048 +
                                                             (tk & 7) * 128 + (two ? (r & 1) * 1024 : 0));
                         uint32_t any = 0;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (two && h) break;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                uint4 w = make_uint4(0, 0, 0, 0);
-                                if (pos < it.q.L) {
-                                    w = v[h * 64 + i];
-                                    const uint32_t lost2 = not_finite2<kBF16>(w.x) | not_finite2<kBF16>(w.y) |
-                                                           not_finite2<kBF16>(w.z) | not_finite2<kBF16>(w.w);
-                                    any |= lost2;
-                                    if (!lost2) continue;
-                                    w.x = finite_or_zero2<kBF16>(w.x), w.y = finite_or_zero2<kBF16>(w.y);
-                                    w.z = finite_or_zero2<kBF16>(w.z), w.w = finite_or_zero2<kBF16>(w.w);
-                                }
-                                v[h * 64 + i] = w;
-                            }
-                        }
+#pragma unroll 2
+                        for (int i = 0; i < (two ? 8 : 16); ++i)
+                            any |= scrub8<kBF16>(v + (i >> 3) * 64 + (i & 7), pos < it.q.L);
                         if (any) atomicOr(lost + k % 3, 1ull << (pos - base));
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -366,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // this thread's dims: all of its row, or with both streams on one row the stream's half
             const int c0 = two ? 0 : 2 * X, c1 = two ? 4 : 2 * X + 2;
             const int head = done.kvh * p.group + done.row0 + row - token * p.group;
+#pragma unroll 1
             for (int c = c0; c < c1; ++c) {
                 float o[32];
 #pragma unroll
@@ -387,21 +373,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0.f;
                 }
-                if (unsigned long long at = gone & mask) {
-                    // values that are not finite and were left out of the products (tokens that this item walked)
-                    do {
-                        const int pos = base + __ffsll(at) - 1;
-                        at &= at - 1;
-                        if (pos / kTile < done.t0 || pos / kTile >= done.t1) continue;
-                        const int id = p.block_tables[(int64_t)done.s * p.max_blocks_per_seq + pos / BS];
-                        if (id < 0 || id >= p.num_blocks) continue;
-                        const uint16_t* v = static_cast<const uint16_t*>(p.values) +
-                                            (((int64_t)id * p.num_kv_heads + done.kvh) * BS + pos % BS) * D + 32 * c;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (not_finite2<kBF16>(v[i])) o[i] += widen16<kBF16>(v[i]);
-                    } while (at);
-                }
                 if (part) {
                     float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
 #pragma unroll
@@ -419,6 +390,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w[e] = zero ? 0u : pack2<kBF16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
                         dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                }
+            }
+            if (row < done.rows && !zero) {
+                // values that are not finite and were left out of the products, of the tokens that this item walked
+                for (unsigned long long at = gone & mask; at; at &= at - 1) {
+                    const int pos = base + __ffsll(at) - 1;
+                    if (pos / kTile < done.t0 || pos / kTile >= done.t1) continue;
+                    const int id = p.block_tables[(int64_t)done.s * p.max_blocks_per_seq + pos / BS];
+                    add_not_finite<kBF16>(part ? p.part_o + prow * D + 32 * c0 : nullptr,
+                                          static_cast<uint16_t*>(p.out) +
+                                              ((int64_t)(done.q.tok0 + token) * p.num_q_heads + head) * D + 32 * c0,
+                                          static_cast<const uint16_t*>(p.values) +
+                                              (((int64_t)id * p.num_kv_heads + done.kvh) * BS + pos % BS) * D + 32 * c0,
+                                          32 * (c1 - c0));
                 }
             }
             if (part && row < done.rows && (two || X == 0)) {
@@ -461,7 +446,7 @@ cudaError_t launch_tree(const DraftParams& p, int dtype, int block_size, const C
     if (e != cudaSuccess) return e;
     ++*launches;
     // a unit of one tile is never divided
-    return p.len_limit > kTile ? launch_draft_merge(p, dtype, kHeadDim, kTreeRows, stream, launches) : cudaSuccess;
+    return p.len_limit > kTile ? launch_draft_merge(p, dtype, kHeadDim, stream, launches) : cudaSuccess;
 }
 
 }  // namespace pkv
