@@ -24,28 +24,43 @@ __global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftP
     __shared__ int last_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
     if (tid == 0) last_s = p.ctas - 1;
+    __syncthreads();
     pdl_wait();
     const int4 d = __ldcg(p.part_desc + (c * 2 + 1) * 2);
-    const int state = d.x, tok0 = d.y, row0 = d.z, rows = d.w;
-    if (!(state & kPartValid) || (state & kPartEnds)) return;  // no unit begins here and ends elsewhere
     const int kvh = __ldcg(p.part_desc + (c * 2 + 1) * 2 + 1).x;
-    const int r0 = blockIdx.y * kRows, n = min(kRows, rows - r0);
-    if (n <= 0) return;
-    __syncthreads();
+    const int state = d.x, tok0 = d.y, row0 = d.z, rows = d.w;
     // the CTA that holds the unit's last tile: the first behind this one that ends a unit which it did not begin
     for (int k = c + 1 + tid; k < p.ctas; k += kMergeThreads)
         if (__ldcg(p.part_desc + k * 4).x & kPartEnds) {
             atomicMin(&last_s, k);
             break;
         }
+    if (!(state & kPartValid) || (state & kPartEnds)) return;  // no unit begins here and ends elsewhere
+    const int r0 = blockIdx.y * kRows, n = min(kRows, rows - r0);
+    if (n <= 0) return;
     __syncthreads();
     const int parts = last_s - c + 1;
     const auto at = [&](int k, int r) { return (int64_t)((c + k) * 2 + (k == 0)) * kUnitRows + r0 + r; };
+    // the first two pieces (there are two at least) are on their way beside their weights
+    float4 early[2][kMergeItems];
+    const auto fetch = [&](int k, float4 (&v)[kMergeItems]) {
+#pragma unroll
+        for (int i = 0; i < kMergeItems; ++i) {
+            const int e = tid + i * kMergeThreads, r = e / (D / 4);
+            v[i] = r < n ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at(k, r) * D) + e % (D / 4))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    fetch(0, early[0]);
+    fetch(1, early[1]);
     // each row's largest maximum and its weight in all, a warp to a row
+#pragma unroll 2
     for (int r = warp; r < n; r += kMergeThreads / 32) {
-        float m = -INFINITY;
-        bool bad = false;
-        for (int k = lane; k < parts; k += 32) {
+        const float2 none = make_float2(-INFINITY, 0.f);
+        const float2 mine = lane < parts ? __ldcg(p.part_ml + at(lane, r)) : none;  // (the rest, if any, is read twice)
+        float m = mine.x;
+        bool bad = mine.y < 0.f;
+        for (int k = lane + 32; k < parts; k += 32) {
             const float2 ml = __ldcg(p.part_ml + at(k, r));
             m = fmaxf(m, ml.x);
             bad |= ml.y < 0.f;
@@ -54,7 +69,7 @@ __global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftP
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         float l = 0.f;
         for (int k = lane; k < parts; k += 32) {
-            const float2 ml = __ldcg(p.part_ml + at(k, r));
+            const float2 ml = k < 32 ? mine : __ldcg(p.part_ml + at(k, r));
             const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);  // (nothing there for this row)
             if (w != 0.f) l += w * ml.y;
             if (k < kMergeParts) weight[r][k] = w;
@@ -83,10 +98,11 @@ __global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftP
         }
         for (int k = 0; k < np; ++k) {
             float4 v[kMergeItems];
+            if (k0 + k < 2) {
 #pragma unroll
-            for (int i = 0; i < kMergeItems; ++i) {
-                const int e = tid + i * kMergeThreads, r = e / (D / 4);
-                if (r < n) v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(k0 + k, r) * D) + e % (D / 4));
+                for (int i = 0; i < kMergeItems; ++i) v[i] = k == 0 ? early[0][i] : early[1][i];
+            } else {
+                fetch(k0 + k, v);
             }
 #pragma unroll
             for (int i = 0; i < kMergeItems; ++i) {

@@ -189,13 +189,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every copy has landed before the CTA ends
         if (lane == 0)
             for (int i = max(0, c - 2); i < c; ++i)
-                for (int k = 0; k < kSlots; ++k) mbar_wait(full0 + 8 * ((i & 1) * kSlots + k), (i / 2) & 1);
+                for (int k = 0; k < kSlots; ++k) wait_bar(full0 + 8 * ((i & 1) * kSlots + k), (i / 2) & 1);
     } else if (warp == kQueryWarp) {
         // ------------------------------------------------------------- queries
         if (lane == 0) {
             int k = 0;
             while (ok && cur.next(p, it)) {
-                if (k > 0) ok = mbar_wait(qempty, (k - 1) & 1);
+                if (k > 0) ok = wait_bar(qempty, (k - 1) & 1);
                 if (!ok) break;
                 mbar_arrive_expect_tx(qfull, kParts * kLatentRows * 128);
                 const int row = it.q.tok0 * p.num_q_heads + it.row0;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++k;
             }
             if (!ok) record_error(p.err, PKV_DEVERR_TIMEOUT);
-            if (k > 0) mbar_wait(qfull, (k - 1) & 1);
+            if (k > 0) wait_bar(qfull, (k - 1) & 1);
         }
     } else if (warp == kProductWarp) {
         // ------------------------------------------------------------ products
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
         // every product that was issued has ended before tensor memory is given back
-        if (last_bar) mbar_wait(last_bar, last_par);
+        if (last_bar) wait_bar(last_bar, last_par);
     } else {
         // ------------------------------------------------------------- softmax
         const int ra = 16 * warp + (lane >> 2), rb = ra + 8;  // this thread's rows
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = it.t0; t < it.t1; ++t, ++c) {
                 const int b = c & 1;
                 const bool guard = (t + 1) * kTile > base;
-                ok = ok && mbar_wait(sfull0 + 8 * b, (c / 2) & 1) && mbar_wait(full0 + 8 * b * kSlots, (c / 2) & 1);
+                ok = ok && wait_bar(sfull0 + 8 * b, (c / 2) & 1) && wait_bar(full0 + 8 * b * kSlots, (c / 2) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 float s[32];
 #pragma unroll
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     lb += b0 + b1;
                 }
                 // the product before has read P and is in O
-                if (c > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(odone, (c - 1) & 1));
+                if (c > 0) ok = __all_sync(0xffffffffu, ok && wait_bar(odone, (c - 1) & 1));
                 if (!ok) continue;
                 if (rescale) {
                     tc_fence_after();
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(pfull);
             }
             // ---- the unit's end
-            if (c > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(odone, (c - 1) & 1));
+            if (c > 0) ok = __all_sync(0xffffffffu, ok && wait_bar(odone, (c - 1) & 1));
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
                 la += __shfl_xor_sync(0xffffffffu, la, o);

@@ -11,9 +11,10 @@
 // streams use each tile of keys and values before it is given back.
 //
 // Shared memory is Q (2 x 48 KiB) and a ring of eight 16 KiB units of 128
-// tokens x 64 values: a tile of keys is three units, a tile of values two.  A
-// unit's copy waits for that unit alone, so the ring holds a tile of values and
-// two of keys in any order.
+// tokens x 64 values: a tile of keys is three units, a tile of values two, in
+// turn.  Eight units back from those of keys t lie values t - 2, and from those
+// of values t keys t - 1: that is all that a copy waits for, and a tile of
+// either kind has one barrier.
 //
 // CTAs of one head follow one another, the longest rows first.
 #include "softmax_tile.cuh"
@@ -36,8 +37,8 @@ struct PromptSmem {
     static constexpr int kQ = 0;  // [2 streams][3 parts][128 rows][128 B]
     static constexpr int kKV = kQ + 2 * kKeyUnits * kUnit;
     static constexpr int kBar = kKV + kRing * kUnit;
-    // full[kRing], empty[kRing], qfull[2], sfull[2], pfull[2], odone[2]
-    static constexpr int kNumBars = 2 * kRing + 8;
+    // keys landed[2], values landed[2], keys read[2], values read[2] (by the tile's parity), qfull[2], sfull[2], pfull[2], odone[2]
+    static constexpr int kNumBars = 16;
     static constexpr int kAddr = kBar + kNumBars * 8;  // tensor memory address
     static constexpr int kLost = kAddr + 8;            // [12] keys whose values were taken out, from the first masked tile on
     static constexpr int kTotal = kLost + kLostTiles * 4 * 4;
@@ -59,8 +60,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_addr(smem);
-    const uint32_t full0 = sbase + S::kBar, empty0 = full0 + 8 * kRing, qfull0 = empty0 + 8 * kRing, sfull0 = qfull0 + 16,
-                   pfull0 = sfull0 + 16, odone0 = pfull0 + 16;
+    const uint32_t kfull0 = sbase + S::kBar, vfull0 = kfull0 + 16, kread0 = vfull0 + 16, vread0 = kread0 + 16,
+                   qfull0 = vread0 + 16, sfull0 = qfull0 + 16, pfull0 = sfull0 + 16, odone0 = pfull0 + 16;
     uint32_t* lost = reinterpret_cast<uint32_t*>(smem + S::kLost);
     const int head = blockIdx.y, seq = blockIdx.z;
     const int q0 = (int)(gridDim.x - 1 - blockIdx.x) * kRows;  // first query of the CTA in its prompt
@@ -92,11 +93,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int masked = max(0, seen0) / kTile;  // tiles before it hold no key that any row masks
 
     if (tid == 0) {
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(full0 + 8 * i, 1);
-            mbar_init(empty0 + 8 * i, 1);
-        }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(kfull0 + 8 * i, 1);
+            mbar_init(vfull0 + 8 * i, 1);
+            mbar_init(kread0 + 8 * i, 1);
+            mbar_init(vread0 + 8 * i, 1);
             mbar_init(qfull0 + 8 * i, 1);
             mbar_init(sfull0 + 8 * i, 1);
             mbar_init(pfull0 + 8 * i, kStreamWarps);
@@ -125,26 +126,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 a0 + q0 + 128 * x);
             };
             queries(0);
-            int u = 0;  // units so far
-            for (int t = 0; t < tiles && ok; ++t) {
-                for (int i = 0; i < kTileUnits && ok; ++i, ++u) {
-                    const int b = u % kRing;
-                    if (u >= kRing) ok = mbar_wait(empty0 + 8 * b, (u / kRing - 1) & 1);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(full0 + 8 * b, kUnit);
-                    const uint32_t dst = sbase + S::kKV + b * kUnit;
-                    if (i == 2)
-                        tma_load_2d(dst, &tmr, full0 + 8 * b, 0, b0 + t * kTile);
+            int t = 0;
+            for (; t < tiles; ++t) {
+                const int par = t & 1, y = b0 + t * kTile;
+                if (t >= 2) ok = wait_bar(vread0 + 8 * par, (t / 2 - 1) & 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(kfull0 + 8 * par, kKeyUnits * kUnit);
+                for (int i = 0; i < kKeyUnits; ++i) {
+                    const uint32_t dst = sbase + S::kKV + (t * kTileUnits + i) % kRing * kUnit;
+                    if (i < 2)
+                        tma_load_3d(dst, &tmkv, kfull0 + 8 * par, 64 * i, head, y);
                     else
-                        tma_load_3d(dst, &tmkv, full0 + 8 * b, 64 * (i < 2 ? i : i - 1), head, b0 + t * kTile);
-                    if (u == 2 && tiles_b > 0) queries(1);
+                        tma_load_2d(dst, &tmr, kfull0 + 8 * par, 0, y);
                 }
+                if (t == 0 && tiles_b > 0) queries(1);
+                if (t >= 1) ok = wait_bar(kread0 + 8 * (par ^ 1), ((t - 1) / 2) & 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(vfull0 + 8 * par, 2 * kUnit);
+                for (int i = 0; i < 2; ++i)
+                    tma_load_3d(sbase + S::kKV + (t * kTileUnits + kKeyUnits + i) % kRing * kUnit, &tmkv, vfull0 + 8 * par,
+                                128 + 64 * i, head, y);
             }
             if (!ok) record_error(p.err, PKV_DEVERR_TIMEOUT);
             // every copy has landed before the CTA ends
-            mbar_wait(qfull0, 0);
-            if (tiles_b > 0 && u > 2) mbar_wait(qfull0 + 8, 0);
-            for (int i = max(0, u - kRing); i < u; ++i) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
+            wait_bar(qfull0, 0);
+            if (tiles_b > 0) wait_bar(qfull0 + 8, 0);
+            for (int i = max(0, t - 2); i < min(tiles, t + 1); ++i) {  // (of a tile that was broken off keys alone)
+                wait_bar(kfull0 + 8 * (i & 1), (i / 2) & 1);
+                if (i < t) wait_bar(vfull0 + 8 * (i & 1), (i / 2) & 1);
+            }
         }
     } else if (warp == kProductWarp) {
         // ------------------------------------------------------------ products
@@ -156,14 +166,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                        v_desc = umma_desc_sw128(sb + S::kKV, kUnit, 1024);  // + (bytes / 16)
         int pend_x = -1, pend_t = 0;  // a tile whose second product is still to come
         uint32_t last_bar = 0, last_par = 0;
-        const auto landed = [&](uint32_t u) { return mbar_wait_warp(full0 + 8 * (u % kRing), (u / kRing) & 1); };
         const auto values = [&]() {
-            const uint32_t x = pend_x, t = pend_t, u = t * kTileUnits + kKeyUnits;
+            const uint32_t x = pend_x, t = pend_t, at = (t * kTileUnits + kKeyUnits) % kRing;
             pend_x = -1;
-            ok = mbar_wait_warp(pfull0 + 8 * x, t & 1) && landed(u) && landed(u + 1);
+            ok = mbar_wait_warp(vfull0 + 8 * (t & 1), (t / 2) & 1) && mbar_wait_warp(pfull0 + 8 * x, t & 1);
             if (!ok) return;
             tc_fence_after();
-            const uint32_t o = tm + 256 + 128 * x, pp = tm + 128 * x, at = u % kRing;
+            const uint32_t o = tm + 256 + 128 * x, pp = tm + 128 * x;
             if (at + 1 < kRing) {
                 const uint64_t vd = v_desc + at * (kUnit / 16);
 #pragma unroll
@@ -176,13 +185,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_f16_ts(el, o + 64, pp + 8 * ks, v1 + ks * 128, id_h, t > 0 || ks > 0);
                 }
             }
-            if (x == 1 || t >= (uint32_t)tb) {  // the last to read it
-                umma_commit(el, empty0 + 8 * at);
-                umma_commit(el, empty0 + 8 * ((u + 1) % kRing));
+            if (x == 1 || t >= (uint32_t)tb) umma_commit(el, vread0 + 8 * (t & 1));  // the last to read it
+            if (t + 1 == (uint32_t)(x ? tb : ta)) {
+                umma_commit(el, odone0 + 8 * x);
+                last_bar = odone0 + 8 * x;
+                last_par = 0;
             }
-            umma_commit(el, odone0 + 8 * x);
-            last_bar = odone0 + 8 * x;
-            last_par = t & 1;
         };
         for (int t = 0; t < tn && ok; ++t) {
 #pragma unroll
@@ -190,20 +198,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t >= (x ? tb : ta) || !ok) continue;
                 if (pend_x == x) values();  // P of this stream lies where S goes
                 if (ok && t == 0) ok = mbar_wait_warp(qfull0 + 8 * x, 0);
-                const uint32_t u = t * kTileUnits;
+                ok = ok && mbar_wait_warp(kfull0 + 8 * (t & 1), (t / 2) & 1);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
                 for (int i = 0; i < kKeyUnits; ++i) {
-                    ok = ok && landed(u + i);
-                    if (!ok) break;
-                    if (i == 0) tc_fence_after();
-                    const uint32_t at = (u + i) % kRing;
-                    const uint64_t qd = q_desc + (x * kKeyUnits + i) * (kUnit / 16), kd = k_desc + at * (kUnit / 16);
+                    const uint64_t qd = q_desc + (x * kKeyUnits + i) * (kUnit / 16),
+                                   kd = k_desc + (uint32_t)(t * kTileUnits + i) % kRing * (kUnit / 16);
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         umma_f16_ss(el, tm + 128 * x, qd + 2 * ks, kd + 2 * ks, id_s, i > 0 || ks > 0);
-                    if (x == 1 || t >= tb) umma_commit(el, empty0 + 8 * at);
                 }
-                if (!ok) break;
+                if (x == 1 || t >= tb) umma_commit(el, kread0 + 8 * (t & 1));  // the last to read it
                 umma_commit(el, sfull0 + 8 * x);
                 last_bar = sfull0 + 8 * x;
                 last_par = t & 1;
@@ -215,25 +221,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && pend_x >= 0) values();
         if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
         // every product that was issued has ended before tensor memory is given back
-        if (last_bar) mbar_wait(last_bar, last_par);
+        if (last_bar) wait_bar(last_bar, last_par);
     } else {
         // ------------------------------------------------------------- softmax
         const int X = warp >> 2, r = tid & 127, row = 128 * X + r;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t s_addr = lane_addr + 128 * X, o_addr = lane_addr + 256 + 128 * X;
         const int mine = X ? tiles_b : tiles_a;
+        const int mine_masked = max(0, seen0 + 128 * X) / kTile;  // tiles before it: no row of the stream masks a key
         const int seen = min(nk, seen0 + row);  // keys that this row attends (rows past the prompt's end: whatever)
         const bool live = 128 * X + 32 * (warp & 3) < rows;
-        float m_run = -INFINITY, l = 0.f;
+        // (a lane without a row, whose scores are anything, never asks for a raise)
+        float m_run = row < rows ? -INFINITY : INFINITY, l = 0.f;
         for (int t = 0; t < mine; ++t) {
             const bool shared = t < tiles_a && t < tiles_b;
             const bool guard = t >= masked;
-            ok = ok && mbar_wait(sfull0 + 8 * X, t & 1);
+            ok = ok && wait_bar(sfull0 + 8 * X, t & 1);
             ok = __all_sync(0xffffffffu, ok);
+            if (live && ok) {
+                tc_fence_after();
+                softmax_tile<kBF16>(s_addr, o_addr, t >= mine_masked, p.scale_log2, t > 0, m_run, l,
+                                    [&](int c) { return before(t * kTile + c, seen); });
+                tc_fence_before();
+            }
             if (guard) {
                 const int u = t * kTileUnits + kKeyUnits;
-                ok = ok && mbar_wait(full0 + 8 * (u % kRing), (u / kRing) & 1) &&
-                     mbar_wait(full0 + 8 * ((u + 1) % kRing), ((u + 1) / kRing) & 1);
+                ok = ok && wait_bar(vfull0 + 8 * (t & 1), (t / 2) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) {
                     // this thread's key: its values past the prompt become zeros, and those not finite are taken out;
@@ -252,17 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (shared) both_streams();
             }
             if (!ok) continue;
-            if (live) {
-                tc_fence_after();
-                softmax_tile<kBF16>(s_addr, o_addr, guard || !(p.scale_log2 > 0.f), p.scale_log2, t > 0, m_run, l,
-                                    [&](int c) { return before(t * kTile + c, seen); });
-                tc_fence_before();
-            }
             __syncwarp();
             if (lane == 0) mbar_arrive(pfull0 + 8 * X);
         }
         both_streams();  // (what was taken out is known)
-        if (mine > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(odone0 + 8 * X, (mine - 1) & 1));
+        if (mine > 0) ok = __all_sync(0xffffffffu, ok && wait_bar(odone0 + 8 * X, 0));
         tc_fence_after();
         const float inv = ok && l != 0.f ? 1.f / l : 0.f;
         uint16_t* dst = out + ((int64_t)(a0 + q0 + row) * p.num_heads + head) * 128;

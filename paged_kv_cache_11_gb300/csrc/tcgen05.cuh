@@ -79,9 +79,15 @@ __device__ __forceinline__ bool mbar_test_warp(uint32_t bar, uint32_t parity) {
         : "memory");
     return __all_sync(0xffffffffu, done != 0);
 }
+// mbar_wait for kernels of several roles, whose warps wait for instructions when their loops are long: the way of a wait that
+// does not end at once is kept out of them.
+static __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity); }
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || mbar_wait_on(bar, parity);
+}
 // A warp's bounded wait: the same answer in all lanes.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    return __all_sync(0xffffffffu, wait_bar(bar, parity));
 }
 
 // Arrive once on `bar` when every tcgen05.mma this thread issued so far has completed.

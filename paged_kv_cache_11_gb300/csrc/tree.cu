@@ -29,7 +29,8 @@
 //
 // Warps: 0-3 and 4-7 the streams' softmax, 8 the copies (one TMA copy for each
 // block of K or V, as 8-token groups of 2 KiB, into a ring of five 32 KiB
-// buffers that runs on across units), 9 the products.
+// buffers that runs on across units), 9 the products, 10 and 11 the streams'
+// queries.
 //
 // Keys past the context, drafted tokens that a row does not descend from, and
 // whatever the ring held before count nothing: their scores are replaced, not
@@ -46,7 +47,8 @@ namespace {
 constexpr int kStreamWarps = 4;
 constexpr int kCopyWarp = 2 * kStreamWarps;
 constexpr int kProductWarp = kCopyWarp + 1;
-constexpr int kThreads = (kProductWarp + 1) * 32;
+constexpr int kQueryWarp = kProductWarp + 1;  // and the next: one for each stream
+constexpr int kThreads = (kQueryWarp + 2) * 32;
 constexpr int kTile = 128;                 // keys
 constexpr int kRing = 5;                   // 32 KiB buffers of K or V, in turn
 constexpr int kBuf = kTile * kHeadDim * 2;
@@ -58,8 +60,8 @@ struct TreeSmem {
     static constexpr int kKV = kQ + 2 * kBuf;
     static constexpr int kXch = kKV + kRing * kBuf;  // [256] maximum and sum of each softmax thread
     static constexpr int kBar = kXch + 256 * 8;
-    // full[kRing], empty[kRing], qfull[2], sfull[2], pfull[2], odone[2]
-    static constexpr int kNumBars = 2 * kRing + 8;
+    // full[kRing], empty[kRing], qfull[2], sfull[2], pfull[2], odone[2], qempty[2]
+    static constexpr int kNumBars = 2 * kRing + 10;
     static constexpr int kLost = kBar + kNumBars * 8;   // [3] drafted tokens whose values were taken out
     static constexpr int kSlot = kLost + 3 * 8;         // tensor memory address
     static constexpr int kBad = kSlot + 8;              // [kRing] a block id outside the pool
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_addr(smem);
     const uint32_t full0 = sbase + S::kBar, empty0 = full0 + 8 * kRing, qfull0 = empty0 + 8 * kRing, sfull0 = qfull0 + 16,
-                   pfull0 = sfull0 + 16, odone0 = pfull0 + 16;
+                   pfull0 = sfull0 + 16, odone0 = pfull0 + 16, qempty0 = odone0 + 16;
     unsigned long long* lost = reinterpret_cast<unsigned long long*>(smem + S::kLost);
     volatile int* bad = reinterpret_cast<volatile int*>(smem + S::kBad);
 
@@ -91,7 +93,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bad[i] = 0;
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(qfull0 + 8 * i, kStreamWarps);
+            mbar_init(qfull0 + 8 * i, 1);
+            mbar_init(qempty0 + 8 * i, 1);
             mbar_init(sfull0 + 8 * i, 1);
             mbar_init(pfull0 + 8 * i, kStreamWarps);
             mbar_init(odone0 + 8 * i, 1);
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++k) {
                     const int b = k % kRing;
-                    if (lane == 0 && k >= kRing) ok = mbar_wait(empty0 + 8 * b, (k / kRing - 1) & 1);
+                    if (lane == 0 && k >= kRing) ok = wait_bar(empty0 + 8 * b, (k / kRing - 1) & 1);
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok) break;
                     if (lane == 0) {
@@ -159,24 +162,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
         // every copy has landed before the CTA ends
         if (lane == 0)
-            for (int i = max(0, k - kRing); i < k; ++i) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
+            for (int i = max(0, k - kRing); i < k; ++i) wait_bar(full0 + 8 * (i % kRing), (i / kRing) & 1);
     } else if (warp == kProductWarp) {
         // ------------------------------------------------------------ products
         const uint32_t el = issuing_lane(), tm = __shfl_sync(0xffffffffu, tmem, 0), sb = __shfl_sync(0xffffffffu, sbase, 0);
         const uint32_t id_s = umma_idesc(kBF16, 128, kTile, false, false), id_o = umma_idesc(kBF16, 128, D, false, true);
         const uint64_t q_desc = umma_desc_sw128(sb + S::kQ, 16, 1024), k_desc = umma_desc_sw128(sb + S::kKV, 16, 2048),
                        v_desc = umma_desc_sw128(sb + S::kKV, 1024, 2048);  // + (bytes / 16)
-        uint32_t nq[2] = {0, 0}, nsc[2] = {0, 0}, np[2] = {0, 0};  // of each stream: units, products Q K, products P V
+        uint32_t nq[2] = {0, 0}, nsc[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};  // of each stream: units begun, Q K, P V, units ended
         // the tile whose P V is still to come: QK of the next tile goes first, so that the tensor core has
         // work while the softmax has its turn
         int pend_x = -1;
-        uint32_t pend_k = 0, pend_first = 0, pend_frees = 0;
+        uint32_t pend_k = 0, pend_first = 0, pend_frees = 0, pend_last = 0;
         uint32_t last_bar = 0, last_par = 0;
         uint32_t kk = 0;  // buffers so far
         const auto values = [&]() {
             const uint32_t x = pend_x, pb = pend_k % kRing;
             pend_x = -1;
-            ok = mbar_wait_warp(pfull0 + 8 * x, np[x] & 1) && mbar_wait_warp(full0 + 8 * pb, (pend_k / kRing) & 1);
+            ok = mbar_wait_warp(pfull0 + 8 * x, np[x] & 1);  // (the softmax has waited for V)
             if (!ok) return;
             tc_fence_after();
             const uint64_t vd = v_desc + pb * (kBuf / 16);
@@ -184,9 +187,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int ks = 0; ks < kTile / 16; ++ks)
                 umma_f16_ts(el, tm + 256 + 128 * x, tm + 128 * x + 8 * ks, vd + ks * 256, id_o, !pend_first || ks > 0);
             if (pend_frees) umma_commit(el, empty0 + 8 * pb);
-            umma_commit(el, odone0 + 8 * x);
-            last_bar = odone0 + 8 * x;
-            last_par = np[x] & 1;
+            if (pend_last) {
+                umma_commit(el, odone0 + 8 * x);
+                last_bar = odone0 + 8 * x;
+                last_par = no[x]++ & 1;
+            }
             ++np[x];
         };
         for (;;) {
@@ -214,6 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma_f16_ss(el, tm + 128 * x, qd + (ks >> 2) * 1024 + (ks & 3) * 2, kd + (ks >> 2) * 64 + (ks & 3) * 2,
                                     id_s, ks > 0);
                     if (!two || x == 1) umma_commit(el, empty0 + 8 * kb);
+                    const bool last = t + (two ? 1 : 2) >= n;  // the stream's last of the unit
+                    if (last) umma_commit(el, qempty0 + 8 * x);
                     umma_commit(el, sfull0 + 8 * x);
                     last_bar = sfull0 + 8 * x;
                     last_par = nsc[x]++ & 1;
@@ -222,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pend_k = kk + 1;
                     pend_first = !begun[x];
                     pend_frees = !two || x == 1;
+                    pend_last = last;
                     begun[x] = true;
                 }
             }
@@ -229,65 +237,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && pend_x >= 0) values();
         if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
         // every product that was issued has ended before tensor memory is given back
-        if (last_bar) mbar_wait(last_bar, last_par);
+        if (last_bar) wait_bar(last_bar, last_par);
+    } else if (warp >= kQueryWarp) {
+        // ------------------------------------------------------------- queries
+        // Q of each unit into the stream's buffer, as soon as the unit before has no product with it left: 16 lanes to
+        // a row of 256 bytes
+        const int X = warp - kQueryWarp;
+        int k = 0, j = 0;  // units of this stream, tiles
+        while (ok && cur.next(p, it)) {
+            const bool two = it.rows > 128;
+            const int tiles = it.t1 - it.t0, j0 = j;
+            j += tiles;
+            if (!two && tiles == 1 && (j0 & 1) != X) continue;  // no tile of this unit is this stream's
+            if (k > 0) ok = mbar_wait_warp(qempty0 + 8 * X, (k - 1) & 1);
+            if (!ok) break;
+            ++k;
+            const int first = two ? 128 * X : 0, rows = min(128, it.rows - first), c = lane & 15;
+            for (int r0 = 0; r0 < rows; r0 += 2) {
+                const int r = r0 + (lane >> 4);
+                if (r < rows) {
+                    const int row = it.row0 + first + r, token = row / p.group, g = row - token * p.group;
+                    cp_async16(sbase + S::kQ + X * kBuf + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                               static_cast<const uint16_t*>(p.q) +
+                                   ((int64_t)(it.q.tok0 + token) * p.num_q_heads + it.kvh * p.group + g) * D + 8 * c);
+                }
+            }
+            cp_async_wait_all();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull0 + 8 * X);
+        }
+        if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
     } else {
         // ------------------------------------------------------------- softmax
         const int X = warp >> 2, r = tid & 127;  // stream, row of its tile (tensor memory lane)
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t s_addr = lane_addr + 128 * X, o_addr = lane_addr + 256;
         float2* xch = reinterpret_cast<float2*>(smem + S::kXch);
-        int ns = 0, no[2] = {0, 0};  // tiles of this stream; products of both
+        int ns = 0, no[2] = {0, 0};  // tiles of this stream; units of both
         int j = 0, k = 0;            // tiles, items
         bool more = cur.next(p, it);
-        // Q of an item into this stream's buffer (which its earlier products have read)
-        const auto load_q = [&](const DraftItem& n, int j0) {
-            const bool two = n.rows > 128;
-            if (!two && n.t1 - n.t0 == 1 && (j0 & 1) != X) return;  // no tile of this unit is this stream's
-            const int row = (two ? 128 * X : 0) + r;
-            uint4 v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = make_uint4(0, 0, 0, 0);
-            if (row < n.rows) {
-                const int token = (n.row0 + row) / p.group, g = n.row0 + row - token * p.group;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(p.q) +
-                    ((int64_t)(n.q.tok0 + token) * p.num_q_heads + n.kvh * p.group + g) * D);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = __ldg(src + i);
-            }
-            if ((two ? 128 * X : 0) + 32 * (warp & 3) < n.rows) {
-                uint8_t* dst = smem + S::kQ + X * kBuf + r * 128;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4)) = v[i];
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(qfull0 + 8 * X);
+        const auto row_mask = [&](const DraftItem& n) -> uint64_t {
+            const int row = (n.rows > 128 ? 128 * X : 0) + r;
+            return row < n.rows ? draft_mask(p, n.q, (n.row0 + row) / p.group) : 0;
         };
-        if (more) load_q(it, 0);
+        uint64_t mask = more ? row_mask(it) : 0;
         while (more) {
             const bool two = it.rows > 128;
             const int row = (two ? 128 * X : 0) + r;
             const bool live = (two ? 128 * X : 0) + 32 * (warp & 3) < it.rows;  // some row of the warp is real
             const int token = min((it.row0 + row) / p.group, it.q.n - 1);
-            const uint64_t mask = row < it.rows ? draft_mask(p, it.q, token) : 0;
             const int base = it.q.L - it.q.n;
-            float m_run = -INFINITY, l = 0.f;
+            // (a lane without a row, whose scores are anything, never asks for a raise)
+            float m_run = row < it.rows ? -INFINITY : INFINITY, l = 0.f;
             bool begun = false, wrong = false;
             for (int t = it.t0; t < it.t1; ++t, ++j) {
                 const bool mine = two || (j & 1) == X;
-                ++no[0], ++no[1];
-                if (!two) --no[(j & 1) ^ 1];
                 const bool guard = (t + 1) * kTile > base;
                 const int vk = 2 * j + 1;
                 if (mine) {
-                    ok = ok && mbar_wait(sfull0 + 8 * X, ns & 1) &&
-                         (!guard || mbar_wait(full0 + 8 * (vk % kRing), (vk / kRing) & 1));
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = __all_sync(0xffffffffu, ok && wait_bar(sfull0 + 8 * X, ns & 1));
                     ++ns;
                 }
-                if (guard && ok && (mine || two)) {
+                if (live && ok && mine) {
+                    tc_fence_after();
+                    softmax_tile<kBF16>(s_addr, o_addr + 128 * X, guard, p.scale_log2, begun, m_run,
+                                        l, [&](int c) { return draft_visible(t * kTile + c, base, mask); });
+                    tc_fence_before();
+                }
+                if (mine) ok = __all_sync(0xffffffffu, ok && wait_bar(full0 + 8 * (vk % kRing), (vk / kRing) & 1));
+                if (guard && ok && mine) {
                     // this thread's token of V: all of a tile that is the stream's own, half of one that both walk
                     const int tk = two ? 64 * X + (r >> 1) : r;
                     const int pos = t * kTile + tk;
@@ -304,23 +323,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (guard && two) both_streams();
                 if (!mine || !ok) continue;
-                if (live) {
-                    tc_fence_after();
-                    softmax_tile<kBF16>(s_addr, o_addr + 128 * X, guard || !(p.scale_log2 > 0.f), p.scale_log2, begun, m_run,
-                                        l, [&](int c) { return draft_visible(t * kTile + c, base, mask); });
-                    tc_fence_before();
-                }
                 begun = true;
-                ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * (vk % kRing), (vk / kRing) & 1));  // (the product waits too)
-                if (!ok) continue;
                 wrong |= bad[vk % kRing] != 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pfull0 + 8 * X);
             }
-            // ---- the unit's end: the next unit's queries are fetched first
+            // ---- the unit's end: the next unit's masks are fetched first
             const DraftItem done = it;
             more = cur.next(p, it);
-            if (ok && more) load_q(it, j);
+            const uint64_t next_mask = more ? row_mask(it) : 0;  // (on its way during the output)
             xch[tid] = make_float2(m_run, wrong || !ok ? -1.f : l);
             if (tid == 0) lost[(k + 1) % 3] = 0;  // (read last before the barrier of the unit before)
             both_streams();
@@ -330,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 has[x] = x >= x0 && x < x1 && (two || done.t1 - done.t0 > 1 || ((j - 1) & 1) == x);
-                if (has[x]) ok = ok && mbar_wait(odone0 + 8 * x, (no[x] - 1) & 1);
+                if (has[x]) ok = ok && wait_bar(odone0 + 8 * x, no[x] & 1);
+                no[x] += two || done.t1 - done.t0 > 1 || ((j - 1) & 1) == x;
             }
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
@@ -346,50 +358,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum = (has[0] ? a.y * f0 : 0.f) + (has[1] ? b.y * f1 : 0.f);
             }
             const bool part = done.partial();
-            const float inv = part ? 1.f : (sum != 0.f ? 1.f / sum : 0.f);
             const int64_t prow = (int64_t)(blockIdx.x * 2 + (done.begins() ? 1 : 0)) * kTreeRows + row;
-            // this thread's dims: all of its row, or with both streams on one row the stream's half
+            // this thread's dims: all of its row, or with both streams on one row the stream's half; 64 at a time, and the
+            // streams go on to their next tiles once both have read
             const int c0 = two ? 0 : 2 * X, c1 = two ? 4 : 2 * X + 2;
             const int head = done.kvh * p.group + done.row0 + row - token * p.group;
+            const float g0 = two ? (X == 0 ? 1.f : 0.f) : has[0] ? f0 : 0.f, g1 = two ? (X == 1 ? 1.f : 0.f) : has[1] ? f1 : 0.f;
 #pragma unroll 1
-            for (int c = c0; c < c1; ++c) {
-                float o[32];
+            for (int c = c0; c < c1; c += 2) {
+                float o[2][32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[h][i] = 0.f;
+                }
                 if (live && ok) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         if (!has[x]) continue;
-                        float v[32];
-                        tmem_ld32_start(o_addr + 128 * x + 32 * c, v);
-                        tmem_ld_wait32(v);
-                        const float f = two ? 1.f : x ? f1 : f0;
+                        const float g = x ? g1 : g0;  // (zero where the other stream's sums are not worth anything)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = f != 0.f ? fmaf(v[i], f, o[i]) : o[i];
+                        for (int h = 0; h < 2; ++h) {
+                            float v[32];
+                            tmem_ld32_start(o_addr + 128 * x + 32 * (c + h), v);
+                            tmem_ld_wait32(v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[h][i] = g != 0.f ? fmaf(v[i], g, o[h][i]) : o[h][i];
+                        }
                     }
                 }
-                if (row >= done.rows) continue;
-                if (sum == 0.f) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                if (c + 2 >= c1) {
+                    tc_fence_before();
+                    both_streams();
+                    tc_fence_after();
                 }
+                if (row >= done.rows) continue;
                 if (part) {
                     float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[8 * h + i] = make_float4(o[h][4 * i], o[h][4 * i + 1], o[h][4 * i + 2], o[h][4 * i + 3]);
                 } else {
+                    const float inv = zero || sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays)
                     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
                                                           ((int64_t)(done.q.tok0 + token) * p.num_q_heads + head) * D +
                                                           32 * c);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = zero ? 0u : pack2<kBF16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
-                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = inv == 0.f ? 0u : pack2<kBF16>(o[h][8 * i + 2 * e] * inv, o[h][8 * i + 2 * e + 1] * inv);
+                            dst[4 * h + i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                 }
             }
             if (row < done.rows && !zero) {
@@ -415,9 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  done.q.tok0, done.row0, done.rows);
                 d[1] = make_int4(done.kvh, 0, 0, 0);
             }
-            tc_fence_before();
-            both_streams();  // both streams' sums have been read
-            tc_fence_after();
+            mask = next_mask;
             ++k;
         }
         if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
