@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                             (key & 7) * 128 + (tid & 1) * 4096);
                         uint32_t any = 0;
 #pragma unroll 2
-                        for (int i = 0; i < 32; ++i) any |= scrub8<kBF16>(v + (i >> 3) * 64 + (i & 7), pos < it.q.L);
+                        for (int i = 0; i < 32; ++i) any |= scrub8<kBF16>(v + (i >> 3) * 64 + ((i + key) & 7), pos < it.q.L);
                         if (any) atomicOr(lost + k % 3, 1ull << (pos - base));
                     }
                 }

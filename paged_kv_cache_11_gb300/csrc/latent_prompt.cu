@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 2
                     for (int i = 0; i < (shared ? 8 : 16); ++i)
                         any |= scrub8<kBF16>(reinterpret_cast<uint4*>(smem + S::kKV + ((u + h0 + (i >> 3)) % kRing) * kUnit +
-                                                                     key * 128) + (i & 7),
+                                                                     key * 128) + ((i + key) & 7),
                                              pos < nk);
                     if (any) atomicOr(lost + (pos - masked * kTile) / 32, 1u << (pos & 31));
                 }

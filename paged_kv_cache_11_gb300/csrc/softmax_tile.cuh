@@ -21,7 +21,8 @@ __device__ __forceinline__ uint32_t finite_or_zero2(uint32_t w) {
     return w & ~((bad & 1u ? 0xffffu : 0u) | (bad & 2u ? 0xffff0000u : 0u));
 }
 
-// Eight 16-bit values of a token in shared memory: zeros for a token that is not there, else with those that are not finite
+// Eight 16-bit values of a token in shared memory (threads that take a token each start at different eighths of its 128
+// bytes, which would all lie in the same banks): zeros for a token that is not there, else with those that are not finite
 // put to zero; whether there were any.
 template <bool kBF16>
 __device__ __forceinline__ uint32_t scrub8(uint4* v, bool there) {

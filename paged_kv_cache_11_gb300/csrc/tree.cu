@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t any = 0;
 #pragma unroll 2
                         for (int i = 0; i < (two ? 8 : 16); ++i)
-                            any |= scrub8<kBF16>(v + (i >> 3) * 64 + (i & 7), pos < it.q.L);
+                            any |= scrub8<kBF16>(v + (i >> 3) * 64 + ((i + tk) & 7), pos < it.q.L);
                         if (any) atomicOr(lost + k % 3, 1ull << (pos - base));
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
