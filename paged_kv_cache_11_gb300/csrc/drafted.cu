@@ -10,8 +10,8 @@
 namespace pkv {
 
 constexpr int kMergeThreads = 256;
-constexpr int kMergeSlices = 4;    // CTAs of one unit
-constexpr int kMergeItems = 8;     // float4 of a thread
+constexpr int kMergeSlices = 8;    // CTAs of one unit
+constexpr int kMergeItems = 4;     // float4 of a thread
 constexpr int kMergeParts = 128;   // pieces at a time
 
 // kRows: of a slice, at most.
@@ -96,21 +96,25 @@ __global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftP
             }
             __syncthreads();
         }
-        for (int k = 0; k < np; ++k) {
-            float4 v[kMergeItems];
-            if (k0 + k < 2) {
-#pragma unroll
-                for (int i = 0; i < kMergeItems; ++i) v[i] = k == 0 ? early[0][i] : early[1][i];
-            } else {
-                fetch(k0 + k, v);
-            }
+        const auto add = [&](int k, const float4 (&v)[kMergeItems]) {
 #pragma unroll
             for (int i = 0; i < kMergeItems; ++i) {
                 const int r = (tid + i * kMergeThreads) / (D / 4);
-                if (r >= n) continue;
-                const float w = weight[r][k];
+                const float w = r < n ? weight[r][k] : 0.f;
                 if (w != 0.f) o[i].x += w * v[i].x, o[i].y += w * v[i].y, o[i].z += w * v[i].z, o[i].w += w * v[i].w;
             }
+        };
+        int k = 0;
+        if (k0 == 0) {
+            add(0, early[0]);
+            add(1, early[1]);
+            k = 2;
+        }
+#pragma unroll 4
+        for (; k < np; ++k) {
+            float4 v[kMergeItems];
+            fetch(k0 + k, v);
+            add(k, v);
         }
     }
 #pragma unroll

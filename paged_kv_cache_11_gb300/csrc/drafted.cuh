@@ -115,15 +115,14 @@ struct DraftCursor {
     DraftSeq q;
     int units;
 
-    __device__ __forceinline__ void start(const DraftParams& p, int s0, int64_t offset, int64_t count) {
+    // From tile t0 of unit u0 of sequence s0 on.
+    __device__ __forceinline__ void start(const DraftParams& p, int s0, const DraftSeq& q0, int u0, int t0, int64_t count) {
         s = s0;
-        left = count;
-        if (left <= 0) return;
-        q = draft_seq(p, s);
+        q = q0;
         units = U::units(p, q);
-        const int tiles = U::tiles(q);
-        u = (int)(offset / tiles);
-        t = (int)(offset - (int64_t)u * tiles);
+        u = u0;
+        t = t0;
+        left = count;
     }
     __device__ __forceinline__ bool next(const DraftParams& p, DraftItem& it) {
         if (left <= 0) return false;
@@ -161,23 +160,30 @@ __device__ __forceinline__ void zero_rows(const DraftParams& p, int tok0, int n,
 // thread of the CTA calls it and gets the same piece.  A piece is the line's
 // length over the CTAs, and kLeast tiles at least (or the longest unit, where
 // that is shorter): a smaller one costs more in starting and merging than it
-// spreads.  On the way the sequences that attend nothing get their zeros, and
-// bad metadata is recorded, each by one CTA.  scratch: (kThreads / 32) * 8 +
-// 32 bytes of shared memory, 8-byte aligned.
+// spreads.  Where no unit is longer than that and each can have a CTA of its
+// own, it has, and nothing is divided.  On the way the sequences that attend
+// nothing get their zeros, and bad metadata is recorded, each by one CTA.
+// scratch: (kThreads / 32) * 16 + 48 bytes of shared memory, 8-byte aligned.
+template <int kThreads>
+__host__ __device__ constexpr int draft_scratch() {
+    return kThreads / 32 * 16 + 48;
+}
 template <int kRows, int kTile, int kThreads, int kLeast>
 __device__ __forceinline__ void draft_schedule(const DraftParams& p, int value_dims, void* scratch,
                                                DraftCursor<kRows, kTile>& cur) {
     using U = UnitShape<kRows, kTile>;
     constexpr int kWarps = kThreads / 32;
-    long long* warp_sum = static_cast<long long*>(scratch);             // [kWarps]
-    long long* found = warp_sum + kWarps;                               // [2]: sequence, offset
-    int* longest = reinterpret_cast<int*>(found + 2);
+    long long* warp_tiles = static_cast<long long*>(scratch);  // [kWarps]
+    long long* warp_units = warp_tiles + kWarps;               // [kWarps]
+    long long* count = warp_units + kWarps;
+    int* longest = reinterpret_cast<int*>(count + 1);
+    int* found = longest + 1;  // [6]: sequence, its first token, tokens, length; unit, tile
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) *longest = 0;
+    if (tid == 0) *longest = 0, *count = 0;
     __syncthreads();
     const int per = (p.num_seqs + kThreads - 1) / kThreads;
     const int first = tid * per;
-    long long sum = 0;
+    long long tiles = 0, units = 0;
     int most = 0;
     for (int k = 0; k < per; ++k) {
         const int s = first + k;
@@ -185,10 +191,11 @@ __device__ __forceinline__ void draft_schedule(const DraftParams& p, int value_d
         q.n = 0, q.idle = false, q.err = 0, q.tok0 = 0, q.L = 0;
         if (s < p.num_seqs) {
             q = draft_seq(p, s);
-            const int units = U::units(p, q), tiles = U::tiles(q);
-            if (units > 0) {
-                sum += (long long)units * tiles;
-                most = max(most, tiles);
+            const int n = U::units(p, q);
+            if (n > 0) {
+                units += n;
+                tiles += (long long)n * U::tiles(q);
+                most = max(most, U::tiles(q));
             }
             if (q.err && s % p.ctas == (int)blockIdx.x) record_error(p.err, q.err);
         }
@@ -200,42 +207,53 @@ __device__ __forceinline__ void draft_schedule(const DraftParams& p, int value_d
         }
     }
     if (most > 0) atomicMax(longest, most);
-    long long scan = sum;  // inclusive over the warp
+    long long scan = tiles, scan_units = units;  // inclusive over the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += v;
+        const long long v = __shfl_up_sync(0xffffffffu, scan, o), w = __shfl_up_sync(0xffffffffu, scan_units, o);
+        if (lane >= o) scan += v, scan_units += w;
     }
-    if (lane == 31) warp_sum[warp] = scan;
+    if (lane == 31) warp_tiles[warp] = scan, warp_units[warp] = scan_units;
     __syncthreads();
-    long long total = 0, before = 0;
-#pragma unroll
+    long long total = 0, before = 0, total_units = 0, before_units = 0;
+#pragma unroll 1
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += warp_sum[w];
-        total += warp_sum[w];
+        if (w < warp) before += warp_tiles[w], before_units += warp_units[w];
+        total += warp_tiles[w];
+        total_units += warp_units[w];
     }
-    before += scan - sum;
-    const long long least = min(kLeast, *longest);
-    const long long piece = max((total + p.ctas - 1) / p.ctas, least);
-    const long long w0 = min(total, piece * blockIdx.x), w1 = min(total, w0 + piece);
-    if (w0 < w1 && before <= w0 && w0 < before + sum) {  // this thread's sequences hold the piece's start
+    const bool whole = *longest <= kLeast && total_units <= p.ctas;  // a unit to a CTA
+    long long w0, w1;
+    if (whole) {
+        before = before_units + scan_units - units, tiles = units;
+        w0 = min(total_units, (long long)blockIdx.x), w1 = min(total_units, w0 + 1);
+    } else {
+        const long long piece = max((total + p.ctas - 1) / p.ctas, (long long)min(kLeast, *longest));
+        before += scan - tiles;
+        w0 = min(total, piece * blockIdx.x), w1 = min(total, w0 + piece);
+    }
+    if (w0 < w1 && before <= w0 && w0 < before + tiles) {  // this thread's sequences hold the piece's start
         long long at = before;
         for (int k = 0; k < per; ++k) {
             const int s = first + k;
             if (s >= p.num_seqs) break;
             const DraftSeq q = draft_seq(p, s);
-            const int units = U::units(p, q);
-            const long long cost = units > 0 ? (long long)units * U::tiles(q) : 0;
-            if (w0 < at + cost) {
-                found[0] = s;
-                found[1] = w0 - at;
+            const int n = U::units(p, q), len = n > 0 && !whole ? U::tiles(q) : 1;
+            if (w0 < at + (long long)n * len) {
+                const long long in = w0 - at;
+                const int u = (int)(in / len);
+                found[0] = s, found[1] = q.tok0, found[2] = q.n, found[3] = q.L;
+                found[4] = u, found[5] = (int)(in - (long long)u * len);
+                *count = whole ? U::tiles(q) : w1 - w0;
                 break;
             }
-            at += cost;
+            at += (long long)n * len;
         }
     }
     __syncthreads();
-    cur.start(p, w0 < w1 ? (int)found[0] : 0, w0 < w1 ? found[1] : 0, w1 - w0);
+    DraftSeq q;
+    q.tok0 = found[1], q.n = found[2], q.L = found[3], q.err = 0, q.idle = false;
+    cur.start(p, found[0], q, found[4], found[5], w0 < w1 ? *count : 0);
 }
 
 // The merge of divided units (drafted.cu): value_dims 128 (tree.cu) or 512 (latent.cu).

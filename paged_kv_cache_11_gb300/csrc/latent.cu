@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     Cursor cur;
     draft_schedule<kLatentRows, kTile, kThreads, kLeast>(p, kValue, smem + S::kAlpha, cur);
-    static_assert((kThreads / 32) * 8 + 32 <= 2 * kLatentRows * 4, "the schedule's scratch");
+    static_assert(draft_scratch<kThreads>() <= 2 * kLatentRows * 4, "the schedule's scratch");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -339,10 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (pos >= base) {
                         uint4* v = reinterpret_cast<uint4*>(smem + S::kKV + b * kSlots * kSlot + (key >> 3) * kGroup +
                                                             (key & 7) * 128 + (tid & 1) * 4096);
-                        uint32_t any = 0;
-#pragma unroll 2
-                        for (int i = 0; i < 32; ++i) any |= scrub8<kBF16>(v + (i >> 3) * 64 + ((i + key) & 7), pos < it.q.L);
-                        if (any) atomicOr(lost + k % 3, 1ull << (pos - base));
+                        // (neighbouring threads start at different eighths of 128 bytes: the same would lie in the same banks)
+                        if (scrub<kBF16>(32, pos < it.q.L, [&](int i) { return v + (i >> 3) * 64 + ((i + key) & 7); }))
+                            atomicOr(lost + k % 3, 1ull << (pos - base));
                     }
                 }
                 float xa = -INFINITY, xb = -INFINITY;

@@ -253,13 +253,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // where both streams use the tile each sees to half of it
                     const int key = shared ? 64 * X + (r >> 1) : r, pos = t * kTile + key;
                     const int h0 = shared ? r & 1 : 0;
-                    uint32_t any = 0;
-#pragma unroll 2
-                    for (int i = 0; i < (shared ? 8 : 16); ++i)
-                        any |= scrub8<kBF16>(reinterpret_cast<uint4*>(smem + S::kKV + ((u + h0 + (i >> 3)) % kRing) * kUnit +
-                                                                     key * 128) + ((i + key) & 7),
-                                             pos < nk);
-                    if (any) atomicOr(lost + (pos - masked * kTile) / 32, 1u << (pos & 31));
+                    const auto at = [&](int i) {  // (neighbouring threads start at different eighths of 128 bytes)
+                        return reinterpret_cast<uint4*>(smem + S::kKV + ((u + h0 + (i >> 3)) % kRing) * kUnit + key * 128) +
+                               ((i + key) & 7);
+                    };
+                    if (scrub<kBF16>(shared ? 8 : 16, pos < nk, at)) atomicOr(lost + (pos - masked * kTile) / 32, 1u << (pos & 31));
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 if (shared) both_streams();

@@ -21,24 +21,36 @@ __device__ __forceinline__ uint32_t finite_or_zero2(uint32_t w) {
     return w & ~((bad & 1u ? 0xffffu : 0u) | (bad & 2u ? 0xffff0000u : 0u));
 }
 
-// Eight 16-bit values of a token in shared memory (threads that take a token each start at different eighths of its 128
-// bytes, which would all lie in the same banks): zeros for a token that is not there, else with those that are not finite
-// put to zero; whether there were any.
-template <bool kBF16>
-__device__ __forceinline__ uint32_t scrub8(uint4* v, bool there) {
+// The values of one token in shared memory, 16 * n bytes at the places at(i): zeros for a token that is not there, else those
+// that are not finite are put to zero; whether there were any.  Looked for by a product with zero, which is NaN for them.
+template <bool kBF16, typename At>
+__device__ __forceinline__ bool scrub(int n, bool there, At at) {
     if (!there) {
-        *v = make_uint4(0, 0, 0, 0);
-        return 0;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) *at(i) = make_uint4(0, 0, 0, 0);
+        return false;
     }
-    uint4 w = *v;
-    const uint32_t bad =
-        not_finite2<kBF16>(w.x) | not_finite2<kBF16>(w.y) | not_finite2<kBF16>(w.z) | not_finite2<kBF16>(w.w);
-    if (bad) {
+    uint32_t acc = 0;
+    const auto see = [&](uint32_t w) {
+        if constexpr (kBF16)
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w), "r"(0u));
+        else
+            asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w), "r"(0u));
+    };
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const uint4 w = *at(i);
+        see(w.x), see(w.y), see(w.z), see(w.w);
+    }
+    if (!not_finite2<kBF16>(acc)) return false;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        uint4 w = *at(i);
         w.x = finite_or_zero2<kBF16>(w.x), w.y = finite_or_zero2<kBF16>(w.y);
         w.z = finite_or_zero2<kBF16>(w.z), w.w = finite_or_zero2<kBF16>(w.w);
-        *v = w;
+        *at(i) = w;
     }
-    return bad;
+    return true;
 }
 
 template <bool kBF16>

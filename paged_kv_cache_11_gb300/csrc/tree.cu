@@ -67,7 +67,7 @@ struct TreeSmem {
     static constexpr int kBad = kSlot + 8;              // [kRing] a block id outside the pool
     static constexpr int kTotal = kBad + kRing * 4 + 4;
     static_assert(kTotal <= 227 * 1024 && kBar % 8 == 0, "shared memory of one CTA");
-    static_assert((kThreads / 32) * 8 + 32 <= kBuf, "the schedule's scratch lies where Q will");
+    static_assert(draft_scratch<kThreads>() <= kBuf, "the schedule's scratch lies where Q will");
 };
 
 __device__ __forceinline__ void both_streams() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -313,11 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (pos >= base) {
                         uint4* v = reinterpret_cast<uint4*>(smem + S::kKV + (vk % kRing) * kBuf + (tk >> 3) * 2048 +
                                                             (tk & 7) * 128 + (two ? (r & 1) * 1024 : 0));
-                        uint32_t any = 0;
-#pragma unroll 2
-                        for (int i = 0; i < (two ? 8 : 16); ++i)
-                            any |= scrub8<kBF16>(v + (i >> 3) * 64 + ((i + tk) & 7), pos < it.q.L);
-                        if (any) atomicOr(lost + k % 3, 1ull << (pos - base));
+                        // (neighbouring threads start at different eighths of 128 bytes: the same would lie in the same banks)
+                        if (scrub<kBF16>(two ? 8 : 16, pos < it.q.L, [&](int i) { return v + (i >> 3) * 64 + ((i + tk) & 7); }))
+                            atomicOr(lost + k % 3, 1ull << (pos - base));
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
