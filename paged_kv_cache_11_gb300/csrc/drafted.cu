@@ -10,15 +10,13 @@
 namespace pkv {
 
 constexpr int kMergeThreads = 256;
-constexpr int kMergeSlices = 8;    // CTAs of one unit
-constexpr int kMergeItems = 4;     // float4 of a thread
 constexpr int kMergeParts = 128;   // pieces at a time
 
-// kRows: of a slice, at most.
-template <bool kBF16, int D, int kRows>
+// A CTA merges a slice of a unit, kMergeItems float4 to a thread.
+template <bool kBF16, int D, int kUnitRows, int kMergeItems>
 __global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftParams p) {
-    static_assert(kRows * D / 4 == kMergeThreads * kMergeItems, "every thread has its items");
-    constexpr int kUnitRows = kRows * kMergeSlices;
+    constexpr int kRows = kMergeThreads * kMergeItems / (D / 4);  // of a slice, at most
+    static_assert(kUnitRows % kRows == 0, "whole slices");
     __shared__ float weight[kRows][kMergeParts];
     __shared__ float top[kRows], total[kRows];
     __shared__ int last_s;
@@ -130,12 +128,24 @@ __global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftP
     }
 }
 
+template <int D, int kUnitRows>
+static cudaError_t launch_merge_t(const DraftParams& p, bool bf16, bool few, cudaStream_t stream) {
+    auto kern = few ? (bf16 ? draft_merge_kernel<true, D, kUnitRows, 1> : draft_merge_kernel<false, D, kUnitRows, 1>)
+                    : (bf16 ? draft_merge_kernel<true, D, kUnitRows, 2> : draft_merge_kernel<false, D, kUnitRows, 2>);
+    const int rows = kMergeThreads * (few ? 1 : 2) / (D / 4);
+    return launch_pdl(kern, dim3(p.ctas, kUnitRows / rows), dim3(kMergeThreads), 0, stream, p);
+}
+
 cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, cudaStream_t stream, int* launches) {
-    constexpr int kTree = kTreeRows / kMergeSlices, kLatent = kLatentRows / kMergeSlices;
-    const bool bf16 = dtype == PKV_BF16;
-    auto kern = value_dims == 128 ? (bf16 ? draft_merge_kernel<true, 128, kTree> : draft_merge_kernel<false, 128, kTree>)
-                                  : (bf16 ? draft_merge_kernel<true, 512, kLatent> : draft_merge_kernel<false, 512, kLatent>);
-    const cudaError_t e = launch_pdl(kern, dim3(p.ctas, kMergeSlices), dim3(kMergeThreads), 0, stream, p);
+    // Few units are divided into many pieces each, and their slices are made small enough to give every SM some; many
+    // units fill the SMs as they are, and smaller slices would only be more CTAs to start (of 152 x 32, and all but the
+    // divided units' have nothing to do).
+    const int unit_rows = value_dims == 128 ? kTreeRows : kLatentRows;
+    const int64_t rows = (int64_t)((p.num_tokens + p.num_seqs - 1) / p.num_seqs) * p.group;
+    const int64_t units = p.num_seqs * (int64_t)p.num_kv_heads * ((rows + unit_rows - 1) / unit_rows);
+    const bool few = units * 16 < 2 * p.ctas, bf16 = dtype == PKV_BF16;
+    const cudaError_t e = value_dims == 128 ? launch_merge_t<128, kTreeRows>(p, bf16, few, stream)
+                                            : launch_merge_t<512, kLatentRows>(p, bf16, few, stream);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

@@ -256,6 +256,12 @@ __device__ __forceinline__ void draft_schedule(const DraftParams& p, int value_d
     cur.start(p, found[0], q, found[4], found[5], w0 < w1 ? *count : 0);
 }
 
+// Can a unit of this call be divided?  Not where all are short and each surely has a CTA of its own (see draft_schedule).
+inline bool draft_divides(const DraftParams& p, int tile, int unit_rows, int least) {
+    if (p.len_limit <= tile) return false;
+    const int64_t units = p.num_kv_heads * (p.num_seqs + (int64_t)p.num_tokens * p.group / unit_rows);
+    return p.len_limit > (int64_t)least * tile || units > p.ctas;
+}
 // The merge of divided units (drafted.cu): value_dims 128 (tree.cu) or 512 (latent.cu).
 cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, cudaStream_t stream, int* launches);
 // tree.cu

@@ -524,8 +524,7 @@ cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size
                                            : (bf16 ? launch_t<true, 32>(p, tmq, tmc, stream) : launch_t<false, 32>(p, tmq, tmc, stream));
     if (e != cudaSuccess) return e;
     ++*launches;
-    // a unit of one tile is never divided
-    return p.len_limit > kTile ? launch_draft_merge(p, dtype, kValue, stream, launches) : cudaSuccess;
+    return draft_divides(p, kTile, kLatentRows, kLeast) ? launch_draft_merge(p, dtype, kValue, stream, launches) : cudaSuccess;
 }
 
 }  // namespace pkv

@@ -466,8 +466,7 @@ cudaError_t launch_tree(const DraftParams& p, int dtype, int block_size, const C
                                            : (bf16 ? launch_t<true, 32>(p, tmk, tmv, stream) : launch_t<false, 32>(p, tmk, tmv, stream));
     if (e != cudaSuccess) return e;
     ++*launches;
-    // a unit of one tile is never divided
-    return p.len_limit > kTile ? launch_draft_merge(p, dtype, kHeadDim, stream, launches) : cudaSuccess;
+    return draft_divides(p, kTile, kTreeRows, kLeast) ? launch_draft_merge(p, dtype, kHeadDim, stream, launches) : cudaSuccess;
 }
 
 }  // namespace pkv
