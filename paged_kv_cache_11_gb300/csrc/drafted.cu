@@ -21,14 +21,14 @@ __global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftP
     __shared__ float top[kRows], total[kRows];
     __shared__ int last_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
-    if (tid == 0) last_s = p.ctas - 1;
+    if (tid == 0) last_s = p.pieces - 1;
     __syncthreads();
     pdl_wait();
     const int4 d = __ldcg(p.part_desc + (c * 2 + 1) * 2);
     const int kvh = __ldcg(p.part_desc + (c * 2 + 1) * 2 + 1).x;
     const int state = d.x, tok0 = d.y, row0 = d.z, rows = d.w;
     // the CTA that holds the unit's last tile: the first behind this one that ends a unit which it did not begin
-    for (int k = c + 1 + tid; k < p.ctas; k += kMergeThreads)
+    for (int k = c + 1 + tid; k < p.pieces; k += kMergeThreads)
         if (__ldcg(p.part_desc + k * 4).x & kPartEnds) {
             atomicMin(&last_s, k);
             break;
@@ -133,19 +133,20 @@ static cudaError_t launch_merge_t(const DraftParams& p, bool bf16, bool few, cud
     auto kern = few ? (bf16 ? draft_merge_kernel<true, D, kUnitRows, 1> : draft_merge_kernel<false, D, kUnitRows, 1>)
                     : (bf16 ? draft_merge_kernel<true, D, kUnitRows, 2> : draft_merge_kernel<false, D, kUnitRows, 2>);
     const int rows = kMergeThreads * (few ? 1 : 2) / (D / 4);
-    return launch_pdl(kern, dim3(p.ctas, kUnitRows / rows), dim3(kMergeThreads), 0, stream, p);
+    return launch_pdl(kern, dim3(p.pieces, kUnitRows / rows), dim3(kMergeThreads), 0, stream, p);
 }
 
-cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, cudaStream_t stream, int* launches) {
+cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, int unit_rows, cudaStream_t stream,
+                               int* launches) {
     // Few units are divided into many pieces each, and their slices are made small enough to give every SM some; many
     // units fill the SMs as they are, and smaller slices would only be more CTAs to start (of 152 x 32, and all but the
     // divided units' have nothing to do).
-    const int unit_rows = value_dims == 128 ? kTreeRows : kLatentRows;
     const int64_t rows = (int64_t)((p.num_tokens + p.num_seqs - 1) / p.num_seqs) * p.group;
     const int64_t units = p.num_seqs * (int64_t)p.num_kv_heads * ((rows + unit_rows - 1) / unit_rows);
-    const bool few = units * 16 < 2 * p.ctas, bf16 = dtype == PKV_BF16;
+    const bool few = units * 16 < 2 * p.pieces, bf16 = dtype == PKV_BF16;
     const cudaError_t e = value_dims == 128 ? launch_merge_t<128, kTreeRows>(p, bf16, few, stream)
-                                            : launch_merge_t<512, kLatentRows>(p, bf16, few, stream);
+                          : unit_rows == kLatentRows ? launch_merge_t<512, kLatentRows>(p, bf16, few, stream)
+                                                     : launch_merge_t<512, 2 * kLatentRows>(p, bf16, few, stream);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

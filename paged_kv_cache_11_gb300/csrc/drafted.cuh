@@ -30,16 +30,16 @@ struct DraftParams {
     const int64_t* tree_masks;    // [num_tokens]; nullptr: chains
     void* out;                    // [num_tokens][num_q_heads][value dims], q's type
     const void* values;           // the pool that values are read from (rows that are not finite)
-    float* part_o;                // [ctas][2][rows of a unit][value dims]
-    float2* part_ml;              // [ctas][2][rows of a unit]: running maximum (log2 domain) and sum
-    int4* part_desc;              // [ctas][2][2]: state, first token, first row, rows; KV head
+    float* part_o;                // [pieces][2][rows of a unit][value dims]
+    float2* part_ml;              // [pieces][2][rows of a unit]: running maximum (log2 domain) and sum
+    int4* part_desc;              // [pieces][2][2]: state, first token, first row, rows; KV head
     int* err;
     int64_t num_blocks;
     int num_seqs, num_tokens, num_q_heads, num_kv_heads;
     int group;                    // query heads of a KV head
     int max_blocks_per_seq;
     int len_limit;                // max_blocks_per_seq * block_size
-    int ctas;
+    int pieces;                   // of the line: CTAs of the grid, or clusters
     float scale_log2;             // scale * log2(e)
 };
 
@@ -156,8 +156,8 @@ __device__ __forceinline__ void zero_rows(const DraftParams& p, int tok0, int n,
     for (int64_t i = lane; i < vecs; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Deals the line to the grid and starts `cur` on this CTA's piece; every
-// thread of the CTA calls it and gets the same piece.  A piece is the line's
+// Deals the line and starts `cur` on piece piece_id of it; every thread of the
+// CTA (and every CTA of a cluster) calls it and gets the same piece.  A piece is the line's
 // length over the CTAs, and kLeast tiles at least (or the longest unit, where
 // that is shorter): a smaller one costs more in starting and merging than it
 // spreads.  Where no unit is longer than that and each can have a CTA of its
@@ -169,7 +169,7 @@ __host__ __device__ constexpr int draft_scratch() {
     return kThreads / 32 * 16 + 48;
 }
 template <int kRows, int kTile, int kThreads, int kLeast>
-__device__ __forceinline__ void draft_schedule(const DraftParams& p, int value_dims, void* scratch,
+__device__ __forceinline__ void draft_schedule(const DraftParams& p, int piece_id, int value_dims, void* scratch,
                                                DraftCursor<kRows, kTile>& cur) {
     using U = UnitShape<kRows, kTile>;
     constexpr int kWarps = kThreads / 32;
@@ -197,9 +197,9 @@ __device__ __forceinline__ void draft_schedule(const DraftParams& p, int value_d
                 tiles += (long long)n * U::tiles(q);
                 most = max(most, U::tiles(q));
             }
-            if (q.err && s % p.ctas == (int)blockIdx.x) record_error(p.err, q.err);
+            if (q.err && s % p.pieces == piece_id) record_error(p.err, q.err);
         }
-        unsigned idle = __ballot_sync(0xffffffffu, q.idle && s % p.ctas == (int)blockIdx.x);
+        unsigned idle = __ballot_sync(0xffffffffu, q.idle && s % p.pieces == piece_id);
         while (idle) {
             const int src = __ffs(idle) - 1;
             idle &= idle - 1;
@@ -222,15 +222,15 @@ __device__ __forceinline__ void draft_schedule(const DraftParams& p, int value_d
         total += warp_tiles[w];
         total_units += warp_units[w];
     }
-    const bool whole = *longest <= kLeast && total_units <= p.ctas;  // a unit to a CTA
+    const bool whole = *longest <= kLeast && total_units <= p.pieces;  // a unit to a CTA
     long long w0, w1;
     if (whole) {
         before = before_units + scan_units - units, tiles = units;
-        w0 = min(total_units, (long long)blockIdx.x), w1 = min(total_units, w0 + 1);
+        w0 = min(total_units, (long long)piece_id), w1 = min(total_units, w0 + 1);
     } else {
-        const long long piece = max((total + p.ctas - 1) / p.ctas, (long long)min(kLeast, *longest));
+        const long long piece = max((total + p.pieces - 1) / p.pieces, (long long)min(kLeast, *longest));
         before += scan - tiles;
-        w0 = min(total, piece * blockIdx.x), w1 = min(total, w0 + piece);
+        w0 = min(total, piece * piece_id), w1 = min(total, w0 + piece);
     }
     if (w0 < w1 && before <= w0 && w0 < before + tiles) {  // this thread's sequences hold the piece's start
         long long at = before;
@@ -260,18 +260,20 @@ __device__ __forceinline__ void draft_schedule(const DraftParams& p, int value_d
 inline bool draft_divides(const DraftParams& p, int tile, int unit_rows, int least) {
     if (p.len_limit <= tile) return false;
     const int64_t units = p.num_kv_heads * (p.num_seqs + (int64_t)p.num_tokens * p.group / unit_rows);
-    return p.len_limit > (int64_t)least * tile || units > p.ctas;
+    return p.len_limit > (int64_t)least * tile || units > p.pieces;
 }
 // The merge of divided units (drafted.cu): value_dims 128 (tree.cu) or 512 (latent.cu).
-cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, cudaStream_t stream, int* launches);
+cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, int unit_rows, cudaStream_t stream,
+                               int* launches);
 // tree.cu
 cudaError_t launch_tree(const DraftParams& p, int dtype, int block_size, const CUtensorMap& tmk, const CUtensorMap& tmv,
                         cudaStream_t stream, int* launches);
 constexpr int kTreeRows = 256;   // query rows of a unit
 // latent.cu
-cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size, const CUtensorMap& tmq,
+cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size, bool pairs, const CUtensorMap& tmq,
                                  const CUtensorMap& tmc, cudaStream_t stream, int* launches);
-constexpr int kLatentRows = 64;
+constexpr int kLatentRows = 64;   // of a CTA; a pair of CTAs takes units of twice as many
+int latent_pairs();               // pairs of CTAs that the current device holds at once (0: not known)
 
 // The position bits that a query row attends among its sequence's drafted tokens.
 __device__ __forceinline__ uint64_t draft_mask(const DraftParams& p, const DraftSeq& q, int token) {

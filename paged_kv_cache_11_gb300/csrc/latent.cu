@@ -33,6 +33,8 @@
 // row's sum is that of the weights before.  Masked places are replaced, not added to, and
 // values that are not finite are kept out of the products of tiles with masks,
 // as there.
+#include <atomic>
+
 #include "drafted.cuh"
 #include "softmax_tile.cuh"
 
@@ -93,11 +95,24 @@ __device__ __forceinline__ bool softmax_any(bool mine) {
     return r != 0;
 }
 
-template <bool kBF16, int BS>
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return (int)r;
+}
+// Every thread of both CTAs of the cluster.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// kPair: the CTA is one of a cluster of two that share a unit of 128 rows.
+template <bool kBF16, int BS, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmc, const DraftParams p) {
     using S = LatentSmem;
-    using Cursor = DraftCursor<kLatentRows, kTile>;
+    constexpr int kUnitRows = kPair ? 2 * kLatentRows : kLatentRows;
+    using Cursor = DraftCursor<kUnitRows, kTile>;
+    const int rank = kPair ? cluster_rank() : 0, piece = kPair ? blockIdx.x / 2 : blockIdx.x;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_addr(smem);
@@ -109,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(full0 + 8 * i, 1);
-            mbar_init(empty0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, kPair ? 2 : 1);  // (a slot is filled in both CTAs at once)
         }
         mbar_init(sfull0, 1);
         mbar_init(sfull0 + 8, 1);
@@ -128,26 +143,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProductWarp) tmem_alloc(sbase + S::kAddr, kTmemCols);
     pdl_wait();
     pdl_launch_dependents();  // (the merge kernel waits for this one's end)
-    if (tid == 0) {           // no partials yet
-        p.part_desc[blockIdx.x * 4] = make_int4(0, 0, 0, 0);
-        p.part_desc[blockIdx.x * 4 + 2] = make_int4(0, 0, 0, 0);
+    if (tid == 0 && rank == 0) {  // no partials yet
+        p.part_desc[piece * 4] = make_int4(0, 0, 0, 0);
+        p.part_desc[piece * 4 + 2] = make_int4(0, 0, 0, 0);
     }
     Cursor cur;
-    draft_schedule<kLatentRows, kTile, kThreads, kLeast>(p, kValue, smem + S::kAlpha, cur);
+    draft_schedule<kUnitRows, kTile, kThreads, kLeast>(p, piece, kValue, smem + S::kAlpha, cur);
     static_assert(draft_scratch<kThreads>() <= 2 * kLatentRows * 4, "the schedule's scratch");
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) cluster_sync();  // the other CTA's barriers are ready
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S::kAddr);
     DraftItem it;
     bool ok = true;  // no wait has run out
+    // The next part of a unit, with this CTA's rows of it.
+    int unit_rows = 0, first_rows = 0;  // rows of the unit, and those of its first CTA
+    const auto next = [&]() -> bool {
+        if (!cur.next(p, it)) return false;
+        unit_rows = it.rows;
+        if constexpr (kPair) {
+            const int mine = first_rows = (it.rows + 1) / 2;
+            it.row0 += rank * mine;
+            it.rows = rank ? it.rows - mine : mine;
+        }
+        return true;
+    };
 
     if (warp == kCopyWarp) {
         // -------------------------------------------------------------- copies
         const uint64_t policy = l2_policy_evict_first();
         const uint32_t el = issuing_lane();
         int c = 0;  // tiles
-        while (ok && cur.next(p, it)) {
+        while (ok && next()) {
             const int32_t* table = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
             const int units = (it.q.L + kSlotKeys - 1) / kSlotKeys;
             int ids = 0;  // block ids of 32 slots, 8 tiles
@@ -177,7 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (jj < units) {
                         if (el) {
                             mbar_arrive_expect_tx(bar, kSlot);
-                            tma_load_4d(sbase + S::kKV + slot * kSlot, &tmc, bar, 0, 0, 0, group, policy);
+                            if constexpr (!kPair)
+                                tma_load_4d(sbase + S::kKV + slot * kSlot, &tmc, bar, 0, 0, 0, group, policy);
+                            else if ((i & 1) == rank)  // the CTAs take turns, each for both
+                                tma_load_4d_multicast(sbase + S::kKV + slot * kSlot, &tmc, bar, 0, 0, 0, group, 3, policy);
                         }
                     } else if (el) {
                         mbar_arrive(bar);  // behind the context: whatever lies there is masked
@@ -189,12 +220,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every copy has landed before the CTA ends
         if (lane == 0)
             for (int i = max(0, c - 2); i < c; ++i)
-                for (int k = 0; k < kSlots; ++k) wait_bar(full0 + 8 * ((i & 1) * kSlots + k), (i / 2) & 1);
+                for (int k = 0; k < kSlots; ++k) {
+                    wait_bar(full0 + 8 * ((i & 1) * kSlots + k), (i / 2) & 1);
+                    // ... and, with a pair, what the other CTA's products have to say here has been said
+                    if (kPair) wait_bar(empty0 + 8 * ((i & 1) * kSlots + k), (i / 2) & 1);
+                }
     } else if (warp == kQueryWarp) {
         // ------------------------------------------------------------- queries
         if (lane == 0) {
             int k = 0;
-            while (ok && cur.next(p, it)) {
+            while (ok && next()) {
                 if (k > 0) ok = wait_bar(qempty, (k - 1) & 1);
                 if (!ok) break;
                 mbar_arrive_expect_tx(qfull, kParts * kLatentRows * 128);
@@ -226,10 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t since = 0;  // of a wait
         while (ok) {
             if (left == 0 && more) {
-                more = cur.next(p, it);
+                more = next();
                 left = __shfl_sync(0xffffffffu, more ? it.t1 - it.t0 : 0, 0);
                 more = left > 0;
-                id_o = umma_idesc(kBF16, 128, (__shfl_sync(0xffffffffu, it.rows, 0) + 15) / 16 * 16, true, false);
+                id_o = umma_idesc(kBF16, 128, max(16, (__shfl_sync(0xffffffffu, it.rows, 0) + 15) / 16 * 16), true, false);
                 first = true;
             }
             if (np < nk && mbar_test_warp(pfull, np & 1)) {
@@ -241,7 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
                         umma_f16_ss(el, tm + 64 * mt, vd + ks * (kSlot / 16) + mt * 128, p_desc + ks * 2, id, !begins || ks > 0);
-                    umma_commit(el, empty0 + 8 * (b * kSlots + ks));
+                    if constexpr (kPair)
+                        umma_commit_multicast(el, empty0 + 8 * (b * kSlots + ks), 3);
+                    else
+                        umma_commit(el, empty0 + 8 * (b * kSlots + ks));
                 }
                 umma_commit(el, odone);
                 last_bar = odone;
@@ -295,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* alpha = reinterpret_cast<float*>(smem + S::kAlpha);
         float* fin = reinterpret_cast<float*>(smem + S::kFin);
         int c = 0, k = 0;
-        while (cur.next(p, it)) {
+        while (next()) {
             const int base = it.q.L - it.q.n;
             const int ta = min((it.row0 + ra) / p.group, it.q.n - 1), tb = min((it.row0 + rb) / p.group, it.q.n - 1);
             const uint64_t mask_a = draft_mask(p, it.q, ta), mask_b = draft_mask(p, it.q, tb);
@@ -423,12 +461,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lb += __shfl_xor_sync(0xffffffffu, lb, o);
             }
             const bool part = it.partial(), zero = !ok || wrong;
-            const int slot = blockIdx.x * 2 + (it.begins() ? 1 : 0);
+            const int slot = piece * 2 + (it.begins() ? 1 : 0);
+            const int64_t prow = (int64_t)slot * kUnitRows + (kPair && rank ? first_rows : 0);  // row 0 of this CTA's
             if ((lane & 3) == 0) {
                 if (part) {
-                    float2* ml = p.part_ml + (int64_t)slot * kLatentRows;
-                    ml[ra] = make_float2(ma, zero ? -1.f : la);
-                    ml[rb] = make_float2(mb, zero ? -1.f : lb);
+                    float2* ml = p.part_ml + prow;
+                    if (ra < it.rows) ml[ra] = make_float2(ma, zero ? -1.f : la);
+                    if (rb < it.rows) ml[rb] = make_float2(mb, zero ? -1.f : lb);
                     fin[ra] = fin[rb] = 1.f;
                 } else {
                     fin[ra] = la != 0.f && !zero ? 1.f / la : 0.f;
@@ -437,10 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (tid == 0) {
                 lost[(k + 1) % 3] = 0;  // (read last before the barrier of the unit before)
-                if (part) {
+                if (part && rank == 0) {
                     p.part_desc[slot * 2] =
                         make_int4(kPartValid | (it.begins() ? kPartBegins : 0) | (it.ends() ? kPartEnds : 0), it.q.tok0,
-                                  it.row0, it.rows);
+                                  it.row0, unit_rows);
                     p.part_desc[slot * 2 + 1] = make_int4(0, 0, 0, 0);
                 }
             }
@@ -459,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i) o[i] = 0.f;
                 }
                 if (part) {
-                    float* dst = p.part_o + ((int64_t)slot * kLatentRows + r0) * kValue + d;
+                    float* dst = p.part_o + (prow + r0) * kValue + d;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (r0 + i < it.rows) dst[(int64_t)i * kValue] = o[i];
@@ -490,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int r = 0; r < it.rows; ++r)
                         if (draft_mask(p, it.q, (it.row0 + r) / p.group) >> bit & 1)
                             add_not_finite<kBF16>(
-                                part ? p.part_o + ((int64_t)slot * kLatentRows + r) * kValue + 4 * tid : nullptr,
+                                part ? p.part_o + (prow + r) * kValue + 4 * tid : nullptr,
                                 static_cast<uint16_t*>(p.out) +
                                     ((int64_t)it.q.tok0 * p.num_q_heads + it.row0 + r) * kValue + 4 * tid,
                                 static_cast<const uint16_t*>(p.values) + ((int64_t)id * BS + pos % BS) * kRow + 4 * tid, 4);
@@ -505,26 +544,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == kProductWarp) tmem_dealloc(tmem, kTmemCols);
+    if constexpr (kPair) cluster_sync();  // nothing of the other CTA's is on its way here any more
 }
 
 template <bool kBF16, int BS>
-cudaError_t launch_t(const DraftParams& p, const CUtensorMap& tmq, const CUtensorMap& tmc, cudaStream_t stream) {
-    auto kern = latent_kernel<kBF16, BS>;
+cudaError_t launch_t(const DraftParams& p, bool pairs, const CUtensorMap& tmq, const CUtensorMap& tmc, cudaStream_t stream) {
+    auto kern = pairs ? latent_kernel<kBF16, BS, true> : latent_kernel<kBF16, BS, false>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LatentSmem::kTotal);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(p.ctas), dim3(kThreads), LatentSmem::kTotal, stream, tmq, tmc, p);
+    if (!pairs) return launch_pdl(kern, dim3(p.pieces), dim3(kThreads), LatentSmem::kTotal, stream, tmq, tmc, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * p.pieces);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = LatentSmem::kTotal;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {2, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, tmq, tmc, p);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size, const CUtensorMap& tmq,
+int latent_pairs() {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = cache[dev].load();
+    if (n == 0) {
+        auto kern = latent_kernel<true, 16, true>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LatentSmem::kTotal) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = LatentSmem::kTotal;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {2, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        cache[dev].store(n);
+    }
+    return n;
+}
+
+cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size, bool pairs, const CUtensorMap& tmq,
                                  const CUtensorMap& tmc, cudaStream_t stream, int* launches) {
     const bool bf16 = dtype == PKV_BF16;
-    const cudaError_t e = block_size == 16 ? (bf16 ? launch_t<true, 16>(p, tmq, tmc, stream) : launch_t<false, 16>(p, tmq, tmc, stream))
-                                           : (bf16 ? launch_t<true, 32>(p, tmq, tmc, stream) : launch_t<false, 32>(p, tmq, tmc, stream));
+    const cudaError_t e =
+        block_size == 16
+            ? (bf16 ? launch_t<true, 16>(p, pairs, tmq, tmc, stream) : launch_t<false, 16>(p, pairs, tmq, tmc, stream))
+            : (bf16 ? launch_t<true, 32>(p, pairs, tmq, tmc, stream) : launch_t<false, 32>(p, pairs, tmq, tmc, stream));
     if (e != cudaSuccess) return e;
     ++*launches;
-    return draft_divides(p, kTile, kLatentRows, kLeast) ? launch_draft_merge(p, dtype, kValue, stream, launches) : cudaSuccess;
+    const int rows = pairs ? 2 * kLatentRows : kLatentRows;
+    return draft_divides(p, kTile, rows, kLeast) ? launch_draft_merge(p, dtype, kValue, rows, stream, launches) : cudaSuccess;
 }
 
 }  // namespace pkv

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.part_desc[blockIdx.x * 4 + 2] = make_int4(0, 0, 0, 0);
     }
     Cursor cur;
-    draft_schedule<kTreeRows, kTile, kThreads, kLeast>(p, D, smem + S::kQ, cur);
+    draft_schedule<kTreeRows, kTile, kThreads, kLeast>(p, blockIdx.x, D, smem + S::kQ, cur);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -454,7 +454,7 @@ cudaError_t launch_t(const DraftParams& p, const CUtensorMap& tmk, const CUtenso
     auto kern = tree_kernel<kBF16, BS>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem::kTotal);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(p.ctas), dim3(kThreads), TreeSmem::kTotal, stream, tmk, tmv, p);
+    return launch_pdl(kern, dim3(p.pieces), dim3(kThreads), TreeSmem::kTotal, stream, tmk, tmv, p);
 }
 
 }  // namespace
@@ -466,7 +466,7 @@ cudaError_t launch_tree(const DraftParams& p, int dtype, int block_size, const C
                                            : (bf16 ? launch_t<true, 32>(p, tmk, tmv, stream) : launch_t<false, 32>(p, tmk, tmv, stream));
     if (e != cudaSuccess) return e;
     ++*launches;
-    return draft_divides(p, kTile, kTreeRows, kLeast) ? launch_draft_merge(p, dtype, kHeadDim, stream, launches) : cudaSuccess;
+    return draft_divides(p, kTile, kTreeRows, kLeast) ? launch_draft_merge(p, dtype, kHeadDim, kTreeRows, stream, launches) : cudaSuccess;
 }
 
 }  // namespace pkv
