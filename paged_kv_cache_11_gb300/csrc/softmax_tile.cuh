@@ -110,7 +110,7 @@ __device__ __forceinline__ f32x2 add_f32x2(f32x2 a, f32x2 b) {
 }
 
 // Raises the row's maximum to mx where that passes it, and rescales what the row has summed.
-__device__ __forceinline__ void raise_maximum(float mx, uint32_t o_addr, bool begun, float& m_run, float& l) {
+__device__ __forceinline__ void raise_maximum(float mx, uint32_t o_addr, float& m_run, float& l) {
     const bool raise = mx > m_run + kRaise;
     if (!__any_sync(0xffffffffu, raise)) return;
     float alpha = 1.f;
@@ -119,7 +119,6 @@ __device__ __forceinline__ void raise_maximum(float mx, uint32_t o_addr, bool be
         m_run = mx;
         l *= alpha;
     }
-    if (!begun) return;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         float o[32];
@@ -150,70 +149,55 @@ __device__ __forceinline__ void weights32(const float (&v)[32], f32x2 f, f32x2 n
 //
 // Twice over S, 32 columns at a time, the largest score and then the weights: a row kept in registers between the two does not
 // fit beside the rest (168 registers a thread).  Taking a tile against the maxima of the tiles before, in one pass whose
-// weights wait in registers, is 500 of 1500 cycles shorter for one warp and 5% slower for the prompts' kernel.  Tiles with
-// masks go another way, a loop that leaves out columns that no row of the warp attends: with both in one unrolled body, or
-// the loop unrolled, the warps wait for instructions.
+// weights wait in registers, is 500 of 1500 cycles shorter for one warp and 5% slower for the prompts' kernel; eight warps to
+// a stream, with half a row's registers each, are slower yet.  Masks are written into S first, so that a tile with masks goes
+// the same way as the others: code that runs once in a unit waits for its instructions, and a loop of its own for such tiles
+// took 5200 cycles where the way of all tiles takes 1500.
 template <bool kBF16, typename Seen>
 __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, bool masked, float scale_log2, bool begun,
                                              float& m_run, float& l, Seen seen) {
-    f32x2 sum = pack_f32x2(0.f, 0.f);
-    if (!masked && scale_log2 > 0.f) {
-        float s[2][32];
-        float mx = -INFINITY;
-        tmem_ld32_start(s_addr, s[0]);
-#pragma unroll
+    // Where the scale is above zero, it is applied on the way into the exponential; else the scores are scaled in S, since
+    // their order is another then.
+    const bool scaled = !(scale_log2 > 0.f);
+    const float f = scaled ? 1.f : scale_log2;
+    if (masked || scaled) {
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-            tmem_ld_wait32(s[c & 1]);
-            tmem_ld32_start(s_addr + 32 * ((c + 1) & 3), s[(c + 1) & 1]);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(s[c & 1][i], s[c & 1][i + 1]));
-        }
-        raise_maximum(mx * scale_log2, o_addr, begun, m_run, l);
-        const float ms = m_run == -INFINITY ? 0.f : m_run;
-        const f32x2 f = pack_f32x2(scale_log2, scale_log2), neg = pack_f32x2(-ms, -ms);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            tmem_ld_wait32(s[c & 1]);
-            if (c < 3) tmem_ld32_start(s_addr + 32 * (c + 1), s[(c + 1) & 1]);
-            uint32_t w[16];
-            weights32<kBF16>(s[c & 1], f, neg, w, sum);
-            tmem_st16_start(s_addr + 16 * c, w);  // over columns that have been read
-        }
-    } else {
-        // (scores are scaled before they are compared: a scale below zero turns their order around)
-        const auto scores = [&](int c, uint32_t bits, float (&s)[32]) {
+            const uint32_t bits = masked ? seen(32 * c) : ~0u;
+            if (!scaled && __all_sync(0xffffffffu, bits == ~0u)) continue;
+            float s[32];
             tmem_ld32_start(s_addr + 32 * c, s);
             tmem_ld_wait32(s);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1 ? s[i] * scale_log2 : -INFINITY;
-        };
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-            const uint32_t bits = masked ? seen(32 * c) : ~0u;
-            if (__all_sync(0xffffffffu, bits == 0)) continue;
-            float s[32];
-            scores(c, bits, s);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(s[i], s[i + 1]));
+            for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1 ? (scaled ? s[i] * scale_log2 : s[i]) : -INFINITY;
+            tmem_st32(s_addr + 32 * c, s);
         }
-        raise_maximum(mx, o_addr, begun, m_run, l);
-        const float ms = m_run == -INFINITY ? 0.f : m_run;
-        const f32x2 f = pack_f32x2(1.f, 1.f), neg = pack_f32x2(-ms, -ms);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-            const uint32_t bits = masked ? seen(32 * c) : ~0u;
-            uint32_t w[16];
-            if (__all_sync(0xffffffffu, bits == 0)) {
+    }
+    f32x2 sum = pack_f32x2(0.f, 0.f);
+    float s[2][32];
+    float mx = -INFINITY;
+    tmem_ld32_start(s_addr, s[0]);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = 0;
-            } else {
-                float s[32];
-                scores(c, bits, s);
-                weights32<kBF16>(s, f, neg, w, sum);
-            }
-            tmem_st16_start(s_addr + 16 * c, w);
-        }
+    for (int c = 0; c < 4; ++c) {
+        tmem_ld_wait32(s[c & 1]);
+        tmem_ld32_start(s_addr + 32 * ((c + 1) & 3), s[(c + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(s[c & 1][i], s[c & 1][i + 1]));
+    }
+    mx *= f;
+    if (begun)
+        raise_maximum(mx, o_addr, m_run, l);
+    else
+        m_run = fmaxf(m_run, mx);
+    const float ms = m_run == -INFINITY ? 0.f : m_run;
+    const f32x2 ff = pack_f32x2(f, f), neg = pack_f32x2(-ms, -ms);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        tmem_ld_wait32(s[c & 1]);
+        if (c < 3) tmem_ld32_start(s_addr + 32 * (c + 1), s[(c + 1) & 1]);
+        uint32_t w[16];
+        weights32<kBF16>(s[c & 1], ff, neg, w, sum);
+        tmem_st16_start(s_addr + 16 * c, w);  // over columns that have been read
     }
     const float2 both = unpack_f32x2(sum);
     l += both.x + both.y;

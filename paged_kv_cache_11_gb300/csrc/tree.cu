@@ -357,35 +357,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool part = done.partial();
             const int64_t prow = (int64_t)(blockIdx.x * 2 + (done.begins() ? 1 : 0)) * kTreeRows + row;
-            // this thread's dims: all of its row, or with both streams on one row the stream's half; 64 at a time, and the
-            // streams go on to their next tiles once both have read
+            // this thread's dims: all of its row, or with both streams on one row the stream's half; the streams go on to
+            // their next tiles once both have read
             const int c0 = two ? 0 : 2 * X, c1 = two ? 4 : 2 * X + 2;
             const int head = done.kvh * p.group + done.row0 + row - token * p.group;
-            const float g0 = two ? (X == 0 ? 1.f : 0.f) : has[0] ? f0 : 0.f, g1 = two ? (X == 1 ? 1.f : 0.f) : has[1] ? f1 : 0.f;
+            const float g0 = two ? 1.f : f0, g1 = two ? 1.f : f1;
+            const float inv = zero || sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays)
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 2) {
-                float o[2][32];
+            for (int c = c0; c < c1; ++c) {
+                float o[32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[h][i] = 0.f;
-                }
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
                 if (live && ok) {
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < 2; ++x) {
-                        if (!has[x]) continue;
-                        const float g = x ? g1 : g0;  // (zero where the other stream's sums are not worth anything)
+                        if (!(x ? has[1] : has[0])) continue;
+                        const float g = x ? g1 : g0;
+                        float v[32];
+                        tmem_ld32_start(o_addr + 128 * x + 32 * c, v);
+                        tmem_ld_wait32(v);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float v[32];
-                            tmem_ld32_start(o_addr + 128 * x + 32 * (c + h), v);
-                            tmem_ld_wait32(v);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[h][i] = g != 0.f ? fmaf(v[i], g, o[h][i]) : o[h][i];
-                        }
+                        for (int i = 0; i < 32; ++i) o[i] = fmaf(v[i], g, o[i]);
                     }
                 }
-                if (c + 2 >= c1) {
+                if (c + 1 == c1) {
                     tc_fence_before();
                     both_streams();
                     tc_fence_after();
@@ -394,25 +389,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (part) {
                     float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[8 * h + i] = make_float4(o[h][4 * i], o[h][4 * i + 1], o[h][4 * i + 2], o[h][4 * i + 3]);
+                    for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 } else {
-                    const float inv = zero || sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays)
                     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                                          ((int64_t)(done.q.tok0 + token) * p.num_q_heads + head) * D +
-                                                          32 * c);
+                                                          ((int64_t)(done.q.tok0 + token) * p.num_q_heads + head) * D + 32 * c);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = inv == 0.f ? 0u : pack2<kBF16>(o[h][8 * i + 2 * e] * inv, o[h][8 * i + 2 * e + 1] * inv);
-                            dst[4 * h + i] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = inv == 0.f ? 0u : pack2<kBF16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
+                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
             }
             if (row < done.rows && !zero) {
