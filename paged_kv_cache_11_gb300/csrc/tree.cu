@@ -38,6 +38,19 @@
 // turn into NaN; so in the tiles that any row masks, values past the context
 // are zeroed and drafted values that are not finite are taken out, and added to
 // the rows that do attend them when those are written.
+//
+// What bounds it.  Copies alone (the same kernel without products and softmax)
+// run at 7.0 TB/s.  8 documents of 131072 tokens, 64/8 heads, 31 drafted tokens
+// (4.3 GB): 900-940 us, 4.7 TB/s, 1.2 PFLOP/s, bound by the chain of a stream's
+// tile, Q K, softmax, P V, of some 4200 cycles in which two tiles of rows are
+// worked off (the copies' pace is 2800; without the softmax 775 us).  64
+// contexts of 512 to 4096, 32/8 heads, 16 tokens (606 MB): 131-139 us, 4.5
+// TB/s; 128 of up to 2048, 40 heads without sharing, 1 to 5 tokens (2.7 GB):
+// 620-690 us, 4.1 TB/s: there the ends of units, when the last tile's softmax,
+// product and output follow one another and the ring runs full, are what is
+// left.  Tried and not kept: output by four warps of its own (they were as long
+// as the chain they took over), twice the softmax warps, a loop for the
+// products, the weights in one pass (softmax_tile.cuh).
 #include "drafted.cuh"
 #include "softmax_tile.cuh"
 
@@ -58,7 +71,7 @@ constexpr uint32_t kTmemCols = 512;        // S and P of the streams: [0, 128), 
 struct TreeSmem {
     static constexpr int kQ = 0;  // [2 streams][2 dims halves][128 rows][128 B]
     static constexpr int kKV = kQ + 2 * kBuf;
-    static constexpr int kXch = kKV + kRing * kBuf;  // [256] maximum and sum of each softmax thread
+    static constexpr int kXch = kKV + kRing * kBuf;  // [256] maximum and sum of each thread of the softmax
     static constexpr int kBar = kXch + 256 * 8;
     // full[kRing], empty[kRing], qfull[2], sfull[2], pfull[2], odone[2], qempty[2]
     static constexpr int kNumBars = 2 * kRing + 10;
