@@ -6,9 +6,7 @@
 //
 // Bytes against operations: a token's row is read once (1152 bytes) for 2 (576
 // + 512) operations of every query row, 121 operations a byte at the 64 rows of
-// a unit here, where the card has 288: one unit's rows are bound by the memory,
-// two units of one sequence (128 heads) by the tensor cores' shared-memory
-// reads, below.
+// a CTA here, where the card has 288.
 //
 // The sums of 64 rows x 512 values are 256 columns of tensor memory when the
 // values are the lanes, so the second product is transposed; the first is not,
@@ -30,9 +28,24 @@
 // Warps: 0-3 the softmax (16 rows each) and the output, 4 the copies of rows, 5
 // the products, 6 the copies of queries.  The maximum is raised lazily, as in
 // tree.cu; a weight is rounded to the cache's 16-bit type for its product, the
-// row's sum is that of the weights before.  Masked places are replaced, not added to, and
-// values that are not finite are kept out of the products of tiles with masks,
-// as there.
+// row's sum is that of the weights before.  Masked places are replaced, not
+// added to, and values that are not finite are kept out of the products of
+// tiles with masks, as there.
+//
+// Batches of more than 64 query rows a sequence go to pairs of CTAs (clusters of
+// two): each has half of a unit's rows, and they take turns at copying, each
+// slot into both CTAs' rings, so that a row leaves L2 once for 128 query rows.
+//
+// What bounds it.  A tile costs the tensor core 36 x 32 + 16 x 48 cycles (the
+// latter by shared memory reads, 128 bytes a cycle), 1920 in all; its copy 3200
+// at the memory's pace.  The ring holds two tiles, and a tile is held from its
+// copy to its last product, so the latencies of both (copy 1700 cycles, softmax
+// 1000) add up to some 3750 cycles a tile.  8 contexts of 131072 tokens, 16
+// heads, 1 to 4 drafted tokens (1.2 GB): 236 us, 5.1 TB/s, 13 us of it the
+// merge; 64 of 512 to 4096 with 128 heads (190 MB): 92 us, 450 TFLOP/s, of it 13
+// the merge of 36 MB of divided sums, and two or three outputs of 3 us a CTA;
+// without pairs 97.  Tiles of 32 keys, four in the ring, were slower (269, 103):
+// products with N = 32 take 34 cycles to issue and not 16.
 #include <atomic>
 
 #include "drafted.cuh"

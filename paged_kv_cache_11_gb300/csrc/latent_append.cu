@@ -8,7 +8,9 @@
 // A warp takes one token's row, 16 values of the latent to a lane, so the
 // norm's sum is one exchange over the warp; or 16 of a token's query heads,
 // eight lanes to a head, whose four loads are all on their way before the
-// first is used.  Pairs (i, i + 32) sit in lanes 4 apart and cost one exchange;
+// first is used: 16384 tokens with 16 heads (128 MB) take 24.2 us, 5.3 TB/s, and
+// a step of 64 tokens with 128 heads 2.0 us, a launch.  (More warps on an SM at
+// fewer registers: 25.1 and 28.6 us; CTAs of 256 threads: 25.2.)  Pairs (i, i + 32) sit in lanes 4 apart and cost one exchange;
 // neighbouring pairs sit in one lane.
 #include "pkv_internal.cuh"
 

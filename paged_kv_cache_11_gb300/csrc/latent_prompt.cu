@@ -17,6 +17,14 @@
 // either kind has one barrier.
 //
 // CTAs of one head follow one another, the longest rows first.
+//
+// What bounds it: two prompts of 8192 tokens with 128 heads (5.5 TFLOP) take
+// 3.88 to 4.0 ms, 1.4 PFLOP/s, 73% of the card's peak and 80% of what it sustains
+// under its power limit.  Without the softmax the products alone take 3.6 ms; the
+// rest is the part of a stream's softmax that the other's products do not cover.
+// (A warp for each stream's products: 3.92 against 3.90 ms.)  Seven prompts of 1
+// to 1537 tokens with 40 heads: 182 us, of it some 8000 cycles for each of the
+// CTAs to start and end, one on an SM at a time.
 #include "softmax_tile.cuh"
 
 namespace pkv {
