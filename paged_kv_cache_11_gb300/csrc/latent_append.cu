@@ -10,8 +10,9 @@
 // eight lanes to a head, whose four loads are all on their way before the
 // first is used: 16384 tokens with 16 heads (128 MB) take 24.2 us, 5.3 TB/s, and
 // a step of 64 tokens with 128 heads 2.0 us, a launch.  (More warps on an SM at
-// fewer registers: 25.1 and 28.6 us; CTAs of 256 threads: 25.2.)  Pairs (i, i + 32) sit in lanes 4 apart and cost one exchange;
-// neighbouring pairs sit in one lane.
+// fewer registers: 25.1 and 28.6 us; CTAs of 256 threads: 25.2.)  Pairs (i, i +
+// 32) sit in lanes 4 apart and cost one exchange; neighbouring pairs sit in one
+// lane.
 #include "pkv_internal.cuh"
 
 namespace pkv {
