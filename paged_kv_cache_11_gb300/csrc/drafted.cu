@@ -3,10 +3,10 @@
 // domain) and weight of piece p,
 //     out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p.
 // A row whose pieces hold no weight is zeros; a piece of negative weight (bad
-// metadata) zeroes its rows.  The pieces lie in L2, where the main kernel left
-// them; a chain of latencies bounds the merge (which unit, where it ends, its
-// weights, its sums): 4 to 5 us for 18 MB in pairs of pieces, 13 us for 36 MB, and
-// 13 for eight units of 19 pieces.
+// metadata) zeroes its rows; what is not finite in any piece stays so.  The
+// pieces lie in L2, where the main kernel left them; a chain of latencies bounds
+// the merge (which unit, where it ends, its weights, its sums): 4 to 5 us for 18
+// MB in pairs of pieces, 13 us for 36 MB, and 13 for eight units of 19 pieces.
 #include "drafted.cuh"
 
 namespace pkv {
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftP
         for (int k = lane; k < parts; k += 32) {
             const float2 ml = k < 32 ? mine : __ldcg(p.part_ml + at(k, r));
             const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);  // (nothing there for this row)
-            if (w != 0.f) l += w * ml.y;
+            l += w * ml.y;  // (a sum that is NaN stays, of a weight of zero too)
             if (k < kMergeParts) weight[r][k] = w;
         }
 #pragma unroll
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kMergeThreads) draft_merge_kernel(const DraftP
             for (int i = 0; i < kMergeItems; ++i) {
                 const int r = (tid + i * kMergeThreads) / (D / 4);
                 const float w = r < n ? weight[r][k] : 0.f;
-                if (w != 0.f) o[i].x += w * v[i].x, o[i].y += w * v[i].y, o[i].z += w * v[i].z, o[i].w += w * v[i].w;
+                o[i].x += w * v[i].x, o[i].y += w * v[i].y, o[i].z += w * v[i].z, o[i].w += w * v[i].w;
             }
         };
         int k = 0;
@@ -143,7 +143,7 @@ cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, 
     // Few units are divided into many pieces each, and their slices are made small enough to give every SM some; many
     // units fill the SMs as they are, and smaller slices would only be more CTAs to start (of 152 x 32, and all but the
     // divided units' have nothing to do).
-    const int64_t rows = (int64_t)((p.num_tokens + p.num_seqs - 1) / p.num_seqs) * p.group;
+    const int64_t rows = ((int64_t)p.num_tokens + p.num_seqs - 1) / p.num_seqs * p.group;
     const int64_t units = p.num_seqs * (int64_t)p.num_kv_heads * ((rows + unit_rows - 1) / unit_rows);
     const bool few = units * 16 < 2 * p.pieces, bf16 = dtype == PKV_BF16;
     const cudaError_t e = value_dims == 128 ? launch_merge_t<128, kTreeRows>(p, bf16, few, stream)

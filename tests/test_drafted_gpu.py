@@ -179,6 +179,46 @@ def test_keys_and_queries_that_are_not_finite(gpu, kind):
     assert off.all() and torch.isnan(b.out[1, 3]).all()
 
 
+@pytest.mark.parametrize("kind,heads", [("tree", 4), ("tree", 64), ("latent", 16), ("latent", 128)])
+def test_what_is_not_finite_in_divided_contexts(gpu, kind, heads):
+    """Contexts long enough to be divided: what spoils one part spoils the row, also where nothing else in that part counts."""
+    n = 3
+    for L in (3000, 40000):
+        b = Batch(30, [(L, n), (50, 2)], heads, 1, 16, BF, kind, "tree")
+        y, bound = b.expected(0)
+        held = b.q[1, 3].clone()
+        b.q[1, 3] = float("nan")
+        run(b)
+        off = (b.out[:n].double() - y).abs() <= bound
+        assert torch.isnan(b.out[1, 3]).all(), L
+        off[1, 3] = True
+        assert off.all(), L
+        b.check(only=[1])
+        b.q[1, 3] = held
+        # the keys of the first half of the context, more than a part of it
+        ids = b.tables[0, :L // 2 // 16].long()
+        b.pools[0][ids] = float("nan")
+        run(b)
+        assert torch.isnan(b.out[:n]).all(), L
+        b.check(only=[1])
+
+
+def test_a_value_of_no_weight_that_is_not_finite(gpu):
+    """Where a part's weights all fall below fp32 against another's: 0 times what is not finite is not finite."""
+    L, n, dim, at = 3000, 2, 9, 37
+    b = Batch(31, [(L, n)], 4, 1, 16, BF, "tree", "chain")
+    b.q.fill_(1.0)
+    b.pools[0][b.tables[0, :1536 // 16].long()] = -20.0     # 2^-326 of the other half's weights, that are about 1
+    y, bound = b.expected(0)
+    b.pools[1][int(b.tables[0, at // 16]), 0, at % 16, dim] = float("inf")
+    run(b)
+    got = b.out.double()
+    assert not torch.isfinite(got[..., dim]).any()
+    ok = (got - y).abs() <= bound
+    ok[..., dim] = True
+    assert ok.all()
+
+
 # ------------------------------------------------------------------ the order of blocks, other streams, graphs
 @pytest.mark.parametrize("kind", KINDS)
 def test_physical_order_does_not_matter(gpu, kind):
