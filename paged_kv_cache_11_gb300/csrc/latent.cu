@@ -530,12 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint32_t*>(dst + (int64_t)2 * i * kValue) = w;
                 }
             }
-            if (gone && !zero) {
+            if (gone) {
                 // values that are not finite and were left out of the products, for the rows that attend them: a thread
                 // takes four values of every row
                 softmax_sync();
 #pragma unroll 1
-                for (unsigned long long at = gone; at; at &= at - 1) {
+                for (unsigned long long at = zero ? 0 : gone; at; at &= at - 1) {
                     const int bit = __ffsll(at) - 1, pos = base + bit;
                     const int id = p.block_tables[(int64_t)it.s * p.max_blocks_per_seq + pos / BS];
 #pragma unroll 1
