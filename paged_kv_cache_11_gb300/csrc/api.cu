@@ -1048,6 +1048,7 @@ pkv_status latent_attention_prefill(const void* q, const void* kv, const void* k
     p.num_queries = num_query_tokens;
     p.num_keys = num_key_tokens;
     p.max_query_len = max_query_len;
+    p.sms = std::max(1, sm_count());
     p.scale_log2 = scale * 1.4426950408889634f;
     // [tokens][heads][values]: one copy brings 64 values of one head of 128 tokens (a tensor without tokens is never
     // copied from; its map only has to exist)

@@ -16,15 +16,24 @@
 // of values t keys t - 1: that is all that a copy waits for, and a tile of
 // either kind has one barrier.
 //
-// CTAs of one head follow one another, the longest rows first.
+// CTAs of one head follow one another, the longest rows first.  A CTA that has
+// issued the copies of its queries' last tile takes the place of one that has
+// not begun (a cluster launch control request) and goes on with that one's
+// queries and keys, so that they are on their way while the last tiles are worked
+// off, and barriers and tensor memory are set up once: 16 prompts of 256 tokens
+// with 128 heads 135 us for 168, 8 of 1024 423 for 477, one of 16384 with 64
+// heads 3.38 ms for 3.47.  (Claimed one item earlier, the grid's last items wait
+// behind long ones: 7 ragged prompts 175 us for 169.)  Grids of one CTA an SM at
+// most claim nothing.
 //
-// What bounds it: two prompts of 8192 tokens with 128 heads (5.5 TFLOP) take
-// 3.88 to 4.0 ms, 1.4 PFLOP/s, 73% of the card's peak and 80% of what it sustains
+// What bounds it: two prompts of 8192 tokens with 128 heads (5.5 TFLOP) take 3.77
+// to 3.8 ms, 1.46 PFLOP/s, 76% of the card's peak and 83% of what it sustains
 // under its power limit.  Without the softmax the products alone take 3.6 ms; the
-// rest is the part of a stream's softmax that the other's products do not cover.
-// (A warp for each stream's products: 3.92 against 3.90 ms.)  Seven prompts of 1
-// to 1537 tokens with 40 heads: 182 us, of it some 8000 cycles for each of the
-// CTAs to start and end, one on an SM at a time.
+// rest is the part of a stream's softmax that the other's products do not cover,
+// and there every instruction of the product warp between a stream's P and its
+// next S counts: flags of its tiles carried from one item to the next cost 5%, the
+// loop over streams not unrolled 10%.  (A warp for each stream's products: 3.92
+// against 3.90 ms.)  Seven prompts of 1 to 1537 tokens with 40 heads: 165 us.
 #include "softmax_tile.cuh"
 
 namespace pkv {
@@ -33,6 +42,7 @@ namespace {
 constexpr int kStreamWarps = 4;
 constexpr int kCopyWarp = 2 * kStreamWarps, kProductWarp = kCopyWarp + 1;
 constexpr int kThreads = (kProductWarp + 1) * 32;
+constexpr int kTakers = 1 + 2 * kStreamWarps;  // the warps that read an item which the copies' has posted
 constexpr int kRows = 256;               // queries of a CTA
 constexpr int kTile = 128;               // keys
 constexpr int kUnit = kTile * 128;       // bytes of a ring unit
@@ -45,13 +55,48 @@ struct PromptSmem {
     static constexpr int kQ = 0;  // [2 streams][3 parts][128 rows][128 B]
     static constexpr int kKV = kQ + 2 * kKeyUnits * kUnit;
     static constexpr int kBar = kKV + kRing * kUnit;
-    // keys landed[2], values landed[2], keys read[2], values read[2] (by the tile's parity), qfull[2], sfull[2], pfull[2], odone[2]
-    static constexpr int kNumBars = 16;
+    // keys landed[2], values landed[2], keys read[2], values read[2] (by the tile's parity), qfull[2], sfull[2], pfull[2],
+    // odone[2], qempty[2]; ifull, iempty, claim
+    static constexpr int kNumBars = 22;  // (one more keeps what follows 16-byte aligned)
     static constexpr int kAddr = kBar + kNumBars * 8;  // tensor memory address
-    static constexpr int kLost = kAddr + 8;            // [12] keys whose values were taken out, from the first masked tile on
-    static constexpr int kTotal = kLost + kLostTiles * 4 * 4;
-    static_assert(kTotal <= 227 * 1024, "shared memory of one CTA");
+    static constexpr int kItem = kAddr + 16;           // an Item
+    static constexpr int kClaim = kItem + 32;          // the answer to a claim
+    // [3 items in turn][12] keys whose values were taken out, from the first masked tile on
+    static constexpr int kLost = kClaim + 16;
+    static constexpr int kTotal = kLost + 3 * kLostTiles * 4 * 4;
+    static_assert(kTotal <= 227 * 1024 && kBar % 16 == 0 && kClaim % 16 == 0, "shared memory of one CTA");
 };
+
+// Up to 256 queries of a prompt and a head.  Query i attends the first seen0 + i keys.
+struct Item {
+    int row, rows, head, seen0;  // first token in q; rows == 0: no more items
+    int key, keys;               // first token in kv
+    __device__ __forceinline__ int tiles(int x) const {  // of a stream
+        const int n = min(rows, 128 * (x + 1));
+        return n > 128 * x ? max(0, seen0 + n - 1 + kTile - 1) / kTile : 0;
+    }
+};
+
+// Asks for a CTA of this grid that has not begun; the answer, 16 bytes, arrives at `dst` and on `bar`.
+__device__ __forceinline__ void claim_cta(uint32_t dst, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+// Was there one, and its place in the grid.
+__device__ __forceinline__ bool claimed_cta(uint32_t src, dim3& at) {
+    uint32_t got, x, y, z;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%4];\n\t"
+        "mov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, h;\n\t}"
+        : "=&r"(got), "=&r"(x), "=&r"(y), "=&r"(z)
+        : "r"(src)
+        : "memory");
+    at = dim3(x, y, z);
+    return got != 0;
+}
 
 __device__ __forceinline__ void both_streams() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -69,36 +114,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_addr(smem);
     const uint32_t kfull0 = sbase + S::kBar, vfull0 = kfull0 + 16, kread0 = vfull0 + 16, vread0 = kread0 + 16,
-                   qfull0 = vread0 + 16, sfull0 = qfull0 + 16, pfull0 = sfull0 + 16, odone0 = pfull0 + 16;
+                   qfull0 = vread0 + 16, sfull0 = qfull0 + 16, pfull0 = sfull0 + 16, odone0 = pfull0 + 16,
+                   qempty0 = odone0 + 16, ifull = qempty0 + 16, iempty = ifull + 8, claim = iempty + 8;
     uint32_t* lost = reinterpret_cast<uint32_t*>(smem + S::kLost);
-    const int head = blockIdx.y, seq = blockIdx.z;
-    const int q0 = (int)(gridDim.x - 1 - blockIdx.x) * kRows;  // first query of the CTA in its prompt
-
-    pdl_wait();
-    pdl_launch_dependents();
-    const int a0 = p.query_starts[seq], a1 = p.query_starts[seq + 1], b0 = p.key_starts[seq], b1 = p.key_starts[seq + 1];
-    const bool no_rows = a0 < 0 || a1 < a0 || a1 > p.num_queries;
-    const bool bad = !no_rows && (b0 < 0 || b1 < b0 || b1 > p.num_keys || a1 - a0 > p.max_query_len);
-    if ((no_rows || bad) && tid == 0 && head == 0 && q0 == 0) record_error(p.err, PKV_DEVERR_QUERY);
-    if (no_rows) return;
     uint16_t* out = static_cast<uint16_t*>(p.out);
-    const int nq = a1 - a0;
-    if (bad) {  // its rows become zeros, whatever their number
-        for (int64_t i = (int64_t)q0 * 16 + tid; i < (int64_t)nq * 16; i += kThreads) {
-            if (blockIdx.x != gridDim.x - 1 && i >= (int64_t)(q0 + kRows) * 16) break;
-            *reinterpret_cast<uint4*>(out + ((a0 + i / 16) * p.num_heads + head) * 128 + i % 16 * 8) = make_uint4(0, 0, 0, 0);
-        }
-        return;
-    }
-    if (q0 >= nq) return;
-    const int nk = b1 - b0;
-    const int rows = min(kRows, nq - q0);
-    // Query i attends the first i + 1 + nk - nq keys.  Of the CTA: its first row's, and the tiles of each stream.
-    const int seen0 = q0 + 1 + nk - nq;
-    const int tiles_a = max(0, seen0 + min(rows, 128) - 1 + kTile - 1) / kTile;
-    const int tiles_b = rows > 128 ? max(0, seen0 + rows - 1 + kTile - 1) / kTile : 0;
-    const int tiles = max(tiles_a, tiles_b);
-    const int masked = max(0, seen0) / kTile;  // tiles before it hold no key that any row masks
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -110,123 +129,215 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(sfull0 + 8 * i, 1);
             mbar_init(pfull0 + 8 * i, kStreamWarps);
             mbar_init(odone0 + 8 * i, 1);
+            mbar_init(qempty0 + 8 * i, 1);
         }
-        for (int i = 0; i < kLostTiles * 4; ++i) lost[i] = 0;
+        mbar_init(ifull, 1);
+        mbar_init(iempty, kTakers);
+        mbar_init(claim, 1);
+        for (int i = 0; i < 3 * kLostTiles * 4; ++i) lost[i] = 0;
         fence_barrier_init();
     }
     if (warp == kProductWarp) tmem_alloc(sbase + S::kAddr, kTmemCols);
+    pdl_wait();
+    pdl_launch_dependents();
+    // The item at a place in the grid (rows == 0: there is none).  lanes > 0: of so many threads that see to bad metadata.
+    const auto item_at = [&](const dim3& at, int lanes) -> Item {
+        const int seq = at.z, q0 = (int)(gridDim.x - 1 - at.x) * kRows;
+        const int a0 = p.query_starts[seq], a1 = p.query_starts[seq + 1], b0 = p.key_starts[seq], b1 = p.key_starts[seq + 1];
+        const bool no_rows = a0 < 0 || a1 < a0 || a1 > p.num_queries;
+        const bool bad = !no_rows && (b0 < 0 || b1 < b0 || b1 > p.num_keys || a1 - a0 > p.max_query_len);
+        if (lanes > 0 && (no_rows || bad)) {
+            if (lane == 0 && at.y == 0 && q0 == 0) record_error(p.err, PKV_DEVERR_QUERY);
+            // the rows of bad ones become zeros, whatever their number
+            for (int64_t r = q0; !no_rows && r < a1 - a0; r += (int64_t)gridDim.x * kRows)
+                for (int i = lane; i < min((int64_t)kRows, a1 - a0 - r) * 16; i += lanes)
+                    *reinterpret_cast<uint4*>(out + ((a0 + r + i / 16) * p.num_heads + at.y) * 128 + i % 16 * 8) =
+                        make_uint4(0, 0, 0, 0);
+        }
+        if (no_rows || bad || q0 >= a1 - a0) return {0, 0, 0, 0, 0, 0};
+        return {a0 + q0, min(kRows, a1 - a0 - q0), (int)at.y, q0 + 1 + (b1 - b0) - (a1 - a0), b0, b1 - b0};
+    };
+    Item it = item_at(blockIdx, warp == kCopyWarp ? 32 : 0);  // of the CTA's own place
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S::kAddr);
     bool ok = true;  // no wait has run out
+    // The next item, the CTA's own first (a whole warp).
+    uint32_t taken = 0;
+    bool own = __all_sync(0xffffffffu, it.rows > 0);
+    const auto take = [&]() -> bool {
+        if (own) {
+            own = false;
+            return true;
+        }
+        if (!p.claims) return false;
+        // (the copies' lane may be looking through a great many empty places)
+        ok = __all_sync(0xffffffffu, ok && mbar_wait_for(ifull, taken & 1, 32 * kWaitLimitNs));
+        if (!ok) return false;
+        ++taken;
+        const int4 a = *reinterpret_cast<const int4*>(smem + S::kItem);
+        const int2 b = *reinterpret_cast<const int2*>(smem + S::kItem + 16);
+        it = {a.x, a.y, a.z, a.w, b.x, b.y};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(iempty);
+        return __all_sync(0xffffffffu, it.rows > 0);  // (a vote: known to be the same in all lanes)
+    };
 
     if (warp == kCopyWarp) {
         // -------------------------------------------------------------- copies
-        if (lane == 0 && tiles > 0) {
+        if (lane == 0) {
             prefetch_tensormap(&tmq);
             prefetch_tensormap(&tmkv);
             prefetch_tensormap(&tmr);
-            const auto queries = [&](int x) {
-                mbar_arrive_expect_tx(qfull0 + 8 * x, kKeyUnits * kUnit);
-                for (int i = 0; i < kKeyUnits; ++i)
-                    tma_load_3d(sbase + S::kQ + (x * kKeyUnits + i) * kUnit, &tmq, qfull0 + 8 * x, 64 * i, head,
-                                a0 + q0 + 128 * x);
-            };
-            queries(0);
-            int t = 0;
-            for (; t < tiles; ++t) {
-                const int par = t & 1, y = b0 + t * kTile;
-                if (t >= 2) ok = wait_bar(vread0 + 8 * par, (t / 2 - 1) & 1);
-                if (!ok) break;
-                mbar_arrive_expect_tx(kfull0 + 8 * par, kKeyUnits * kUnit);
-                for (int i = 0; i < kKeyUnits; ++i) {
-                    const uint32_t dst = sbase + S::kKV + (t * kTileUnits + i) % kRing * kUnit;
-                    if (i < 2)
-                        tma_load_3d(dst, &tmkv, kfull0 + 8 * par, 64 * i, head, y);
-                    else
-                        tma_load_2d(dst, &tmr, kfull0 + 8 * par, 0, y);
+            uint32_t nq[2] = {0, 0}, nk = 0, nv = 0;  // of each stream's Q, of tiles: those copied
+            uint32_t claims = 0, posted = 0;
+            // The next item: the place of a CTA that has not begun, claimed when the copies of the item before have been
+            // issued, two tiles before its end.
+            const auto claimed = [&]() -> bool {
+                if (own) {
+                    own = false;
+                    return true;
                 }
-                if (t == 0 && tiles_b > 0) queries(1);
-                if (t >= 1) ok = wait_bar(kread0 + 8 * (par ^ 1), ((t - 1) / 2) & 1);
-                if (!ok) break;
-                mbar_arrive_expect_tx(vfull0 + 8 * par, 2 * kUnit);
-                for (int i = 0; i < 2; ++i)
-                    tma_load_3d(sbase + S::kKV + (t * kTileUnits + kKeyUnits + i) % kRing * kUnit, &tmkv, vfull0 + 8 * par,
-                                128 + 64 * i, head, y);
+                if (!p.claims) return false;
+                it = {0, 0, 0, 0, 0, 0};
+                for (bool more = true; more && ok && it.rows == 0;) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive_expect_tx(claim, 16);
+                    claim_cta(sbase + S::kClaim, claim);
+                    ok = wait_bar(claim, claims++ & 1);
+                    dim3 at;
+                    more = ok && claimed_cta(sbase + S::kClaim, at);
+                    if (more) it = item_at(at, 1);
+                }
+                // until the softmax, which may be at the item before, has taken it
+                if (posted > 0) ok = ok && wait_bar(iempty, (posted - 1) & 1);
+                if (!ok) it.rows = 0;  // (the others need not wait for more)
+                *reinterpret_cast<int4*>(smem + S::kItem) = make_int4(it.row, it.rows, it.head, it.seen0);
+                *reinterpret_cast<int2*>(smem + S::kItem + 16) = make_int2(it.key, it.keys);
+                mbar_arrive(ifull);
+                ++posted;
+                return it.rows > 0;
+            };
+            while (claimed()) {
+                const auto queries = [&](int x) {
+                    if (nq[x] > 0) ok = ok && wait_bar(qempty0 + 8 * x, (nq[x] - 1) & 1);
+                    if (!ok) return;
+                    ++nq[x];
+                    mbar_arrive_expect_tx(qfull0 + 8 * x, kKeyUnits * kUnit);
+                    for (int i = 0; i < kKeyUnits; ++i)
+                        tma_load_3d(sbase + S::kQ + (x * kKeyUnits + i) * kUnit, &tmq, qfull0 + 8 * x, 64 * i, it.head,
+                                    it.row + 128 * x);
+                };
+                const int tiles_a = it.tiles(0), tiles_b = it.tiles(1), tiles = max(tiles_a, tiles_b);
+                if (tiles_a > 0) queries(0);
+                for (int t = 0; t < tiles; ++t) {
+                    const uint32_t par = nk & 1;
+                    const int y = it.key + t * kTile;
+                    if (nk >= 2) ok = ok && wait_bar(vread0 + 8 * par, (nk / 2 - 1) & 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(kfull0 + 8 * par, kKeyUnits * kUnit);
+                    for (int i = 0; i < kKeyUnits; ++i) {
+                        const uint32_t dst = sbase + S::kKV + (nk * kTileUnits + i) % kRing * kUnit;
+                        if (i < 2)
+                            tma_load_3d(dst, &tmkv, kfull0 + 8 * par, 64 * i, it.head, y);
+                        else
+                            tma_load_2d(dst, &tmr, kfull0 + 8 * par, 0, y);
+                    }
+                    ++nk;
+                    if (t == 0 && tiles_b > 0) queries(1);
+                    if (nv >= 1) ok = ok && wait_bar(kread0 + 8 * (par ^ 1), ((nv - 1) / 2) & 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(vfull0 + 8 * par, 2 * kUnit);
+                    for (int i = 0; i < 2; ++i)
+                        tma_load_3d(sbase + S::kKV + (nv * kTileUnits + kKeyUnits + i) % kRing * kUnit, &tmkv, vfull0 + 8 * par,
+                                    128 + 64 * i, it.head, y);
+                    ++nv;
+                }
             }
             if (!ok) record_error(p.err, PKV_DEVERR_TIMEOUT);
             // every copy has landed before the CTA ends
-            wait_bar(qfull0, 0);
-            if (tiles_b > 0) wait_bar(qfull0 + 8, 0);
-            for (int i = max(0, t - 2); i < min(tiles, t + 1); ++i) {  // (of a tile that was broken off keys alone)
-                wait_bar(kfull0 + 8 * (i & 1), (i / 2) & 1);
-                if (i < t) wait_bar(vfull0 + 8 * (i & 1), (i / 2) & 1);
-            }
+            for (int x = 0; x < 2; ++x)
+                if (nq[x] > 0) wait_bar(qfull0 + 8 * x, (nq[x] - 1) & 1);
+            for (uint32_t i = max(nk, 2u) - 2; i < nk; ++i) wait_bar(kfull0 + 8 * (i & 1), (i / 2) & 1);
+            for (uint32_t i = max(nv, 2u) - 2; i < nv; ++i) wait_bar(vfull0 + 8 * (i & 1), (i / 2) & 1);
         }
     } else if (warp == kProductWarp) {
         // ------------------------------------------------------------ products
         const uint32_t el = issuing_lane(), tm = __shfl_sync(0xffffffffu, tmem, 0), sb = __shfl_sync(0xffffffffu, sbase, 0);
-        const int ta = __shfl_sync(0xffffffffu, tiles_a, 0), tb = __shfl_sync(0xffffffffu, tiles_b, 0), tn = max(ta, tb);
         const uint32_t id_s = umma_idesc(kBF16, 128, kTile, false, false);
         const uint32_t id_o = umma_idesc(kBF16, 128, 128, false, true), id_h = umma_idesc(kBF16, 128, 64, false, true);
         const uint64_t q_desc = umma_desc_sw128(sb + S::kQ, 16, 1024), k_desc = umma_desc_sw128(sb + S::kKV, 16, 1024),
                        v_desc = umma_desc_sw128(sb + S::kKV, kUnit, 1024);  // + (bytes / 16)
-        int pend_x = -1, pend_t = 0;  // a tile whose second product is still to come
         uint32_t last_bar = 0, last_par = 0;
-        const auto values = [&]() {
-            const uint32_t x = pend_x, t = pend_t, at = (t * kTileUnits + kKeyUnits) % kRing;
-            pend_x = -1;
-            ok = mbar_wait_warp(vfull0 + 8 * (t & 1), (t / 2) & 1) && mbar_wait_warp(pfull0 + 8 * x, t & 1);
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t o = tm + 256 + 128 * x, pp = tm + 128 * x;
-            if (at + 1 < kRing) {
-                const uint64_t vd = v_desc + at * (kUnit / 16);
-#pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks) umma_f16_ts(el, o, pp + 8 * ks, vd + ks * 128, id_o, t > 0 || ks > 0);
-            } else {  // the two halves of the values do not stand together in the ring
-                const uint64_t v0 = k_desc + at * (kUnit / 16), v1 = k_desc;
-#pragma unroll 1
-                for (int ks = 0; ks < kTile / 16; ++ks) {
-                    umma_f16_ts(el, o, pp + 8 * ks, v0 + ks * 128, id_h, t > 0 || ks > 0);
-                    umma_f16_ts(el, o + 64, pp + 8 * ks, v1 + ks * 128, id_h, t > 0 || ks > 0);
-                }
-            }
-            if (x == 1 || t >= (uint32_t)tb) umma_commit(el, vread0 + 8 * (t & 1));  // the last to read it
-            if (t + 1 == (uint32_t)(x ? tb : ta)) {
-                umma_commit(el, odone0 + 8 * x);
-                last_bar = odone0 + 8 * x;
-                last_par = 0;
-            }
-        };
-        for (int t = 0; t < tn && ok; ++t) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (t >= (x ? tb : ta) || !ok) continue;
-                if (pend_x == x) values();  // P of this stream lies where S goes
-                if (ok && t == 0) ok = mbar_wait_warp(qfull0 + 8 * x, 0);
-                ok = ok && mbar_wait_warp(kfull0 + 8 * (t & 1), (t / 2) & 1);
-                if (!ok) break;
+        uint32_t tile0 = 0, par0 = 0, items = 0;  // tiles of the items before; bits of the streams: those of each, their items
+        while (take()) {
+            const int ta = __shfl_sync(0xffffffffu, it.tiles(0), 0), tb = __shfl_sync(0xffffffffu, it.tiles(1), 0),
+                      tn = max(ta, tb);
+            int pend_x = -1, pend_t = 0;  // a tile whose second product is still to come
+            const auto values = [&]() {
+                const uint32_t x = pend_x, t = pend_t, g = tile0 + t, at = (g * kTileUnits + kKeyUnits) % kRing;
+                pend_x = -1;
+                ok = mbar_wait_warp(vfull0 + 8 * (g & 1), (g / 2) & 1) && mbar_wait_warp(pfull0 + 8 * x, (par0 >> x ^ t) & 1);
+                if (!ok) return;
                 tc_fence_after();
+                const uint32_t o = tm + 256 + 128 * x, pp = tm + 128 * x;
+                if (at + 1 < kRing) {
+                    const uint64_t vd = v_desc + at * (kUnit / 16);
 #pragma unroll
-                for (int i = 0; i < kKeyUnits; ++i) {
-                    const uint64_t qd = q_desc + (x * kKeyUnits + i) * (kUnit / 16),
-                                   kd = k_desc + (uint32_t)(t * kTileUnits + i) % kRing * (kUnit / 16);
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        umma_f16_ss(el, tm + 128 * x, qd + 2 * ks, kd + 2 * ks, id_s, i > 0 || ks > 0);
+                    for (int ks = 0; ks < kTile / 16; ++ks) umma_f16_ts(el, o, pp + 8 * ks, vd + ks * 128, id_o, t > 0 || ks > 0);
+                } else {  // the two halves of the values do not stand together in the ring
+                    const uint64_t v0 = k_desc + at * (kUnit / 16), v1 = k_desc;
+#pragma unroll 1
+                    for (int ks = 0; ks < kTile / 16; ++ks) {
+                        umma_f16_ts(el, o, pp + 8 * ks, v0 + ks * 128, id_h, t > 0 || ks > 0);
+                        umma_f16_ts(el, o + 64, pp + 8 * ks, v1 + ks * 128, id_h, t > 0 || ks > 0);
+                    }
                 }
-                if (x == 1 || t >= tb) umma_commit(el, kread0 + 8 * (t & 1));  // the last to read it
-                umma_commit(el, sfull0 + 8 * x);
-                last_bar = sfull0 + 8 * x;
-                last_par = t & 1;
-                if (pend_x >= 0) values();
-                pend_x = x;
-                pend_t = t;
+                if (x == 1 || t >= (uint32_t)tb) umma_commit(el, vread0 + 8 * (g & 1));  // the last to read it
+                if (t + 1 == (uint32_t)(x ? tb : ta)) {
+                    umma_commit(el, odone0 + 8 * x);
+                    last_bar = odone0 + 8 * x;
+                    last_par = items >> x & 1;
+                }
+            };
+            for (int t = 0; t < tn && ok; ++t) {
+                const uint32_t g = tile0 + t;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (t >= (x ? tb : ta) || !ok) continue;
+                    if (pend_x == x) values();  // P of this stream lies where S goes
+                    if (ok && t == 0) ok = mbar_wait_warp(qfull0 + 8 * x, items >> x & 1);
+                    ok = ok && mbar_wait_warp(kfull0 + 8 * (g & 1), (g / 2) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < kKeyUnits; ++i) {
+                        const uint64_t qd = q_desc + (x * kKeyUnits + i) * (kUnit / 16),
+                                       kd = k_desc + (g * kTileUnits + i) % kRing * (kUnit / 16);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_f16_ss(el, tm + 128 * x, qd + 2 * ks, kd + 2 * ks, id_s, i > 0 || ks > 0);
+                    }
+                    if (x == 1 || t >= tb) umma_commit(el, kread0 + 8 * (g & 1));  // the last to read it
+                    umma_commit(el, sfull0 + 8 * x);
+                    last_bar = sfull0 + 8 * x;
+                    last_par = (par0 >> x ^ t) & 1;
+                    if (pend_x >= 0) values();
+                    pend_x = x;
+                    pend_t = t;
+                }
             }
+            if (!ok) break;
+            // every Q K has been issued: the queries may be replaced when they have ended
+            if (ta > 0) umma_commit(el, qempty0);
+            if (tb > 0) umma_commit(el, qempty0 + 8);
+            if (pend_x >= 0) values();
+            if (!ok) break;
+            tile0 += tn;
+            par0 ^= (ta & 1) | (tb & 1) << 1;
+            items ^= (ta > 0) | (tb > 0) << 1;
         }
-        if (ok && pend_x >= 0) values();
         if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
         // every product that was issued has ended before tensor memory is given back
         if (last_bar) wait_bar(last_bar, last_par);
@@ -235,81 +346,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int X = warp >> 2, r = tid & 127, row = 128 * X + r;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t s_addr = lane_addr + 128 * X, o_addr = lane_addr + 256 + 128 * X;
-        const int mine = X ? tiles_b : tiles_a;
-        const int mine_masked = max(0, seen0 + 128 * X) / kTile;  // tiles before it: no row of the stream masks a key
-        const int seen = min(nk, seen0 + row);  // keys that this row attends (rows past the prompt's end: whatever)
-        const bool live = 128 * X + 32 * (warp & 3) < rows;
-        // (a lane without a row, whose scores are anything, never asks for a raise)
-        float m_run = row < rows ? -INFINITY : INFINITY, l = 0.f;
-        for (int t = 0; t < mine; ++t) {
-            const bool shared = t < tiles_a && t < tiles_b;
-            const bool guard = t >= masked;
-            ok = ok && wait_bar(sfull0 + 8 * X, t & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (live && ok) {
-                tc_fence_after();
-                softmax_tile<kBF16>(s_addr, o_addr, t >= mine_masked, p.scale_log2, t > 0, m_run, l,
-                                    [&](int c) { return before(t * kTile + c, seen); });
-                tc_fence_before();
-            }
-            if (guard) {
-                const int u = t * kTileUnits + kKeyUnits;
-                ok = ok && wait_bar(vfull0 + 8 * (t & 1), (t / 2) & 1);
+        uint32_t items = 0, tile0 = 0, ns = 0, no = 0;  // items, and their tiles; of this stream: tiles, items
+        while (take()) {
+            const int tiles_a = it.tiles(0), tiles_b = it.tiles(1), mine = X ? tiles_b : tiles_a;
+            const int masked = max(0, it.seen0) / kTile;  // tiles before it hold no key that any row masks
+            const int mine_masked = max(0, it.seen0 + 128 * X) / kTile;  // ... that any row of the stream masks
+            const int seen = min(it.keys, it.seen0 + row);  // keys that this row attends (rows past the prompt's end: whatever)
+            const bool live = 128 * X + 32 * (warp & 3) < it.rows;
+            uint32_t* mine_lost = lost + items % 3 * (kLostTiles * 4);
+            // (a lane without a row, whose scores are anything, never asks for a raise)
+            float m_run = row < it.rows ? -INFINITY : INFINITY, l = 0.f;
+            for (int t = 0; t < mine; ++t) {
+                const bool shared = t < tiles_a && t < tiles_b;
+                const bool guard = t >= masked;
+                ok = ok && wait_bar(sfull0 + 8 * X, ns & 1);
                 ok = __all_sync(0xffffffffu, ok);
-                if (ok) {
-                    // this thread's key: its values past the prompt become zeros, and those not finite are taken out;
-                    // where both streams use the tile each sees to half of it
-                    const int key = shared ? 64 * X + (r >> 1) : r, pos = t * kTile + key;
-                    const int h0 = shared ? r & 1 : 0;
-                    const auto at = [&](int i) {  // (neighbouring threads start at different eighths of 128 bytes)
-                        return reinterpret_cast<uint4*>(smem + S::kKV + ((u + h0 + (i >> 3)) % kRing) * kUnit + key * 128) +
-                               ((i + key) & 7);
-                    };
-                    if (scrub<kBF16>(shared ? 8 : 16, pos < nk, at)) atomicOr(lost + (pos - masked * kTile) / 32, 1u << (pos & 31));
+                ++ns;
+                if (live && ok) {
+                    tc_fence_after();
+                    softmax_tile<kBF16>(s_addr, o_addr, t >= mine_masked, p.scale_log2, t > 0, m_run, l,
+                                        [&](int c) { return before(t * kTile + c, seen); });
+                    tc_fence_before();
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                if (shared) both_streams();
-            }
-            if (!ok) continue;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pfull0 + 8 * X);
-        }
-        both_streams();  // (what was taken out is known)
-        if (mine > 0) ok = __all_sync(0xffffffffu, ok && wait_bar(odone0 + 8 * X, 0));
-        tc_fence_after();
-        const float inv = ok && l != 0.f ? 1.f / l : 0.f;
-        uint16_t* dst = out + ((int64_t)(a0 + q0 + row) * p.num_heads + head) * 128;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-            float o[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            if (live && ok && mine > 0) {
-                tmem_ld32_start(o_addr + 32 * c, o);
-                tmem_ld_wait32(o);
-            }
-            if (row >= rows) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = inv != 0.f ? pack2<kBF16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv) : 0u;
-                *reinterpret_cast<uint4*>(dst + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-        if (row < rows && ok) {
-            // values that are not finite and were left out of the products
-#pragma unroll 1
-            for (int w = 0; w < kLostTiles * 4; ++w)
-                for (uint32_t at = lost[w]; at; at &= at - 1) {
-                    const int pos = masked * kTile + 32 * w + __ffs(at) - 1;
-                    if (pos < seen)
-                        add_not_finite<kBF16>(nullptr, dst,
-                                              static_cast<const uint16_t*>(p.values) + (b0 + pos) * p.kv_stride +
-                                                  head * p.kv_head_stride + 128,
-                                              128);
+                if (guard) {
+                    const uint32_t tile = tile0 + t, u = tile * kTileUnits + kKeyUnits;
+                    ok = ok && wait_bar(vfull0 + 8 * (tile & 1), (tile / 2) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok) {
+                        // this thread's key: its values past the prompt become zeros, and those not finite are taken out;
+                        // where both streams use the tile each sees to half of it
+                        const int key = shared ? 64 * X + (r >> 1) : r, pos = t * kTile + key;
+                        const int h0 = shared ? r & 1 : 0;
+                        const auto at = [&](int i) {  // (neighbouring threads start at different eighths of 128 bytes)
+                            return reinterpret_cast<uint4*>(smem + S::kKV + ((u + h0 + (i >> 3)) % kRing) * kUnit + key * 128) +
+                                   ((i + key) & 7);
+                        };
+                        if (scrub<kBF16>(shared ? 8 : 16, pos < it.keys, at))
+                            atomicOr(mine_lost + (pos - masked * kTile) / 32, 1u << (pos & 31));
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if (shared) both_streams();
                 }
+                if (!ok) continue;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull0 + 8 * X);
+            }
+            // (read last before the barrier of the item before)
+            if (tid < kLostTiles * 4) lost[(items + 1) % 3 * (kLostTiles * 4) + tid] = 0;
+            both_streams();  // (what was taken out is known)
+            if (mine > 0) ok = __all_sync(0xffffffffu, ok && wait_bar(odone0 + 8 * X, no & 1));
+            no += mine > 0;
+            tc_fence_after();
+            const float inv = ok && l != 0.f ? 1.f / l : 0.f;
+            uint16_t* dst = out + ((int64_t)(it.row + row) * p.num_heads + it.head) * 128;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float o[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                if (live && ok && mine > 0) {
+                    tmem_ld32_start(o_addr + 32 * c, o);
+                    tmem_ld_wait32(o);
+                }
+                if (row >= it.rows) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = inv != 0.f ? pack2<kBF16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv) : 0u;
+                    *reinterpret_cast<uint4*>(dst + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            tc_fence_before();
+            if (row < it.rows && ok) {
+                // values that are not finite and were left out of the products
+#pragma unroll 1
+                for (int w = 0; w < kLostTiles * 4; ++w)
+                    for (uint32_t at = mine_lost[w]; at; at &= at - 1) {
+                        const int pos = masked * kTile + 32 * w + __ffs(at) - 1;
+                        if (pos < seen)
+                            add_not_finite<kBF16>(nullptr, dst,
+                                                  static_cast<const uint16_t*>(p.values) + (it.key + pos) * p.kv_stride +
+                                                      it.head * p.kv_head_stride + 128,
+                                                  128);
+                    }
+            }
+            ++items;
+            tile0 += max(tiles_a, tiles_b);
         }
         if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
     }
@@ -321,12 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_latent_prompt(const LatentPromptParams& p, int dtype, const CUtensorMap& tmq, const CUtensorMap& tmkv,
+cudaError_t launch_latent_prompt(const LatentPromptParams& in, int dtype, const CUtensorMap& tmq, const CUtensorMap& tmkv,
                                  const CUtensorMap& tmr, cudaStream_t stream, int* launches) {
     auto kern = dtype == PKV_BF16 ? latent_prompt_kernel<true> : latent_prompt_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem::kTotal);
     if (e != cudaSuccess) return e;
-    const dim3 grid((p.max_query_len + kRows - 1) / kRows, p.num_heads, p.num_seqs);
+    const dim3 grid((in.max_query_len + kRows - 1) / kRows, in.num_heads, in.num_seqs);
+    LatentPromptParams p = in;
+    p.claims = (int64_t)grid.x * grid.y > (p.sms - 1) / (int64_t)grid.z;  // (more than one CTA an SM)
     e = launch_pdl(kern, grid, dim3(kThreads), PromptSmem::kTotal, stream, tmq, tmkv, tmr, p);
     if (e == cudaSuccess) ++*launches;
     return e;

@@ -216,6 +216,8 @@ struct LatentPromptParams {
     int num_seqs, num_heads;
     int num_queries, num_keys;   // tokens of q; of kv and k_rope
     int max_query_len;
+    int sms;
+    bool claims;                 // CTAs take the places of others that have not begun
     float scale_log2;
 };
 cudaError_t launch_latent_prompt(const LatentPromptParams& p, int dtype, const CUtensorMap& tmq, const CUtensorMap& tmkv,

@@ -342,6 +342,61 @@ def test_prompt_bad_metadata(gpu):
     p.check(only=[0, 1])
 
 
+MANY = [(5, 5), (0, 0), (300, 300), (1, 1), (0, 40), (129, 400), (700, 200), (257, 257), (3, 0), (64, 64), (900, 1500), (256, 256)]
+
+
+@pytest.mark.parametrize("heads,dtype,slices", [(48, BF, False), (33, FP, True), (128, BF, True)])
+def test_more_prompts_than_ctas(gpu, heads, dtype, slices):
+    """Grids of many times the SMs, most of whose places are empty or short, with and without a bound of the lengths."""
+    p = Prompts(9, MANY, heads, dtype, extra=3, slices=slices, gap=4)
+    p.check(run(p))
+    p.out.fill_(SENTINEL)
+    p.check(run(p, max_query_len=None))
+
+
+def test_more_prompts_than_ctas_with_bad_metadata(gpu):
+    make = lambda: Prompts(10, MANY, 48, BF, extra=2)
+    p = make()
+    run(p, expect=10, max_query_len=299)
+    p.check(zeros=[2, 6, 10])
+    p = make()
+    p.ks[9] = -5
+    run(p, expect=10)
+    p.check(zeros=[8, 9])
+    p = make()
+    p.qs[5] = 1 << 30
+    run(p, expect=10)
+    p.check(only=[0, 1, 2, 3, 6, 7, 8, 9, 10, 11])
+    assert (p.out[p.qs_list[5]:p.qs_list[6]] == SENTINEL).all()
+
+
+def test_many_prompts_at_once(gpu):
+    """Two streams and a graph whose grids are larger than the SMs."""
+    ps = [Prompts(11 + i, [(700 + i, 800), (40, 40), (600, 600)], 64, BF) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for p, s in zip(ps, streams):
+            p.call(stream=s)
+    torch.cuda.synchronize()
+    assert pkv.check_device_error() == 0
+    for p in ps:
+        p.check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for p in ps:
+            p.call()
+    for p in ps:
+        p.q.copy_(torch.randn_like(p.q))
+        p.out.fill_(SENTINEL)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert pkv.check_device_error() == 0
+    for p in ps:
+        p.check()
+
+
 def test_prompts_on_streams_and_in_graphs(gpu):
     ps = [Prompts(8 + i, [(500 + i, 600), (40, 40)], 4, BF) for i in range(2)]
     streams = [torch.cuda.Stream() for _ in ps]
