@@ -27,7 +27,7 @@
 // most claim nothing.
 //
 // What bounds it: two prompts of 8192 tokens with 128 heads (5.5 TFLOP) take 3.77
-// to 3.8 ms, 1.46 PFLOP/s, 76% of the card's peak and 83% of what it sustains
+// to 3.85 ms, 1.45 PFLOP/s, 75% of the card's peak and 82% of what it sustains
 // under its power limit.  Without the softmax the products alone take 3.6 ms; the
 // rest is the part of a stream's softmax that the other's products do not cover,
 // and there every instruction of the product warp between a stream's P and its

@@ -1,6 +1,7 @@
 // marshal.cpp -- argument marshalling of the calls on rotated rows, 8-bit
-// pools, drafted tokens and latent caches, for binding.py: checks of the tensors, the C ABI's descriptors and
-// pointers, the outputs that the caller did not give, and the current stream.
+// pools, drafted tokens and latent caches, for binding.py: checks of the
+// tensors, the C ABI's descriptors and pointers, the outputs that the caller did
+// not give, and the current stream.
 // A step of a few short sequences takes the GPU 2 to 6 us; the same checks in
 // Python took the host 9 to 18 us, and 52 us for the caches of 40 layers.
 //

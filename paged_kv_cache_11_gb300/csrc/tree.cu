@@ -41,16 +41,18 @@
 //
 // What bounds it.  Copies alone (the same kernel without products and softmax)
 // run at 7.0 TB/s.  8 documents of 131072 tokens, 64/8 heads, 31 drafted tokens
-// (4.3 GB): 900-940 us, 4.7 TB/s, 1.2 PFLOP/s, bound by the chain of a stream's
-// tile, Q K, softmax, P V, of some 4200 cycles in which two tiles of rows are
+// (4.3 GB): 880-925 us, 4.8 TB/s, 1.2 PFLOP/s, bound by the chain of a stream's
+// tile, Q K, softmax, P V, of some 4100 cycles in which two tiles of rows are
 // worked off (the copies' pace is 2800; without the softmax 775 us).  64
-// contexts of 512 to 4096, 32/8 heads, 16 tokens (606 MB): 131-139 us, 4.5
+// contexts of 512 to 4096, 32/8 heads, 16 tokens (606 MB): 128-134 us, 4.6
 // TB/s; 128 of up to 2048, 40 heads without sharing, 1 to 5 tokens (2.7 GB):
-// 620-690 us, 4.1 TB/s: there the ends of units, when the last tile's softmax,
+// 620 us, 4.4 TB/s: there the ends of units, when the last tile's softmax,
 // product and output follow one another and the ring runs full, are what is
 // left.  Tried and not kept: output by four warps of its own (they were as long
 // as the chain they took over), twice the softmax warps, a loop for the
-// products, the weights in one pass (softmax_tile.cuh).
+// products, the weights in one pass (softmax_tile.cuh), the first Q K of a unit
+// before the last P V of the one before (what has to be remembered of a tile from
+// one unit to the next costs more in every tile: 138 for 132 us).
 #include "drafted.cuh"
 #include "softmax_tile.cuh"
 
@@ -182,47 +184,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t id_s = umma_idesc(kBF16, 128, kTile, false, false), id_o = umma_idesc(kBF16, 128, D, false, true);
         const uint64_t q_desc = umma_desc_sw128(sb + S::kQ, 16, 1024), k_desc = umma_desc_sw128(sb + S::kKV, 16, 2048),
                        v_desc = umma_desc_sw128(sb + S::kKV, 1024, 2048);  // + (bytes / 16)
-        uint32_t nq[2] = {0, 0}, nsc[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};  // of each stream: units begun, Q K, P V, units ended
-        // the tile whose P V is still to come: QK of the next tile goes first, so that the tensor core has
-        // work while the softmax has its turn
-        int pend_x = -1;
-        uint32_t pend_k = 0, pend_first = 0, pend_frees = 0, pend_last = 0;
         uint32_t last_bar = 0, last_par = 0;
-        uint32_t kk = 0;  // buffers so far
-        const auto values = [&]() {
-            const uint32_t x = pend_x, pb = pend_k % kRing;
-            pend_x = -1;
-            ok = mbar_wait_warp(pfull0 + 8 * x, np[x] & 1);  // (the softmax has waited for V)
-            if (!ok) return;
-            tc_fence_after();
-            const uint64_t vd = v_desc + pb * (kBuf / 16);
-#pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-                umma_f16_ts(el, tm + 256 + 128 * x, tm + 128 * x + 8 * ks, vd + ks * 256, id_o, !pend_first || ks > 0);
-            if (pend_frees) umma_commit(el, empty0 + 8 * pb);
-            if (pend_last) {
-                umma_commit(el, odone0 + 8 * x);
-                last_bar = odone0 + 8 * x;
-                last_par = no[x]++ & 1;
-            }
-            ++np[x];
-        };
+        uint32_t tile0 = 0, par0 = 0, units = 0;  // tiles so far; bits of the streams: their tiles, their units
         for (;;) {
             const bool more = cur.next(p, it);
             const int n = __shfl_sync(0xffffffffu, more && ok ? it.t1 - it.t0 : 0, 0);
             const bool two = __shfl_sync(0xffffffffu, it.rows, 0) > 128;
             if (n == 0) break;
-            bool begun[2] = {false, false};
-            for (int t = 0; t < n && ok; ++t, kk += 2) {
-                const uint32_t kb = kk % kRing;
+            const int sh = two ? 0 : 1;  // a stream's tile t of the unit is its (t >> sh)-th
+            // the tile whose P V is still to come: QK of the next tile goes first, so that the tensor core has
+            // work while the softmax has its turn
+            int pend_x = -1, pend_t = 0;
+            const auto values = [&]() {
+                const uint32_t x = pend_x, t = pend_t, pb = (2 * (tile0 + t) + 1) % kRing;
+                pend_x = -1;
+                ok = mbar_wait_warp(pfull0 + 8 * x, (par0 >> x ^ t >> sh) & 1);  // (the softmax has waited for V)
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t vd = v_desc + pb * (kBuf / 16);
+#pragma unroll
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                    umma_f16_ts(el, tm + 256 + 128 * x, tm + 128 * x + 8 * ks, vd + ks * 256, id_o, t >> sh > 0 || ks > 0);
+                if (!two || x == 1) umma_commit(el, empty0 + 8 * pb);
+                if ((int)t + 1 + sh >= n) {  // the stream's last of the unit
+                    umma_commit(el, odone0 + 8 * x);
+                    last_bar = odone0 + 8 * x;
+                    last_par = units >> x & 1;
+                }
+            };
+            for (int t = 0; t < n && ok; ++t) {
+                const uint32_t kk = 2 * (tile0 + t), kb = kk % kRing;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (!two && x != (kk >> 1 & 1)) continue;
                     if (pend_x == x && ok) values();  // P of this stream lies where S goes
-                    if (!begun[x] && ok) {
-                        ok = mbar_wait_warp(qfull0 + 8 * x, nq[x] & 1);
-                        ++nq[x];
-                    }
+                    if (t >> sh == 0 && ok) ok = mbar_wait_warp(qfull0 + 8 * x, units >> x & 1);
                     ok = ok && mbar_wait_warp(full0 + 8 * kb, (kk / kRing) & 1);
                     if (!ok) break;
                     tc_fence_after();
@@ -232,22 +228,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma_f16_ss(el, tm + 128 * x, qd + (ks >> 2) * 1024 + (ks & 3) * 2, kd + (ks >> 2) * 64 + (ks & 3) * 2,
                                     id_s, ks > 0);
                     if (!two || x == 1) umma_commit(el, empty0 + 8 * kb);
-                    const bool last = t + (two ? 1 : 2) >= n;  // the stream's last of the unit
-                    if (last) umma_commit(el, qempty0 + 8 * x);
                     umma_commit(el, sfull0 + 8 * x);
                     last_bar = sfull0 + 8 * x;
-                    last_par = nsc[x]++ & 1;
+                    last_par = (par0 >> x ^ t >> sh) & 1;
                     if (pend_x >= 0) values();
                     pend_x = x;
-                    pend_k = kk + 1;
-                    pend_first = !begun[x];
-                    pend_frees = !two || x == 1;
-                    pend_last = last;
-                    begun[x] = true;
+                    pend_t = t;
                 }
             }
+            if (!ok) break;
+            // tiles of each stream
+            const int x1 = tile0 & 1, c0 = two ? n : (n + 1 - x1) >> 1, c1 = two ? n : (n + x1) >> 1;
+            // every Q K has been issued: the queries may be replaced when they have ended
+            if (c0 > 0) umma_commit(el, qempty0);
+            if (c1 > 0) umma_commit(el, qempty0 + 8);
+            values();
+            tile0 += n;
+            par0 ^= (c0 & 1) | (c1 & 1) << 1;
+            units ^= (c0 > 0) | (c1 > 0) << 1;
         }
-        if (ok && pend_x >= 0) values();
         if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT);
         // every product that was issued has ended before tensor memory is given back
         if (last_bar) wait_bar(last_bar, last_par);
