@@ -105,6 +105,18 @@ __device__ __forceinline__ uint32_t before(int c, int seen) {
     return seen - c >= 32 ? ~0u : seen > c ? (1u << (seen - c)) - 1 : 0u;
 }
 
+// The rows of a prompt with bad metadata become zeros, whatever their number: a head's, from query q0 on, 256 for each place in
+// the grid's first dimension.
+__device__ __noinline__ void zero_prompt(const LatentPromptParams& p, int a0, int a1, int q0, int head, int lane, int lanes) {
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    for (int64_t r = q0; r < a1 - a0; r += (int64_t)gridDim.x * kRows)
+        for (int i = lane; i < min((int64_t)kRows, a1 - a0 - r) * 16; i += lanes)
+            *reinterpret_cast<uint4*>(out + ((a0 + r + i / 16) * p.num_heads + head) * 128 + i % 16 * 8) = make_uint4(0, 0, 0, 0);
+}
+
+// The wait for an item: the copies' lane may be looking through a great many empty places.
+__device__ __noinline__ bool wait_item(uint32_t bar, uint32_t parity) { return mbar_wait_for(bar, parity, 32 * kWaitLimitNs); }
+
 template <bool kBF16>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmkv,
@@ -137,6 +149,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 3 * kLostTiles * 4; ++i) lost[i] = 0;
         fence_barrier_init();
     }
+    if (warp == kCopyWarp && lane == 0) {
+        prefetch_tensormap(&tmq);
+        prefetch_tensormap(&tmkv);
+        prefetch_tensormap(&tmr);
+    }
     if (warp == kProductWarp) tmem_alloc(sbase + S::kAddr, kTmemCols);
     pdl_wait();
     pdl_launch_dependents();
@@ -148,11 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool bad = !no_rows && (b0 < 0 || b1 < b0 || b1 > p.num_keys || a1 - a0 > p.max_query_len);
         if (lanes > 0 && (no_rows || bad)) {
             if (lane == 0 && at.y == 0 && q0 == 0) record_error(p.err, PKV_DEVERR_QUERY);
-            // the rows of bad ones become zeros, whatever their number
-            for (int64_t r = q0; !no_rows && r < a1 - a0; r += (int64_t)gridDim.x * kRows)
-                for (int i = lane; i < min((int64_t)kRows, a1 - a0 - r) * 16; i += lanes)
-                    *reinterpret_cast<uint4*>(out + ((a0 + r + i / 16) * p.num_heads + at.y) * 128 + i % 16 * 8) =
-                        make_uint4(0, 0, 0, 0);
+            if (bad) zero_prompt(p, a0, a1, q0, at.y, lane, lanes);
         }
         if (no_rows || bad || q0 >= a1 - a0) return {0, 0, 0, 0, 0, 0};
         return {a0 + q0, min(kRows, a1 - a0 - q0), (int)at.y, q0 + 1 + (b1 - b0) - (a1 - a0), b0, b1 - b0};
@@ -172,8 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         }
         if (!p.claims) return false;
-        // (the copies' lane may be looking through a great many empty places)
-        ok = __all_sync(0xffffffffu, ok && mbar_wait_for(ifull, taken & 1, 32 * kWaitLimitNs));
+        ok = __all_sync(0xffffffffu, ok && wait_item(ifull, taken & 1));
         if (!ok) return false;
         ++taken;
         const int4 a = *reinterpret_cast<const int4*>(smem + S::kItem);
@@ -187,9 +199,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCopyWarp) {
         // -------------------------------------------------------------- copies
         if (lane == 0) {
-            prefetch_tensormap(&tmq);
-            prefetch_tensormap(&tmkv);
-            prefetch_tensormap(&tmr);
             uint32_t nq[2] = {0, 0}, nk = 0, nv = 0;  // of each stream's Q, of tiles: those copied
             uint32_t claims = 0, posted = 0;
             // The next item: the place of a CTA that has not begun, claimed when the copies of the item before have been
