@@ -37,10 +37,10 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-// Products (A in shared or tensor memory, B in shared memory) from a whole warp that stays together: `el` is set in the one lane that issues (issuing_lane, the same all
-// along), the operands are the same in all lanes.  In code that one lane runs alone each product costs some 45 cycles to
-// issue, its descriptors being moved to uniform registers one by one; so it costs 20, and products of 64 x 64 x 16 run at
-// the 32 cycles that the tensor core needs.
+// Products (A in shared or tensor memory, B in shared memory) from a whole warp that stays together: `el` is set in the one
+// lane that issues (issuing_lane, the same all along), the operands are the same in all lanes.  In code that one lane runs
+// alone each product costs some 45 cycles to issue, its descriptors being moved to uniform registers one by one; so it costs
+// 20, and products of 64 x 64 x 16 run at the 32 cycles that the tensor core needs.
 __device__ __forceinline__ uint32_t issuing_lane() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
