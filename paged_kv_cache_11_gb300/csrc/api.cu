@@ -934,13 +934,9 @@ pkv_status paged_latent_decode(const void* q, const void* latent_cache, const in
         st = encode_map(&tmc, latent_cache, cache->dtype, 4, dims, strides, box);
         if (st != PKV_OK) return st;
     }
-    // More than 64 query rows a sequence (of the batch's average): pairs of CTAs share what they read, and the line's pieces
-    // are theirs.  (Workspaces are sized for as many rows in all.)
-    const int pairs = rows > (__int128)kLatentRows * num_seqs ? latent_pairs() : 0;
-    if (pairs > 0) p.pieces = std::min(pairs, p.pieces / 2);
     int launches = 0;
     const cudaError_t e =
-        launch_latent_decode(p, cache->dtype, cache->block_size, pairs > 0, tmq, tmc, static_cast<cudaStream_t>(stream), &launches);
+        launch_latent_decode(p, cache->dtype, cache->block_size, tmq, tmc, static_cast<cudaStream_t>(stream), &launches);
     g_launches += launches;
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

@@ -147,8 +147,7 @@ cudaError_t launch_draft_merge(const DraftParams& p, int dtype, int value_dims, 
     const int64_t units = p.num_seqs * (int64_t)p.num_kv_heads * ((rows + unit_rows - 1) / unit_rows);
     const bool few = units * 16 < 2 * p.pieces, bf16 = dtype == PKV_BF16;
     const cudaError_t e = value_dims == 128 ? launch_merge_t<128, kTreeRows>(p, bf16, few, stream)
-                          : unit_rows == kLatentRows ? launch_merge_t<512, kLatentRows>(p, bf16, few, stream)
-                                                     : launch_merge_t<512, 2 * kLatentRows>(p, bf16, few, stream);
+                                               : launch_merge_t<512, kLatentRows>(p, bf16, few, stream);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

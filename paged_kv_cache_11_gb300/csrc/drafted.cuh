@@ -39,7 +39,7 @@ struct DraftParams {
     int group;                    // query heads of a KV head
     int max_blocks_per_seq;
     int len_limit;                // max_blocks_per_seq * block_size
-    int pieces;                   // of the line: CTAs of the grid, or clusters
+    int pieces;                   // of the line: CTAs of the grid
     float scale_log2;             // scale * log2(e)
 };
 
@@ -157,7 +157,7 @@ __device__ __forceinline__ void zero_rows(const DraftParams& p, int tok0, int n,
 }
 
 // Deals the line and starts `cur` on piece piece_id of it; every thread of the
-// CTA (and every CTA of a cluster) calls it and gets the same piece.  A piece is the line's
+// CTA calls it and gets the same piece.  A piece is the line's
 // length over the CTAs, and kLeast tiles at least (or the longest unit, where
 // that is shorter): a smaller one costs more in starting and merging than it
 // spreads.  Where no unit is longer than that and each can have a CTA of its
@@ -270,10 +270,9 @@ cudaError_t launch_tree(const DraftParams& p, int dtype, int block_size, const C
                         cudaStream_t stream, int* launches);
 constexpr int kTreeRows = 256;   // query rows of a unit
 // latent.cu
-cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size, bool pairs, const CUtensorMap& tmq,
-                                 const CUtensorMap& tmc, cudaStream_t stream, int* launches);
-constexpr int kLatentRows = 64;   // of a CTA; a pair of CTAs takes units of twice as many
-int latent_pairs();               // pairs of CTAs that the current device holds at once (0: not known)
+cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size, const CUtensorMap& tmq, const CUtensorMap& tmc,
+                                 cudaStream_t stream, int* launches);
+constexpr int kLatentRows = 64;  // query rows of a unit
 
 // The position bits that a query row attends among its sequence's drafted tokens.
 __device__ __forceinline__ uint64_t draft_mask(const DraftParams& p, const DraftSeq& q, int token) {

@@ -6,7 +6,8 @@
 //
 // Bytes against operations: a token's row is read once (1152 bytes) for 2 (576
 // + 512) operations of every query row, 121 operations a byte at the 64 rows of
-// a CTA here, where the card has 288.
+// a unit, where the card has 288.  A sequence of more rows is walked once for
+// every 64 of them.
 //
 // The sums of 64 rows x 512 values are 256 columns of tensor memory when the
 // values are the lanes, so the second product is transposed; the first is not,
@@ -32,22 +33,18 @@
 // added to, and values that are not finite are kept out of the products of
 // tiles with masks, as there.
 //
-// Batches of more than 64 query rows a sequence go to pairs of CTAs (clusters of
-// two): each has half of a unit's rows, and they take turns at copying, each
-// slot into both CTAs' rings, so that a row leaves L2 once for 128 query rows.
-//
 // What bounds it.  A tile costs the tensor core 36 x 32 + 16 x 48 cycles (the
 // latter by shared memory reads, 128 bytes a cycle), 1920 in all; its copy 3200
 // at the memory's pace.  The ring holds two tiles, and a tile is held from its
 // copy to its last product, so the latencies of both (copy 1700 cycles, softmax
 // 1000) add up to some 3750 cycles a tile.  8 contexts of 131072 tokens, 16
 // heads, 1 to 4 drafted tokens (1.2 GB): 236 us, 5.1 TB/s, 13 us of it the
-// merge; 64 of 512 to 4096 with 128 heads (190 MB): 92 us, 450 TFLOP/s, of it 13
-// the merge of 36 MB of divided sums, and two or three outputs of 3 us a CTA;
-// without pairs 97.  Tiles of 32 keys, four in the ring, were slower (269, 103):
-// products with N = 32 take 34 cycles to issue and not 16.
-#include <atomic>
-
+// merge; 64 of 512 to 4096 with 128 heads (190 MB): 96 us, 430 TFLOP/s, of it 13
+// the merge of 36 MB of divided sums, and two or three outputs of 3 us a CTA.
+// Tiles of 32 keys, four in the ring, were slower (269, 103): products with N =
+// 32 take 34 cycles to issue and not 16.  (Pairs of CTAs that copied each row
+// into both rings at once took 92 us for the 96; such copies are not used here,
+// since nothing keeps them to memory of this GPU.)
 #include "drafted.cuh"
 #include "softmax_tile.cuh"
 
@@ -108,24 +105,11 @@ __device__ __forceinline__ bool softmax_any(bool mine) {
     return r != 0;
 }
 
-__device__ __forceinline__ int cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return (int)r;
-}
-// Every thread of both CTAs of the cluster.
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// kPair: the CTA is one of a cluster of two that share a unit of 128 rows.
-template <bool kBF16, int BS, bool kPair>
+template <bool kBF16, int BS>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmc, const DraftParams p) {
     using S = LatentSmem;
-    constexpr int kUnitRows = kPair ? 2 * kLatentRows : kLatentRows;
-    using Cursor = DraftCursor<kUnitRows, kTile>;
-    const int rank = kPair ? cluster_rank() : 0, piece = kPair ? blockIdx.x / 2 : blockIdx.x;
+    using Cursor = DraftCursor<kLatentRows, kTile>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_addr(smem);
@@ -137,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(full0 + 8 * i, 1);
-            mbar_init(empty0 + 8 * i, kPair ? 2 : 1);  // (a slot is filled in both CTAs at once)
+            mbar_init(empty0 + 8 * i, 1);
         }
         mbar_init(sfull0, 1);
         mbar_init(sfull0 + 8, 1);
@@ -156,39 +140,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProductWarp) tmem_alloc(sbase + S::kAddr, kTmemCols);
     pdl_wait();
     pdl_launch_dependents();  // (the merge kernel waits for this one's end)
-    if (tid == 0 && rank == 0) {  // no partials yet
-        p.part_desc[piece * 4] = make_int4(0, 0, 0, 0);
-        p.part_desc[piece * 4 + 2] = make_int4(0, 0, 0, 0);
+    if (tid == 0) {           // no partials yet
+        p.part_desc[blockIdx.x * 4] = make_int4(0, 0, 0, 0);
+        p.part_desc[blockIdx.x * 4 + 2] = make_int4(0, 0, 0, 0);
     }
     Cursor cur;
-    draft_schedule<kUnitRows, kTile, kThreads, kLeast>(p, piece, kValue, smem + S::kAlpha, cur);
+    draft_schedule<kLatentRows, kTile, kThreads, kLeast>(p, blockIdx.x, kValue, smem + S::kAlpha, cur);
     static_assert(draft_scratch<kThreads>() <= 2 * kLatentRows * 4, "the schedule's scratch");
     tc_fence_before();
     __syncthreads();
-    if constexpr (kPair) cluster_sync();  // the other CTA's barriers are ready
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S::kAddr);
     DraftItem it;
     bool ok = true;  // no wait has run out
-    // The next part of a unit, with this CTA's rows of it.
-    int unit_rows = 0, first_rows = 0;  // rows of the unit, and those of its first CTA
-    const auto next = [&]() -> bool {
-        if (!cur.next(p, it)) return false;
-        unit_rows = it.rows;
-        if constexpr (kPair) {
-            const int mine = first_rows = (it.rows + 1) / 2;
-            it.row0 += rank * mine;
-            it.rows = rank ? it.rows - mine : mine;
-        }
-        return true;
-    };
 
     if (warp == kCopyWarp) {
         // -------------------------------------------------------------- copies
         const uint64_t policy = l2_policy_evict_first();
         const uint32_t el = issuing_lane();
         int c = 0;  // tiles
-        while (ok && next()) {
+        while (ok && cur.next(p, it)) {
             const int32_t* table = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
             const int units = (it.q.L + kSlotKeys - 1) / kSlotKeys;
             int ids = 0;  // block ids of 32 slots, 8 tiles
@@ -218,10 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (jj < units) {
                         if (el) {
                             mbar_arrive_expect_tx(bar, kSlot);
-                            if constexpr (!kPair)
-                                tma_load_4d(sbase + S::kKV + slot * kSlot, &tmc, bar, 0, 0, 0, group, policy);
-                            else if ((i & 1) == rank)  // the CTAs take turns, each for both
-                                tma_load_4d_multicast(sbase + S::kKV + slot * kSlot, &tmc, bar, 0, 0, 0, group, 3, policy);
+                            tma_load_4d(sbase + S::kKV + slot * kSlot, &tmc, bar, 0, 0, 0, group, policy);
                         }
                     } else if (el) {
                         mbar_arrive(bar);  // behind the context: whatever lies there is masked
@@ -233,16 +201,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every copy has landed before the CTA ends
         if (lane == 0)
             for (int i = max(0, c - 2); i < c; ++i)
-                for (int k = 0; k < kSlots; ++k) {
-                    wait_bar(full0 + 8 * ((i & 1) * kSlots + k), (i / 2) & 1);
-                    // ... and, with a pair, what the other CTA's products have to say here has been said
-                    if (kPair) wait_bar(empty0 + 8 * ((i & 1) * kSlots + k), (i / 2) & 1);
-                }
+                for (int k = 0; k < kSlots; ++k) wait_bar(full0 + 8 * ((i & 1) * kSlots + k), (i / 2) & 1);
     } else if (warp == kQueryWarp) {
         // ------------------------------------------------------------- queries
         if (lane == 0) {
             int k = 0;
-            while (ok && next()) {
+            while (ok && cur.next(p, it)) {
                 if (k > 0) ok = wait_bar(qempty, (k - 1) & 1);
                 if (!ok) break;
                 mbar_arrive_expect_tx(qfull, kParts * kLatentRows * 128);
@@ -274,10 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t since = 0;  // of a wait
         while (ok) {
             if (left == 0 && more) {
-                more = next();
+                more = cur.next(p, it);
                 left = __shfl_sync(0xffffffffu, more ? it.t1 - it.t0 : 0, 0);
                 more = left > 0;
-                id_o = umma_idesc(kBF16, 128, max(16, (__shfl_sync(0xffffffffu, it.rows, 0) + 15) / 16 * 16), true, false);
+                id_o = umma_idesc(kBF16, 128, (__shfl_sync(0xffffffffu, it.rows, 0) + 15) / 16 * 16, true, false);
                 first = true;
             }
             if (np < nk && mbar_test_warp(pfull, np & 1)) {
@@ -289,10 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
                         umma_f16_ss(el, tm + 64 * mt, vd + ks * (kSlot / 16) + mt * 128, p_desc + ks * 2, id, !begins || ks > 0);
-                    if constexpr (kPair)
-                        umma_commit_multicast(el, empty0 + 8 * (b * kSlots + ks), 3);
-                    else
-                        umma_commit(el, empty0 + 8 * (b * kSlots + ks));
+                    umma_commit(el, empty0 + 8 * (b * kSlots + ks));
                 }
                 umma_commit(el, odone);
                 last_bar = odone;
@@ -346,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* alpha = reinterpret_cast<float*>(smem + S::kAlpha);
         float* fin = reinterpret_cast<float*>(smem + S::kFin);
         int c = 0, k = 0;
-        while (next()) {
+        while (cur.next(p, it)) {
             const int base = it.q.L - it.q.n;
             const int ta = min((it.row0 + ra) / p.group, it.q.n - 1), tb = min((it.row0 + rb) / p.group, it.q.n - 1);
             const uint64_t mask_a = draft_mask(p, it.q, ta), mask_b = draft_mask(p, it.q, tb);
@@ -474,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lb += __shfl_xor_sync(0xffffffffu, lb, o);
             }
             const bool part = it.partial(), zero = !ok || wrong;
-            const int slot = piece * 2 + (it.begins() ? 1 : 0);
-            const int64_t prow = (int64_t)slot * kUnitRows + (kPair && rank ? first_rows : 0);  // row 0 of this CTA's
+            const int slot = blockIdx.x * 2 + (it.begins() ? 1 : 0);
+            const int64_t prow = (int64_t)slot * kLatentRows;
             if ((lane & 3) == 0) {
                 if (part) {
                     float2* ml = p.part_ml + prow;
@@ -489,10 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (tid == 0) {
                 lost[(k + 1) % 3] = 0;  // (read last before the barrier of the unit before)
-                if (part && rank == 0) {
+                if (part) {
                     p.part_desc[slot * 2] =
                         make_int4(kPartValid | (it.begins() ? kPartBegins : 0) | (it.ends() ? kPartEnds : 0), it.q.tok0,
-                                  it.row0, unit_rows);
+                                  it.row0, it.rows);
                     p.part_desc[slot * 2 + 1] = make_int4(0, 0, 0, 0);
                 }
             }
@@ -557,69 +518,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == kProductWarp) tmem_dealloc(tmem, kTmemCols);
-    if constexpr (kPair) cluster_sync();  // nothing of the other CTA's is on its way here any more
 }
 
 template <bool kBF16, int BS>
-cudaError_t launch_t(const DraftParams& p, bool pairs, const CUtensorMap& tmq, const CUtensorMap& tmc, cudaStream_t stream) {
-    auto kern = pairs ? latent_kernel<kBF16, BS, true> : latent_kernel<kBF16, BS, false>;
+cudaError_t launch_t(const DraftParams& p, const CUtensorMap& tmq, const CUtensorMap& tmc, cudaStream_t stream) {
+    auto kern = latent_kernel<kBF16, BS>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LatentSmem::kTotal);
     if (e != cudaSuccess) return e;
-    if (!pairs) return launch_pdl(kern, dim3(p.pieces), dim3(kThreads), LatentSmem::kTotal, stream, tmq, tmc, p);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * p.pieces);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = LatentSmem::kTotal;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {2, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, tmq, tmc, p);
+    return launch_pdl(kern, dim3(p.pieces), dim3(kThreads), LatentSmem::kTotal, stream, tmq, tmc, p);
 }
 
 }  // namespace
 
-int latent_pairs() {
-    static std::atomic<int> cache[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    int n = cache[dev].load();
-    if (n == 0) {
-        auto kern = latent_kernel<true, 16, true>;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LatentSmem::kTotal) != cudaSuccess) return 0;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = LatentSmem::kTotal;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim = {2, 1, 1};
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return 0;
-        }
-        cache[dev].store(n);
-    }
-    return n;
-}
-
-cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size, bool pairs, const CUtensorMap& tmq,
-                                 const CUtensorMap& tmc, cudaStream_t stream, int* launches) {
+cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size, const CUtensorMap& tmq, const CUtensorMap& tmc,
+                                 cudaStream_t stream, int* launches) {
     const bool bf16 = dtype == PKV_BF16;
     const cudaError_t e =
         block_size == 16
-            ? (bf16 ? launch_t<true, 16>(p, pairs, tmq, tmc, stream) : launch_t<false, 16>(p, pairs, tmq, tmc, stream))
-            : (bf16 ? launch_t<true, 32>(p, pairs, tmq, tmc, stream) : launch_t<false, 32>(p, pairs, tmq, tmc, stream));
+            ? (bf16 ? launch_t<true, 16>(p, tmq, tmc, stream) : launch_t<false, 16>(p, tmq, tmc, stream))
+            : (bf16 ? launch_t<true, 32>(p, tmq, tmc, stream) : launch_t<false, 32>(p, tmq, tmc, stream));
     if (e != cudaSuccess) return e;
     ++*launches;
-    const int rows = pairs ? 2 * kLatentRows : kLatentRows;
-    return draft_divides(p, kTile, rows, kLeast) ? launch_draft_merge(p, dtype, kValue, rows, stream, launches) : cudaSuccess;
+    return draft_divides(p, kTile, kLatentRows, kLeast) ? launch_draft_merge(p, dtype, kValue, kLatentRows, stream, launches)
+                                                        : cudaSuccess;
 }
 
 }  // namespace pkv

@@ -69,14 +69,6 @@ __device__ __forceinline__ void umma_commit(uint32_t el, uint32_t bar) {
         "r"(el)
         : "memory");
 }
-// ... on the barriers at this place in every CTA of the cluster that `mask` names.
-__device__ __forceinline__ void umma_commit_multicast(uint32_t el, uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-        "h"(mask), "r"(el)
-        : "memory");
-}
 // Has the phase of this parity ended?  (Without waiting; the same answer in all lanes.)
 __device__ __forceinline__ bool mbar_test_warp(uint32_t bar, uint32_t parity) {
     uint32_t done;
