@@ -381,8 +381,10 @@ pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void
  * K and V of positions that a token does not attend, and of the blocks' rows
  * behind the context, may hold anything.  Values that are not finite make
  * not finite the outputs of the tokens that attend them, and of no others.
- * Weights are rounded to the cache's type for their product with V;
- * everything else is in 32 bits.
+ * Weights are rounded once to the cache's type for their product with V (half
+ * a step, 2^-8 of a weight in bf16 and 2^-11 in fp16, and in fp16 by up to 2^-32
+ * of the largest weight for the smallest ones; paged_attention_decode carries
+ * what its weights lose along); everything else is in 32 bits.
  * The result does not depend on physical block ids, and is the same from run
  * to run.
  * Bad metadata never faults: query_starts out of order or range

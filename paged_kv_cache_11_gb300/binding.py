@@ -401,7 +401,8 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
 
     Tokens query_starts[s] .. query_starts[s + 1] - 1 of q (at most 64) are sequence s's; bit j of a token's tree_masks says
     whether it attends the j-th of them (None: a chain, each attends those up to itself).  ``context_lens`` counts them: their
-    K and V are in the cache.  Without query_starts every sequence has one token.
+    K and V are in the cache.  Without query_starts every sequence has one token.  Weights are rounded to q's dtype for their
+    product with V (paged_attention_decode carries what they lose along, and has fp32 outputs).
     """
     if stream is not None:
         with _on(stream, q):

@@ -28,8 +28,9 @@
 //
 // Warps: 0-3 the softmax (16 rows each) and the output, 4 the copies of rows, 5
 // the products, 6 the copies of queries.  The maximum is raised lazily, as in
-// tree.cu; a weight is rounded to the cache's 16-bit type for its product, the
-// row's sum is that of the weights before.  Masked places are replaced, not
+// tree.cu; a weight is rounded to the cache's 16-bit type for its product (fp16's
+// at seven binades more, softmax_tile.cuh), the row's sum is that of the weights
+// before.  Masked places are replaced, not
 // added to, and values that are not finite are kept out of the products of
 // tiles with masks, as there.
 //
@@ -385,12 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     alpha[b * kLatentRows + rb] = fb;
                 }
                 const bool rescale = softmax_any(t > it.t0 && (raise_a || raise_b));
-                const float na = ma == -INFINITY ? 0.f : ma, nb = mb == -INFINITY ? 0.f : mb;
+                const float na = kWeightExponent<kBF16> - (ma == -INFINITY ? 0.f : ma);
+                const float nb = kWeightExponent<kBF16> - (mb == -INFINITY ? 0.f : mb);
                 uint32_t wa[8], wb[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float a0 = fast_exp2(fmaf(s[4 * i], f, -na)), a1 = fast_exp2(fmaf(s[4 * i + 1], f, -na));
-                    const float b0 = fast_exp2(fmaf(s[4 * i + 2], f, -nb)), b1 = fast_exp2(fmaf(s[4 * i + 3], f, -nb));
+                    const float a0 = fast_exp2(fmaf(s[4 * i], f, na)), a1 = fast_exp2(fmaf(s[4 * i + 1], f, na));
+                    const float b0 = fast_exp2(fmaf(s[4 * i + 2], f, nb)), b1 = fast_exp2(fmaf(s[4 * i + 3], f, nb));
                     wa[i] = pack2<kBF16>(a0, a1);
                     wb[i] = pack2<kBF16>(b0, b1);
                     la += a0 + a1;

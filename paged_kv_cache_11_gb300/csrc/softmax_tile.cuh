@@ -86,6 +86,14 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // weights up to 2^8 against the old one are as good.
 constexpr float kRaise = 8.f;
 
+// Weights are 2^(score - maximum + this) on their way to 16 bits.  fp16 ends at 2^16 and the weights at 2^kRaise, so its steps
+// of 2^-24 near zero are used seven binades further down: what a weight loses there is at most 2^-32 of the largest, so that 2^21
+// tokens of the smallest weights are held to the output's own half step (without it 131072 tokens 18 below one other in the
+// exponent, 2^-9 of the output, would be zeros).  The factor is in the row's sum and its products alike, and every part of a
+// divided context has it.  bf16 has fp32's range.
+template <bool kBF16>
+constexpr float kWeightExponent = kBF16 ? 0.f : 7.f;
+
 // Two fp32 values in a register pair, and their arithmetic.
 typedef uint64_t f32x2;
 __device__ __forceinline__ f32x2 pack_f32x2(float lo, float hi) {
@@ -130,7 +138,7 @@ __device__ __forceinline__ void raise_maximum(float mx, uint32_t o_addr, float& 
     }
 }
 
-// 32 scores v to weights 2^(v f - ms): 16 pairs to `w`, their sum added to `sum`.
+// 32 scores v to weights 2^(v f + neg_ms): 16 pairs to `w`, their sum added to `sum`.
 template <bool kBF16>
 __device__ __forceinline__ void weights32(const float (&v)[32], f32x2 f, f32x2 neg_ms, uint32_t (&w)[16], f32x2& sum) {
 #pragma unroll
@@ -189,8 +197,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, b
         raise_maximum(mx, o_addr, m_run, l);
     else
         m_run = fmaxf(m_run, mx);
-    const float ms = m_run == -INFINITY ? 0.f : m_run;
-    const f32x2 ff = pack_f32x2(f, f), neg = pack_f32x2(-ms, -ms);
+    const float neg_ms = kWeightExponent<kBF16> - (m_run == -INFINITY ? 0.f : m_run);
+    const f32x2 ff = pack_f32x2(f, f), neg = pack_f32x2(neg_ms, neg_ms);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         tmem_ld_wait32(s[c & 1]);

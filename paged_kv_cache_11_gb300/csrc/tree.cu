@@ -25,7 +25,8 @@
 // passes it by 2^8 (weights up to 2^8 against the old one are as good).  A
 // weight is rounded to the cache's 16-bit type for the product, half a step at
 // most, 2^-8 (bf16), of each weight, some up and some down, where the output is
-// rounded by as much; the row's sum is that of the weights before, in 32 bits.
+// rounded by as much (softmax_tile.cuh: fp16's range); the row's sum is that of
+// the weights before, in 32 bits.
 //
 // Warps: 0-3 and 4-7 the streams' softmax, 8 the copies (one TMA copy for each
 // block of K or V, as 8-token groups of 2 KiB, into a ring of five 32 KiB
