@@ -488,13 +488,15 @@ size_t paged_latent_decode_workspace_bytes(void);
  * k_rope:   token t at base + t * k_rope_stride: kv_out of paged_latent_append_rope behind its first latent_dim values.
  * query_starts, key_starts: [num_seqs + 1] int32 device memory, in order.
  *           Rows of q and out outside the sequences are left alone.
- * max_query_len: host-side upper bound of the sequences' n.
+ * max_query_len: host-side upper bound of the sequences' n, at most
+ *           num_query_tokens (which is always one; more is refused).
  * out:      [num_query_tokens][num_heads][value_dim], 16-byte aligned.
  * q, kv and k_rope are 16-byte aligned.  What is not finite stays with the
  * queries that attend it, and weights are rounded as for paged_attention_tree.
  * Bad metadata never faults: query_starts out of order or range leave the
- * sequence's rows alone, key_starts out of order or range and n >
- * max_query_len get zeros (PKV_DEVERR_QUERY).
+ * sequence's rows alone (and may leave alone those of sequences that lie over
+ * others), key_starts out of order or range and n > max_query_len get zeros
+ * (PKV_DEVERR_QUERY).
  * Supported: nope_dim 128, rope_dim 64, value_dim 128; bf16 or fp16; num_heads and num_seqs <= 65535.
  */
 pkv_status latent_attention_prefill(const void* q, const void* kv, const void* k_rope, const int32_t* query_starts,

@@ -16,12 +16,22 @@
 // of values t keys t - 1: that is all that a copy waits for, and a tile of
 // either kind has one barrier.
 //
-// CTAs of one head follow one another, the longest rows first.  A CTA that has
-// issued the copies of its queries' last tile takes the place of one that has
-// not begun (a cluster launch control request) and goes on with that one's
-// queries and keys, so that they are on their way while the last tiles are worked
-// off, and barriers and tensor memory are set up once: 16 prompts of 256 tokens
-// with 128 heads 135 us for 168, 8 of 1024 423 for 477, one of 16384 with 64
+// The strips of 256 queries of all prompts stand in a line, a prompt's last (and
+// longest) first, and the grid is that line for every head.  The host knows an
+// upper bound of its length, from the tokens, the prompts and the longest of them;
+// a CTA counts the strips before each prompt (or before every so many, past 512
+// prompts) when it starts, and a warp looks a place up, 32 prompts or counts at a
+// time; up to 32 prompts it goes by their lengths alone.  (A place for each prompt
+// and strip of the longest would be 1e9 places for the 2e5 strips of 16384 prompts
+// whose longest is not known.  1024 prompts of 64 tokens with 8 heads take 225 us
+// with and without a bound, so 220 with one and 6200 without; one prompt of 4000
+// tokens among 200 of 40 takes 198, so 258; one of 100 alone 7.0, so 6.85.)
+//
+// A CTA that has issued the copies of its queries' last tile takes the place of
+// one that has not begun (a cluster launch control request) and goes on with that
+// one's queries and keys, so that they are on their way while the last tiles are
+// worked off, and barriers and tensor memory are set up once: 16 prompts of 256 tokens
+// with 128 heads 137 us for 168, 8 of 1024 426 for 477, one of 16384 with 64
 // heads 3.38 ms for 3.47.  (Claimed one item earlier, the grid's last items wait
 // behind long ones: 7 ragged prompts 175 us for 169.)  Grids of one CTA an SM at
 // most claim nothing.
@@ -33,7 +43,9 @@
 // and there every instruction of the product warp between a stream's P and its
 // next S counts: flags of its tiles carried from one item to the next cost 5%, the
 // loop over streams not unrolled 10%.  (A warp for each stream's products: 3.92
-// against 3.90 ms.)  Seven prompts of 1 to 1537 tokens with 40 heads: 165 us.
+// against 3.90 ms.)  Seven prompts of 1 to 1537 tokens with 40 heads: 169 us.
+#include <algorithm>
+
 #include "softmax_tile.cuh"
 
 namespace pkv {
@@ -48,6 +60,7 @@ constexpr int kTile = 128;               // keys
 constexpr int kUnit = kTile * 128;       // bytes of a ring unit
 constexpr int kKeyUnits = 3, kTileUnits = 5;
 constexpr int kRing = 8;
+constexpr int kMarks = 512;              // of the line of strips: where every so many prompts begin
 constexpr int kLostTiles = 3;            // tiles that some of a CTA's queries mask: 255 keys and a part of one more
 constexpr uint32_t kTmemCols = 512;      // S and P of the streams: [0, 128), [128, 256); O: [256, 384), [384, 512)
 
@@ -63,7 +76,9 @@ struct PromptSmem {
     static constexpr int kClaim = kItem + 32;          // the answer to a claim
     // [3 items in turn][12] keys whose values were taken out, from the first masked tile on
     static constexpr int kLost = kClaim + 16;
-    static constexpr int kTotal = kLost + 3 * kLostTiles * 4 * 4;
+    static constexpr int kMark = kLost + 3 * kLostTiles * 4 * 4;  // [kMarks + 1]
+    static constexpr int kSum = kMark + (kMarks + 1) * 4;         // [8] of the warps that count
+    static constexpr int kTotal = kSum + 8 * 4;
     static_assert(kTotal <= 227 * 1024 && kBar % 16 == 0 && kClaim % 16 == 0, "shared memory of one CTA");
 };
 
@@ -105,22 +120,96 @@ __device__ __forceinline__ uint32_t before(int c, int seen) {
     return seen - c >= 32 ? ~0u : seen > c ? (1u << (seen - c)) - 1 : 0u;
 }
 
-// The rows of a prompt with bad metadata become zeros, whatever their number: a head's, from query q0 on, 256 for each place in
-// the grid's first dimension.
-__device__ __noinline__ void zero_prompt(const LatentPromptParams& p, int a0, int a1, int q0, int head, int lane, int lanes) {
+// Strips of a prompt whose queries are tokens a0 .. a1 - 1: 0 where these are no rows.
+__device__ __forceinline__ int strips_of(int a0, int a1, int num_queries, int max_query_len) {
+    return a0 < 0 || a1 < a0 || a1 > num_queries ? 0 : (min(a1 - a0, max_query_len) + kRows - 1) / kRows;
+}
+
+__device__ __forceinline__ bool bad_prompt(const LatentPromptParams& p, int a0, int a1, int b0, int b1) {
+    return a0 < 0 || a1 < a0 || a1 > p.num_queries || b0 < 0 || b1 < b0 || b1 > p.num_keys || a1 - a0 > p.max_query_len;
+}
+
+// marks[i] = strips of the prompts before i * per, up to i = used (a whole CTA; a barrier of the caller's follows).  Counts end
+// at the grid's length, which only bad metadata (prompts over one another) passes; that is recorded here.
+__device__ __noinline__ void mark_strips(const LatentPromptParams& p, int per, int used, int* marks, int* sums) {
+    const int tid = threadIdx.x, lane = tid & 31, most = (int)gridDim.x;
+    int mine[2] = {0, 0}, scan = 0;
+    if (2 * (tid & ~31) < used) {  // (whole warps)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            for (int s = (2 * tid + h) * per; s < min((2 * tid + h + 1) * per, p.num_seqs); ++s) {
+                const int a0 = p.query_starts[s], a1 = p.query_starts[s + 1], b0 = p.key_starts[s], b1 = p.key_starts[s + 1];
+                if (bad_prompt(p, a0, a1, b0, b1)) record_error(p.err, PKV_DEVERR_QUERY);
+                mine[h] = min(most, mine[h] + strips_of(a0, a1, p.num_queries, p.max_query_len));
+            }
+        scan = mine[0] + mine[1];  // inclusive over the warp
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += v;
+        }
+        if (lane == 31) sums[tid >> 5] = min(most, scan);
+    }
+    if (used > 64) __syncthreads();
+    if (2 * tid >= used) return;
+    int before = scan - mine[0] - mine[1];
+    for (int w = 0; w < tid >> 5; ++w) before += sums[w];
+    if (tid == 0) marks[0] = 0;
+    marks[2 * tid + 1] = min(most, before + mine[0]);
+    marks[2 * tid + 2] = min(most, before + mine[0] + mine[1]);
+}
+
+// Strip x of the line: the prompt that it is in (-1: x is behind the line's end), and its number there.  A whole warp.
+__device__ __noinline__ int2 find_strip(const LatentPromptParams& p, int per, int used, const int* marks, int x) {
+    const int lane = threadIdx.x & 31;
+    int s = 0, count = p.num_seqs;  // prompts that it is among
+    if (count > 32) {
+        if (x >= marks[used]) return make_int2(-1, 0);
+        // the last mark that x has come to: of those sixteen apart, then of sixteen
+        static_assert(kMarks == 32 * 16, "two looks");
+        int i = 16 * lane;
+        unsigned passed = __ballot_sync(0xffffffffu, i < used && marks[i] <= x);
+        const int from = 16 * (31 - __clz(passed));
+        i = from + (lane & 15);
+        passed = __ballot_sync(0xffffffffu, lane < 16 && i < used && marks[i] <= x);
+        i = from + 31 - __clz(passed);
+        x -= marks[i];
+        if (per == 1) return make_int2(i, x);
+        s = i * per;
+        count = min(per, count - s);
+    }
+    for (;; s += 32, count -= 32) {
+        const int mine =
+            lane < count ? strips_of(p.query_starts[s + lane], p.query_starts[s + lane + 1], p.num_queries, p.max_query_len) : 0;
+        int scan = mine;  // inclusive over the warp
+        for (int o = 1; o < min(32, count); o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += v;
+        }
+        const unsigned in = __ballot_sync(0xffffffffu, lane < count && x < scan);
+        if (in) return make_int2(s + __ffs(in) - 1, x - __shfl_sync(0xffffffffu, scan - mine, __ffs(in) - 1));
+        if (count <= 32) return make_int2(-1, 0);
+        x -= __shfl_sync(0xffffffffu, scan, 31);
+    }
+}
+
+// The rows of a prompt with bad metadata become zeros, whatever their number: a head's, from query q0 on, 256 for each of its
+// strips.
+__device__ __noinline__ void zero_prompt(const LatentPromptParams& p, int a0, int a1, int q0, int strips, int head) {  // (a whole warp)
+    const int lane = threadIdx.x & 31;
     uint16_t* out = static_cast<uint16_t*>(p.out);
-    for (int64_t r = q0; r < a1 - a0; r += (int64_t)gridDim.x * kRows)
-        for (int i = lane; i < min((int64_t)kRows, a1 - a0 - r) * 16; i += lanes)
+    for (int64_t r = q0; r < a1 - a0; r += (int64_t)strips * kRows)
+        for (int i = lane; i < min((int64_t)kRows, a1 - a0 - r) * 16; i += 32)
             *reinterpret_cast<uint4*>(out + ((a0 + r + i / 16) * p.num_heads + head) * 128 + i % 16 * 8) = make_uint4(0, 0, 0, 0);
 }
 
-// The wait for an item: the copies' lane may be looking through a great many empty places.
+// The wait for an item: the copies' lane may be looking through many empty places.
 __device__ __noinline__ bool wait_item(uint32_t bar, uint32_t parity) { return mbar_wait_for(bar, parity, 32 * kWaitLimitNs); }
 
 template <bool kBF16>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmkv,
-                         const __grid_constant__ CUtensorMap tmr, const LatentPromptParams p) {
+                         const __grid_constant__ CUtensorMap tmr, const __grid_constant__ LatentPromptParams p) {
     using S = PromptSmem;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -157,20 +246,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProductWarp) tmem_alloc(sbase + S::kAddr, kTmemCols);
     pdl_wait();
     pdl_launch_dependents();
-    // The item at a place in the grid (rows == 0: there is none).  lanes > 0: of so many threads that see to bad metadata.
-    const auto item_at = [&](const dim3& at, int lanes) -> Item {
-        const int seq = at.z, q0 = (int)(gridDim.x - 1 - at.x) * kRows;
-        const int a0 = p.query_starts[seq], a1 = p.query_starts[seq + 1], b0 = p.key_starts[seq], b1 = p.key_starts[seq + 1];
-        const bool no_rows = a0 < 0 || a1 < a0 || a1 > p.num_queries;
-        const bool bad = !no_rows && (b0 < 0 || b1 < b0 || b1 > p.num_keys || a1 - a0 > p.max_query_len);
-        if (lanes > 0 && (no_rows || bad)) {
-            if (lane == 0 && at.y == 0 && q0 == 0) record_error(p.err, PKV_DEVERR_QUERY);
-            if (bad) zero_prompt(p, a0, a1, q0, at.y, lane, lanes);
-        }
-        if (no_rows || bad || q0 >= a1 - a0) return {0, 0, 0, 0, 0, 0};
-        return {a0 + q0, min(kRows, a1 - a0 - q0), (int)at.y, q0 + 1 + (b1 - b0) - (a1 - a0), b0, b1 - b0};
+    int* marks = reinterpret_cast<int*>(smem + S::kMark);
+    const int per = (p.num_seqs + kMarks - 1) / kMarks, used = (p.num_seqs + per - 1) / per;
+    const auto starts_of = [&](int s, int2& q, int2& k) {
+        q = make_int2(p.query_starts[s], p.query_starts[s + 1]);
+        k = make_int2(p.key_starts[s], p.key_starts[s + 1]);
     };
-    Item it = item_at(blockIdx, warp == kCopyWarp ? 32 : 0);  // of the CTA's own place
+    // A strip of the prompt whose queries and keys begin and end at q and k, and a head: the item (rows == 0: there is none).
+    // zeroes: this warp sees to the rows of a prompt with bad metadata.
+    const auto item_of = [&](int2 q, int2 k, int strip, int head, bool zeroes) -> Item {
+        const int strips = strips_of(q.x, q.y, p.num_queries, p.max_query_len), q0 = (strips - 1 - strip) * kRows, n = q.y - q.x;
+        if (strip < 0 || q0 < 0) return {0, 0, 0, 0, 0, 0};
+        if (bad_prompt(p, q.x, q.y, k.x, k.y)) {
+            if (zeroes) zero_prompt(p, q.x, q.y, q0, strips, head);
+            return {0, 0, 0, 0, 0, 0};
+        }
+        return {q.x + q0, min(kRows, n - q0), head, q0 + 1 + (k.y - k.x) - n, k.x, k.y - k.x};
+    };
+    // The CTA's own place: what find_strip finds, with a load and a few exchanges less where there are few prompts.
+    int2 q, k;
+    int strip = blockIdx.x;
+    if (p.num_seqs == 1) {
+        starts_of(0, q, k);
+    } else if (p.num_seqs <= 32) {
+        starts_of(min(lane, p.num_seqs - 1), q, k);
+        const int mine = lane < p.num_seqs ? strips_of(q.x, q.y, p.num_queries, p.max_query_len) : 0;
+        int scan = mine;  // inclusive over the warp
+        for (int o = 1; o < p.num_seqs; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += v;
+        }
+        const unsigned in = __ballot_sync(0xffffffffu, strip < scan);
+        const int at = in ? __ffs(in) - 1 : 0;
+        strip = in ? strip - __shfl_sync(0xffffffffu, scan - mine, at) : -1;
+        q = make_int2(__shfl_sync(0xffffffffu, q.x, at), __shfl_sync(0xffffffffu, q.y, at));
+        k = make_int2(__shfl_sync(0xffffffffu, k.x, at), __shfl_sync(0xffffffffu, k.y, at));
+    } else {
+        mark_strips(p, per, used, marks, reinterpret_cast<int*>(smem + S::kSum));
+        __syncthreads();
+        const int2 at = find_strip(p, per, used, marks, strip);
+        starts_of(max(at.x, 0), q, k);
+        strip = at.x < 0 ? -1 : at.y;
+    }
+    Item it = item_of(q, k, strip, blockIdx.y, warp == kCopyWarp);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -198,37 +316,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kCopyWarp) {
         // -------------------------------------------------------------- copies
-        if (lane == 0) {
-            uint32_t nq[2] = {0, 0}, nk = 0, nv = 0;  // of each stream's Q, of tiles: those copied
-            uint32_t claims = 0, posted = 0;
-            // The next item: the place of a CTA that has not begun, claimed when the copies of the item before have been
-            // issued, two tiles before its end.
-            const auto claimed = [&]() -> bool {
-                if (own) {
-                    own = false;
-                    return true;
-                }
-                if (!p.claims) return false;
-                it = {0, 0, 0, 0, 0, 0};
-                for (bool more = true; more && ok && it.rows == 0;) {
+        uint32_t nq[2] = {0, 0}, nk = 0, nv = 0;  // of each stream's Q, of tiles: those copied (by lane 0)
+        uint32_t claims = 0, posted = 0;
+        // The next item: the place of a CTA that has not begun, claimed when the copies of the item before have been
+        // issued, two tiles before its end.
+        const auto claimed = [&]() -> bool {
+            if (own) {
+                own = false;
+                return true;
+            }
+            if (!p.claims) return false;
+            it = {0, 0, 0, 0, 0, 0};
+            for (bool more = true; more && it.rows == 0;) {
+                dim3 at;
+                if (lane == 0 && ok) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive_expect_tx(claim, 16);
                     claim_cta(sbase + S::kClaim, claim);
                     ok = wait_bar(claim, claims++ & 1);
-                    dim3 at;
                     more = ok && claimed_cta(sbase + S::kClaim, at);
-                    if (more) it = item_at(at, 1);
+                } else if (lane == 0) {
+                    more = false;
                 }
+                more = __shfl_sync(0xffffffffu, more, 0);
+                if (more) {
+                    const int2 found = find_strip(p, per, used, marks, __shfl_sync(0xffffffffu, (int)at.x, 0));
+                    starts_of(max(found.x, 0), q, k);
+                    it = item_of(q, k, found.x < 0 ? -1 : found.y, __shfl_sync(0xffffffffu, (int)at.y, 0), true);
+                }
+            }
+            if (lane == 0) {
                 // until the softmax, which may be at the item before, has taken it
                 if (posted > 0) ok = ok && wait_bar(iempty, (posted - 1) & 1);
                 if (!ok) it.rows = 0;  // (the others need not wait for more)
                 *reinterpret_cast<int4*>(smem + S::kItem) = make_int4(it.row, it.rows, it.head, it.seen0);
                 *reinterpret_cast<int2*>(smem + S::kItem + 16) = make_int2(it.key, it.keys);
                 mbar_arrive(ifull);
-                ++posted;
-                return it.rows > 0;
-            };
-            while (claimed()) {
+            }
+            ++posted;
+            return __shfl_sync(0xffffffffu, it.rows, 0) > 0;
+        };
+        while (claimed()) {
+            if (lane == 0) {
                 const auto queries = [&](int x) {
                     if (nq[x] > 0) ok = ok && wait_bar(qempty0 + 8 * x, (nq[x] - 1) & 1);
                     if (!ok) return;
@@ -264,6 +393,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++nv;
                 }
             }
+            __syncwarp();
+        }
+        if (lane == 0) {
             if (!ok) record_error(p.err, PKV_DEVERR_TIMEOUT);
             // every copy has landed before the CTA ends
             for (int x = 0; x < 2; ++x)
@@ -273,6 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kProductWarp) {
         // ------------------------------------------------------------ products
+        // (first what mark_strips does for more prompts, away from the copies' way)
+        if (lane < p.num_seqs && p.num_seqs <= 32 &&
+            bad_prompt(p, p.query_starts[lane], p.query_starts[lane + 1], p.key_starts[lane], p.key_starts[lane + 1]))
+            record_error(p.err, PKV_DEVERR_QUERY);
+        __syncwarp();
         const uint32_t el = issuing_lane(), tm = __shfl_sync(0xffffffffu, tmem, 0), sb = __shfl_sync(0xffffffffu, sbase, 0);
         const uint32_t id_s = umma_idesc(kBF16, 128, kTile, false, false);
         const uint32_t id_o = umma_idesc(kBF16, 128, 128, false, true), id_h = umma_idesc(kBF16, 128, 64, false, true);
@@ -459,9 +596,12 @@ cudaError_t launch_latent_prompt(const LatentPromptParams& in, int dtype, const 
     auto kern = dtype == PKV_BF16 ? latent_prompt_kernel<true> : latent_prompt_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem::kTotal);
     if (e != cudaSuccess) return e;
-    const dim3 grid((in.max_query_len + kRows - 1) / kRows, in.num_heads, in.num_seqs);
+    // No more strips than these, whatever the prompts' lengths: n tokens make at most (n + kRows - 1) / kRows.
+    const int64_t strips = std::min(in.num_seqs * (((int64_t)in.max_query_len + kRows - 1) / kRows),
+                                    (in.num_queries + (int64_t)in.num_seqs * (kRows - 1)) / kRows);
+    const dim3 grid((unsigned)strips, in.num_heads);
     LatentPromptParams p = in;
-    p.claims = (int64_t)grid.x * grid.y > (p.sms - 1) / (int64_t)grid.z;  // (more than one CTA an SM)
+    p.claims = strips * grid.y > p.sms;  // (more than one CTA an SM)
     e = launch_pdl(kern, grid, dim3(kThreads), PromptSmem::kTotal, stream, tmq, tmkv, tmr, p);
     if (e == cudaSuccess) ++*launches;
     return e;
