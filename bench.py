@@ -145,7 +145,7 @@ def decode_source_hash(grouped: bool = False) -> str:
     (whose traffic figure is the sum over its two kernels)."""
     import hashlib
     h = hashlib.sha256()
-    names = ("decode.cu", "decode_common.cuh", "pkv_internal.cuh") + (("group_prefix.cu",) if grouped else ())
+    names = ("decode.cu", "decode_common.cuh", "pkv_internal.cuh") + (("group_prefix.cu", "tcgen05.cuh") if grouped else ())
     for name in names:
         h.update(_code_only((ROOT / "paged_kv_cache_11_gb300" / "csrc" / name).read_text()).encode())
     return h.hexdigest()[:16]

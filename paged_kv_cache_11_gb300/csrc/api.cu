@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "drafted.cuh"
+#include "latent.cuh"
 #include "pkv_internal.cuh"
 
 namespace pkv {

@@ -46,7 +46,9 @@
 // 32 take 34 cycles to issue and not 16.  (Pairs of CTAs that copied each row
 // into both rings at once took 92 us for the 96; such copies are not used here,
 // since nothing keeps them to memory of this GPU.)
+#include "copies.cuh"
 #include "drafted.cuh"
+#include "latent.cuh"
 #include "softmax_tile.cuh"
 
 namespace pkv {

@@ -13,7 +13,7 @@
 // fewer registers: 25.1 and 28.6 us; CTAs of 256 threads: 25.2.)  Pairs (i, i +
 // 32) sit in lanes 4 apart and cost one exchange; neighbouring pairs sit in one
 // lane.
-#include "pkv_internal.cuh"
+#include "latent.cuh"
 
 namespace pkv {
 namespace {

@@ -183,46 +183,6 @@ struct RopeParams {
 // dtype: PKV_BF16 or PKV_FP16; fp8: the pool is e4m3 with scales.
 cudaError_t launch_rope_append(const RopeParams& p, int dtype, bool fp8, cudaStream_t stream, int* launches);
 
-// A row of a latent cache: the latent and the key part with the position.
-constexpr int kLatentDim = 512, kLatentRope = 64, kLatentRow = kLatentDim + kLatentRope;
-
-// Write into a paged latent cache (latent_append.cu); strides in elements.
-struct LatentAppendParams {
-    int* err;
-    const uint16_t* q;           // 64 values a head
-    const uint16_t* kv;          // 512 + 64 values a token
-    const int64_t* positions;
-    const float* cos_sin;        // [max_position][64]; nullptr: no rotation
-    const uint16_t* kv_norm;     // [512] or nullptr
-    const int64_t* slot_mapping;
-    uint16_t* q_out;
-    uint16_t* kv_out;            // [num_tokens][576] or nullptr
-    uint16_t* cache;             // [num_slots][576]
-    int64_t num_tokens, num_slots, max_position;
-    int64_t q_stride, q_head_stride, q_out_stride, q_out_head_stride, kv_stride;
-    int num_heads, head_tasks, interleaved;
-    float norm_eps;
-};
-cudaError_t launch_latent_append(const LatentAppendParams& p, int dtype, cudaStream_t stream, int* launches);
-
-// Attention of prompts over expanded keys and values (latent_prompt.cu).
-struct LatentPromptParams {
-    int* err;
-    const int32_t* query_starts; // [num_seqs + 1]
-    const int32_t* key_starts;   // [num_seqs + 1]
-    const void* values;          // expanded rows: 128 key values, 128 values a head
-    void* out;                   // [query tokens][num_heads][128]
-    int64_t kv_stride, kv_head_stride;  // elements
-    int num_seqs, num_heads;
-    int num_queries, num_keys;   // tokens of q; of kv and k_rope
-    int max_query_len;
-    int sms;
-    bool claims;                 // CTAs take the places of others that have not begun
-    float scale_log2;
-};
-cudaError_t launch_latent_prompt(const LatentPromptParams& p, int dtype, const CUtensorMap& tmq, const CUtensorMap& tmkv,
-                                 const CUtensorMap& tmr, cudaStream_t stream, int* launches);
-
 // Whole-block copies of 8-bit pools with their scales, up to
 // kCopyFp8MaxLayers layers per launch (append_copy.cu).
 constexpr int kCopyFp8MaxLayers = 48;
@@ -358,14 +318,6 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
-// 2-D tiled TMA load, as tma_load_3d without a cache hint.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
 // 3-D tiled TMA load (coordinates innermost first) into this CTA's shared
 // memory, completion counted on the mbarrier `bar` in bytes.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
@@ -374,15 +326,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
-        : "memory");
-}
-
-// ... without a cache hint.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -395,12 +338,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
         : "memory");
 }
-
-// 16 bytes from global to shared memory, behind the thread's back; cp_async_wait_all waits for all of the thread's.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"

@@ -54,6 +54,7 @@
 // products, the weights in one pass (softmax_tile.cuh), the first Q K of a unit
 // before the last P V of the one before (what has to be remembered of a tile from
 // one unit to the next costs more in every tile: 138 for 132 us).
+#include "copies.cuh"
 #include "drafted.cuh"
 #include "softmax_tile.cuh"
 
