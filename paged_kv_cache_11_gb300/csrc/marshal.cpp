@@ -19,7 +19,6 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <algorithm>
 #include <optional>
 #include <stdexcept>
 #include <vector>
@@ -517,8 +516,7 @@ PyObject* prefill(PyObject* const* a) {
     strides_of(kv, d.kv_stride, d.kv_head_stride);
     d.k_rope_stride = k_rope.size(0) > 1 ? k_rope.stride(0) : kRope;
     const int32_t seqs = narrow(qs.numel() - 1), nq = narrow(q.size(0)), nk = narrow(kv.size(0)),
-                  // a server's fixed bound may be more than a batch has tokens
-                  longest = a[6] == Py_None ? nq : narrow(std::min<int64_t>(asked, nq));
+                  longest = a[6] == Py_None ? nq : narrow(asked);
     const c10::cuda::CUDAGuard guard(dev.index);
     at::Tensor made;
     out = output(out, made, {q.size(0), q.size(1), D}, q);

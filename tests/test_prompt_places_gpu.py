@@ -94,14 +94,3 @@ def test_the_time_without_a_bound_of_the_longest(gpu):
     assert pkv.check_device_error() == 0
     p.check(only=[0, 511, 1023])
     assert times[None] <= 2 * times[64], times
-
-
-def test_a_bound_beyond_the_batch(gpu):
-    """A server's fixed bound, of the longest prompt that it takes."""
-    p = Prompts(4, [(20, 20), (300, 300)], 3, BF, extra=1)
-    for bound in (321, 4096, 1 << 40):
-        p.out.fill_(SENTINEL)
-        run(p, max_query_len=bound)
-        p.check()
-    with pytest.raises(pkv.PagedKVError):
-        p.call(max_query_len=-1)
