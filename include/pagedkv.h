@@ -388,7 +388,8 @@ pkv_status paged_attention_decode_fp8(const void* q, int32_t q_dtype, const void
  * The result does not depend on physical block ids, and is the same from run
  * to run.
  * Bad metadata never faults: query_starts out of order or range
- * (PKV_DEVERR_QUERY) leave the sequence's rows alone; more than 64 query
+ * (PKV_DEVERR_QUERY) leave the sequence's rows alone (sequences that lie over
+ * one another write the rows in no certain order); more than 64 query
  * tokens (PKV_DEVERR_QUERY), a context length out of range or below n
  * (PKV_DEVERR_CONTEXT_LEN) and a block id outside the pool
  * (PKV_DEVERR_BLOCK_ID; the query heads of the KV heads that read it) get

@@ -40,6 +40,7 @@ struct DraftParams {
     int max_blocks_per_seq;
     int len_limit;                // max_blocks_per_seq * block_size
     int pieces;                   // of the line: CTAs of the grid
+    bool merged;                  // a merge follows (draft_divides)
     float scale_log2;             // scale * log2(e)
 };
 
@@ -161,7 +162,9 @@ __device__ __forceinline__ void zero_rows(const DraftParams& p, int tok0, int n,
 // length over the CTAs, and kLeast tiles at least (or the longest unit, where
 // that is shorter): a smaller one costs more in starting and merging than it
 // spreads.  Where no unit is longer than that and each can have a CTA of its
-// own, it has, and nothing is divided.  On the way the sequences that attend
+// own, it has, and nothing is divided; nor where no merge follows, and only
+// sequences that lie over one another (bad metadata) can make more units than
+// CTAs: then a CTA has several, whole.  On the way the sequences that attend
 // nothing get their zeros, and bad metadata is recorded, each by one CTA.
 // scratch: (kThreads / 32) * 16 + 48 bytes of shared memory, 8-byte aligned.
 template <int kThreads>
@@ -222,11 +225,12 @@ __device__ __forceinline__ void draft_schedule(const DraftParams& p, int piece_i
         total += warp_tiles[w];
         total_units += warp_units[w];
     }
-    const bool whole = *longest <= kLeast && total_units <= p.pieces;  // a unit to a CTA
+    const bool whole = *longest <= kLeast && (total_units <= p.pieces || !p.merged);
     long long w0, w1;
     if (whole) {
         before = before_units + scan_units - units, tiles = units;
-        w0 = min(total_units, (long long)piece_id), w1 = min(total_units, w0 + 1);
+        const long long each = total_units <= p.pieces ? 1 : (total_units + p.pieces - 1) / p.pieces;
+        w0 = min(total_units, each * piece_id), w1 = min(total_units, w0 + each);
     } else {
         const long long piece = max((total + p.pieces - 1) / p.pieces, (long long)min(kLeast, *longest));
         before += scan - tiles;
@@ -237,14 +241,26 @@ __device__ __forceinline__ void draft_schedule(const DraftParams& p, int piece_i
         for (int k = 0; k < per; ++k) {
             const int s = first + k;
             if (s >= p.num_seqs) break;
-            const DraftSeq q = draft_seq(p, s);
+            DraftSeq q = draft_seq(p, s);
             const int n = U::units(p, q), len = n > 0 && !whole ? U::tiles(q) : 1;
             if (w0 < at + (long long)n * len) {
                 const long long in = w0 - at;
-                const int u = (int)(in / len);
+                int u = (int)(in / len);
                 found[0] = s, found[1] = q.tok0, found[2] = q.n, found[3] = q.L;
                 found[4] = u, found[5] = (int)(in - (long long)u * len);
-                *count = whole ? U::tiles(q) : w1 - w0;
+                *count = !whole ? w1 - w0 : U::tiles(q);
+                if (whole && w1 - w0 > 1) {  // the tiles of so many units
+                    long long more = w1 - w0, sum = 0;
+                    for (int k = s;;) {
+                        const long long take = min(more, (long long)(U::units(p, q) - u));
+                        sum += take * U::tiles(q);
+                        more -= take;
+                        if (more == 0) break;
+                        q = draft_seq(p, ++k);
+                        u = 0;
+                    }
+                    *count = sum;
+                }
                 break;
             }
             at += (long long)n * len;
@@ -256,7 +272,8 @@ __device__ __forceinline__ void draft_schedule(const DraftParams& p, int piece_i
     cur.start(p, found[0], q, found[4], found[5], w0 < w1 ? *count : 0);
 }
 
-// Can a unit of this call be divided?  Not where all are short and each surely has a CTA of its own (see draft_schedule).
+// Can a unit of this call be divided, so that a merge has to follow?  Not where all are short and each surely has a CTA of its
+// own (see draft_schedule).
 inline bool draft_divides(const DraftParams& p, int tile, int unit_rows, int least) {
     if (p.len_limit <= tile) return false;
     const int64_t units = p.num_kv_heads * (p.num_seqs + (int64_t)p.num_tokens * p.group / unit_rows);

@@ -534,8 +534,10 @@ cudaError_t launch_t(const DraftParams& p, const CUtensorMap& tmq, const CUtenso
 
 }  // namespace
 
-cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size, const CUtensorMap& tmq, const CUtensorMap& tmc,
+cudaError_t launch_latent_decode(const DraftParams& in, int dtype, int block_size, const CUtensorMap& tmq, const CUtensorMap& tmc,
                                  cudaStream_t stream, int* launches) {
+    DraftParams p = in;
+    p.merged = draft_divides(p, kTile, kLatentRows, kLeast);
     const bool bf16 = dtype == PKV_BF16;
     const cudaError_t e =
         block_size == 16
@@ -543,8 +545,7 @@ cudaError_t launch_latent_decode(const DraftParams& p, int dtype, int block_size
             : (bf16 ? launch_t<true, 32>(p, tmq, tmc, stream) : launch_t<false, 32>(p, tmq, tmc, stream));
     if (e != cudaSuccess) return e;
     ++*launches;
-    return draft_divides(p, kTile, kLatentRows, kLeast) ? launch_draft_merge(p, dtype, kValue, kLatentRows, stream, launches)
-                                                        : cudaSuccess;
+    return p.merged ? launch_draft_merge(p, dtype, kValue, kLatentRows, stream, launches) : cudaSuccess;
 }
 
 }  // namespace pkv

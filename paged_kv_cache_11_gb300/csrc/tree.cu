@@ -461,14 +461,16 @@ cudaError_t launch_t(const DraftParams& p, const CUtensorMap& tmk, const CUtenso
 
 }  // namespace
 
-cudaError_t launch_tree(const DraftParams& p, int dtype, int block_size, const CUtensorMap& tmk, const CUtensorMap& tmv,
+cudaError_t launch_tree(const DraftParams& in, int dtype, int block_size, const CUtensorMap& tmk, const CUtensorMap& tmv,
                         cudaStream_t stream, int* launches) {
+    DraftParams p = in;
+    p.merged = draft_divides(p, kTile, kTreeRows, kLeast);
     const bool bf16 = dtype == PKV_BF16;
     const cudaError_t e = block_size == 16 ? (bf16 ? launch_t<true, 16>(p, tmk, tmv, stream) : launch_t<false, 16>(p, tmk, tmv, stream))
                                            : (bf16 ? launch_t<true, 32>(p, tmk, tmv, stream) : launch_t<false, 32>(p, tmk, tmv, stream));
     if (e != cudaSuccess) return e;
     ++*launches;
-    return draft_divides(p, kTile, kTreeRows, kLeast) ? launch_draft_merge(p, dtype, kHeadDim, kTreeRows, stream, launches) : cudaSuccess;
+    return p.merged ? launch_draft_merge(p, dtype, kHeadDim, kTreeRows, stream, launches) : cudaSuccess;
 }
 
 }  // namespace pkv
