@@ -44,8 +44,8 @@ struct DraftParams {
     float scale_log2;             // scale * log2(e)
 };
 
-// State of a partial: it exists, it holds its unit's first tile, its last.
-enum { kPartValid = 1, kPartBegins = 2, kPartEnds = 4 };
+// State of a partial: it exists, it holds its unit's last tile.  (Its unit's first tile is in slot 1.)
+enum { kPartValid = 1, kPartEnds = 2 };
 
 // What sequence s asks for: n query tokens, rows tok0 .. of q, the last n of
 // its L positions.  n == 0: no rows.  idle: its rows are zeros (an empty
@@ -164,8 +164,11 @@ __device__ __forceinline__ void zero_rows(const DraftParams& p, int tok0, int n,
 // spreads.  Where no unit is longer than that and each can have a CTA of its
 // own, it has, and nothing is divided; nor where no merge follows, and only
 // sequences that lie over one another (bad metadata) can make more units than
-// CTAs: then a CTA has several, whole.  On the way the sequences that attend
-// nothing get their zeros, and bad metadata is recorded, each by one CTA.
+// CTAs: then a CTA has several, whole.  Each CTA reads all lengths, a run of
+// sequences to a thread: 2 us for 1000 sequences, 20 (tree.cu) to 30 (latent.cu)
+// for 10000 and 155 to 255 for 65535, at most a tenth of a call whose contexts
+// are the shortest.  On the way the sequences that attend nothing get their
+// zeros, and bad metadata is recorded, each by one CTA.
 // scratch: (kThreads / 32) * 16 + 48 bytes of shared memory, 8-byte aligned.
 template <int kThreads>
 __host__ __device__ constexpr int draft_scratch() {
