@@ -440,6 +440,9 @@ size_t paged_attention_tree_workspace_bytes(void);
  * and its rows of q_out and kv_out are zeros.  Two tokens with the same slot
  * race.  num_tokens == 0 is a no-op.  Supported: latent_dim 512, rope_dim 64,
  * bf16 or fp16, any block size.
+ * copy_blocks, swap_blocks and compact_tokens take such pools under a
+ * pkv_cache_desc of one KV head with head_dim latent_dim + rope_dim: the pools
+ * of two layers as K and V, or one for both.
  */
 pkv_status paged_latent_append_rope(const void* q, const void* kv, const int64_t* positions, const float* cos_sin,
                                     const void* kv_norm, const int64_t* slot_mapping, int64_t num_tokens, void* q_out,

@@ -460,8 +460,8 @@ def latent_attention_prefill(q: torch.Tensor, kv: torch.Tensor, k_rope: torch.Te
     rotated key values that the heads share; returns ``out`` [num_query_tokens, num_heads, 128].
 
     Sequence s's queries are the last of its keys' positions (more keys than queries: a prefix that is cached).  Tokens and
-    heads of q and kv, and rows of k_rope, may be any multiple of 8 elements apart.  ``max_query_len`` bounds the prompts'
-    lengths (default: all of q).
+    heads of q and kv, and rows of k_rope, may be any multiple of 8 elements apart.  ``max_query_len`` is an upper
+    bound of the prompts' lengths, at most q's tokens, which are the default: the time does not hang on it.
     """
     if stream is not None:
         with _on(stream, q):
