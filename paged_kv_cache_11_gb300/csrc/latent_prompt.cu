@@ -36,8 +36,8 @@
 // behind long ones: 7 ragged prompts 175 us for 169.)  Grids of one CTA an SM at
 // most claim nothing.
 //
-// What bounds it: two prompts of 8192 tokens with 128 heads (5.5 TFLOP) take 3.77
-// to 3.85 ms, 1.45 PFLOP/s, 75% of the card's peak and 82% of what it sustains
+// What bounds it: two prompts of 8192 tokens with 128 heads (5.5 TFLOP) take 3.79
+// to 3.89 ms, 1.44 PFLOP/s, 75% of the card's peak and 82% of what it sustains
 // under its power limit.  Without the softmax the products alone take 3.6 ms; the
 // rest is the part of a stream's softmax that the other's products do not cover,
 // and there every instruction of the product warp between a stream's P and its

@@ -44,12 +44,12 @@
 //
 // What bounds it.  Copies alone (the same kernel without products and softmax)
 // run at 7.0 TB/s.  8 documents of 131072 tokens, 64/8 heads, 31 drafted tokens
-// (4.3 GB): 880-925 us, 4.8 TB/s, 1.2 PFLOP/s, bound by the chain of a stream's
+// (4.3 GB): 880-930 us, 4.7 TB/s, 1.2 PFLOP/s, bound by the chain of a stream's
 // tile, Q K, softmax, P V, of some 4100 cycles in which two tiles of rows are
 // worked off (the copies' pace is 2800; without the softmax 775 us).  64
 // contexts of 512 to 4096, 32/8 heads, 16 tokens (606 MB): 128-134 us, 4.6
 // TB/s; 128 of up to 2048, 40 heads without sharing, 1 to 5 tokens (2.7 GB):
-// 620 us, 4.4 TB/s: there the ends of units, when the last tile's softmax,
+// 605-715 us from run to run, 3.8-4.5 TB/s: there the ends of units, when the last tile's softmax,
 // product and output follow one another and the ring runs full, are what is
 // left.  Tried and not kept: output by four warps of its own (they were as long
 // as the chain they took over), twice the softmax warps, a loop for the
