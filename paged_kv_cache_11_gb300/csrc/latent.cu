@@ -320,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = it.t0; t < it.t1; ++t, ++c) {
                 const int b = c & 1;
                 const bool guard = (t + 1) * kTile > base;
-                ok = ok && wait_bar(sfull0 + 8 * b, (c / 2) & 1) && wait_bar(full0 + 8 * b * kSlots, (c / 2) & 1);
+                // (the slot whose values this warp looks through below, and `bad` with it)
+                ok = ok && wait_bar(sfull0 + 8 * b, (c / 2) & 1) && wait_bar(full0 + 8 * (b * kSlots + warp), (c / 2) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 float s[32];
 #pragma unroll
@@ -352,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (guard && ok) {
                     // the products of this tile's keys have ended: half of a token's value for each thread
                     const int key = tid >> 1, pos = t * kTile + key;
+                    static_assert(kSlotKeys == 16 && kSlots == kSoftWarps, "a warp's keys are a slot's");
                     if (pos >= base) {
                         uint4* v = reinterpret_cast<uint4*>(smem + S::kKV + b * kSlots * kSlot + (key >> 3) * kGroup +
                                                             (key & 7) * 128 + (tid & 1) * 4096);
