@@ -158,10 +158,9 @@ __device__ __forceinline__ void zero_rows(const DraftParams& p, int tok0, int n,
 }
 
 // Deals the line and starts `cur` on piece piece_id of it; every thread of the
-// CTA calls it and gets the same piece.  A piece is the line's
-// length over the CTAs, and kLeast tiles at least (or the longest unit, where
-// that is shorter): a smaller one costs more in starting and merging than it
-// spreads.  Where no unit is longer than that and each can have a CTA of its
+// CTA calls it and gets the same piece.  A piece is the line's length over the
+// CTAs, and kLeast tiles at least (or the longest unit, where that is shorter): a
+// smaller one costs more in starting and merging than it spreads.  Where no unit is longer than that and each can have a CTA of its
 // own, it has, and nothing is divided; nor where no merge follows, and only
 // sequences that lie over one another (bad metadata) can make more units than
 // CTAs: then a CTA has several, whole.  Each CTA reads all lengths, a run of

@@ -31,9 +31,8 @@
 // the products, 6 the copies of queries.  The maximum is raised lazily, as in
 // tree.cu; a weight is rounded to the cache's 16-bit type for its product (fp16's
 // at seven binades more, softmax_tile.cuh), the row's sum is that of the weights
-// before.  Masked places are replaced, not
-// added to, and values that are not finite are kept out of the products of
-// tiles with masks, as there.
+// before.  Masked places are replaced, not added to, and values that are not
+// finite are kept out of the products of tiles with masks, as there.
 //
 // What bounds it.  A tile costs the tensor core 36 x 32 + 16 x 48 cycles (the
 // latter by shared memory reads, 128 bytes a cycle), 1920 in all; its copy 3200

@@ -49,13 +49,13 @@
 // worked off (the copies' pace is 2800; without the softmax 775 us).  64
 // contexts of 512 to 4096, 32/8 heads, 16 tokens (606 MB): 128-134 us, 4.6
 // TB/s; 128 of up to 2048, 40 heads without sharing, 1 to 5 tokens (2.7 GB):
-// 605-715 us from run to run, 3.8-4.5 TB/s: there the ends of units, when the last tile's softmax,
-// product and output follow one another and the ring runs full, are what is
-// left.  Tried and not kept: output by four warps of its own (they were as long
-// as the chain they took over), twice the softmax warps, a loop for the
-// products, the weights in one pass (softmax_tile.cuh), the first Q K of a unit
-// before the last P V of the one before (what has to be remembered of a tile from
-// one unit to the next costs more in every tile: 138 for 132 us).
+// 605-715 us from run to run, 3.8-4.5 TB/s: there the ends of units, when the
+// last tile's softmax, product and output follow one another and the ring runs
+// full, are what is left.  Tried and not kept: output by four warps of its own
+// (they were as long as the chain they took over), twice the softmax warps, a
+// loop for the products, the weights in one pass (softmax_tile.cuh), the first Q K
+// of a unit before the last P V of the one before (what has to be remembered of a
+// tile from one unit to the next costs more in every tile: 138 for 132 us).
 #include "copies.cuh"
 #include "drafted.cuh"
 #include "softmax_tile.cuh"
