@@ -25,7 +25,9 @@
 // and strip of the longest would be 1e9 places for the 2e5 strips of 16384 prompts
 // whose longest is not known.  1024 prompts of 64 tokens with 8 heads take 225 us
 // with and without a bound, so 220 with one and 6200 without; one prompt of 4000
-// tokens among 200 of 40 takes 198, so 258; one of 100 alone 7.0, so 6.85.)
+// tokens among 200 of 40 takes 198, so 258; one of 100 alone 7.0, so 6.85.)  A
+// place behind the line's end costs a claim, 1 us: 20000 sequences of which 50 have
+// new tokens, 7 each, with 64 heads 250 us for the 50 sequences' 100.
 //
 // A CTA that has issued the copies of its queries' last tile takes the place of
 // one that has not begun (a cluster launch control request) and goes on with that
@@ -598,9 +600,10 @@ cudaError_t launch_latent_prompt(const LatentPromptParams& in, int dtype, const 
     auto kern = dtype == PKV_BF16 ? latent_prompt_kernel<true> : latent_prompt_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem::kTotal);
     if (e != cudaSuccess) return e;
-    // No more strips than these, whatever the prompts' lengths: n tokens make at most (n + kRows - 1) / kRows.
-    const int64_t strips = std::min(in.num_seqs * (((int64_t)in.max_query_len + kRows - 1) / kRows),
-                                    (in.num_queries + (int64_t)in.num_seqs * (kRows - 1)) / kRows);
+    // No more strips than these, whatever the prompts' lengths: n tokens make at most (n + kRows - 1) / kRows, and a strip has a
+    // token.
+    const int64_t strips = std::min({in.num_seqs * (((int64_t)in.max_query_len + kRows - 1) / kRows),
+                                     (in.num_queries + (int64_t)in.num_seqs * (kRows - 1)) / kRows, (int64_t)in.num_queries});
     const dim3 grid((unsigned)strips, in.num_heads);
     LatentPromptParams p = in;
     p.claims = strips * grid.y > p.sms;  // (more than one CTA an SM)

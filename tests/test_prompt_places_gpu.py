@@ -94,3 +94,26 @@ def test_the_time_without_a_bound_of_the_longest(gpu):
     assert pkv.check_device_error() == 0
     p.check(only=[0, 511, 1023])
     assert times[None] <= 2 * times[64], times
+
+
+def test_the_time_of_a_batch_most_of_which_is_empty(gpu):
+    """20000 sequences, 50 of which have new tokens, against those 50 alone.  The lengths of all are read (20 us at most), and the
+    strips that the tokens could make, one each, are looked through: 64 heads of them, less the 50, over the SMs, each a claim
+    of 2 us at most.  (A place for each sequence would be 20000 for a head.)"""
+    some = [(3 + i % 9, 40) for i in range(50)]
+    times = []
+    for seqs in (some, [some[i // 400] if i % 400 == 7 else (0, 0) for i in range(20000)]):
+        p = Prompts(5, seqs, 64, BF)
+        t = []
+        for _ in range(6):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            pkv.latent_attention_prefill(p.q, p.kv, p.k_rope, p.qs, p.ks, p.scale, out=p.out)
+            b.record()
+            b.synchronize()
+            t.append(a.elapsed_time(b))
+        times.append(min(t[1:]))
+        assert pkv.check_device_error() == 0
+        p.check(only=range(7, len(seqs), 400) if len(seqs) > 50 else None)
+    claims = (p.q.shape[0] - 50) * 64 / torch.cuda.get_device_properties(gpu).multi_processor_count
+    assert times[1] <= times[0] + 0.02 + 0.002 * claims, (times, claims)
