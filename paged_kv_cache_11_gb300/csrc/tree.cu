@@ -44,7 +44,7 @@
 //
 // What bounds it.  Copies alone (the same kernel without products and softmax)
 // run at 7.0 TB/s.  8 documents of 131072 tokens, 64/8 heads, 31 drafted tokens
-// (4.3 GB): 880-930 us, 4.7 TB/s, 1.2 PFLOP/s, bound by the chain of a stream's
+// (4.3 GB): 870-930 us, 4.7 TB/s, 1.2 PFLOP/s, bound by the chain of a stream's
 // tile, Q K, softmax, P V, of some 4100 cycles in which two tiles of rows are
 // worked off (the copies' pace is 2800; without the softmax 775 us).  64
 // contexts of 512 to 4096, 32/8 heads, 16 tokens (606 MB): 128-134 us, 4.6
